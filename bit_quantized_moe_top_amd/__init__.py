@@ -685,4 +685,8 @@ def moe_shared_gemm_bf16(a: torch.Tensor, w: torch.Tensor, epilogue: int = EPI_N
     return out
 
 
-from .layer import HybridMoELayer, MoELayer  # noqa: E402,F401  (composition of the calls above)
+from .mx import *  # noqa: E402,F401,F403  (the MXFP4 calls)
+from .mx import __all__ as _mx_all  # noqa: E402
+from .layer import HybridMoELayer, MoELayer, MxMoELayer  # noqa: E402,F401  (composition of the calls above)
+
+__all__ += _mx_all

@@ -3,41 +3,13 @@
 //
 // Validation happens before any HIP call, so argument errors are reported on a
 // machine without a GPU.  No entry point allocates, frees or synchronizes.
-#include <string.h>
+#include "api.hpp"
 
-#include "kernels.hpp"
-
-namespace {
-
-constexpr int kMaxDevices = 64;
-// per-device result of the architecture check: 0 unknown, 1 gfx950, -1 other
-int g_device_ok[kMaxDevices];
-
-int check_device() {
-  int dev = -1;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0) return MOEQ_ERR_DEVICE;
-  if (dev < kMaxDevices && g_device_ok[dev] != 0) return g_device_ok[dev] > 0 ? MOEQ_OK : MOEQ_ERR_DEVICE;
-  hipDeviceProp_t prop;
-  if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return MOEQ_ERR_DEVICE;
-  const bool ok = strncmp(prop.gcnArchName, "gfx950", 6) == 0;
-  if (dev < kMaxDevices) g_device_ok[dev] = ok ? 1 : -1;
-  return ok ? MOEQ_OK : MOEQ_ERR_DEVICE;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int launch_status(hipError_t err) { return err == hipSuccess ? MOEQ_OK : MOEQ_ERR_LAUNCH; }
-
-hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
-
-// a plan read by a kernel: 4-byte aligned and at least moe_plan_size(E, R) bytes
-int check_plan(const void* plan, size_t plan_bytes, int E, int R) {
-  if (reinterpret_cast<uintptr_t>(plan) & 3u) return MOEQ_ERR_INVALID_ARG;
-  if (plan_bytes < moeq::plan_words(E, R) * sizeof(int32_t)) return MOEQ_ERR_WORKSPACE;
-  return MOEQ_OK;
-}
-
-}  // namespace
+using moeq::aligned16;
+using moeq::as_stream;
+using moeq::check_device;
+using moeq::check_plan;
+using moeq::launch_status;
 
 extern "C" {
 
@@ -48,7 +20,7 @@ const char* moe_status_string(int status) {
     case MOEQ_OK: return "ok";
     case MOEQ_ERR_INVALID_ARG: return "invalid argument";
     case MOEQ_ERR_UNSUPPORTED: return "unsupported size";
-    case MOEQ_ERR_WORKSPACE: return "plan buffer too small";
+    case MOEQ_ERR_WORKSPACE: return "plan or workspace buffer too small";
     case MOEQ_ERR_DEVICE: return "no gfx950 device";
     case MOEQ_ERR_LAUNCH: return "kernel launch failed";
     case MOEQ_ERR_SCRATCH: return "sizes exceed the library's scratch array";

@@ -17,9 +17,10 @@ import torch
 
 from . import (EPI_NONE, EPI_SILU_MUL, moe_combine, moe_expert_mlp_fp8row, moe_expert_mlp_w4a8,
                moe_grouped_gemm_aqlm, moe_grouped_gemm_fp8row, moe_grouped_gemm_nvfp4,
-               moe_grouped_gemm_w4a8, moe_plan_size,
-               moe_requant_fp8_fnuz, moe_route_quant_permute, moe_router_logits, moe_shared_gemm_bf16, pack_int4_g128,
-               quant_fp8_per_token)
+               moe_grouped_gemm_mxfp4, moe_grouped_gemm_w4a8, moe_layer_mxfp4_few, moe_permute,
+               moe_plan_size,
+               moe_requant_fp8_fnuz, moe_route_quant_permute, moe_route_topk, moe_router_logits, moe_shared_gemm_bf16, pack_int4_g128,
+               quant_fp8_per_token, quant_mxfp4, tile_mxfp4_weights)
 
 
 class MoELayer:
@@ -230,5 +231,116 @@ class HybridMoELayer(MoELayer):
         step("gemm_down", self._gemm_both, b["h_q"], b["h_s"], b["plan"], "w2", EPI_NONE, b["o"])
         step("combine", moe_combine, b["o"], b["plan"], b["w"], None, y=b["y"], E=self.E)
         return b if return_all else b["y"]
+
+    __call__ = forward
+
+
+class MxMoELayer(MoELayer):
+    """Routed experts with MXFP4 weights (E2M1 codes, an E8M0 scale per 32 K).
+
+    forward(): any number of tokens, activations in MXFP4 too (route, quantize x, plan, gate/up
+    product with SiLU, quantize h, down product, combine); the gate/up product reads each token's
+    one quantized row, so no gathered copy is made.
+    forward_few(): up to 16 tokens in two kernels, activations in bf16.  Its results are closer to
+    the unquantized layer's than forward()'s, which rounds x and h to 4 bits.
+    """
+
+    def __init__(self, H: int, I: int, E: int, k: int, renormalize: bool = True, device="cuda"):
+        super().__init__(H, I, E, k, "w4a8", renormalize, device)
+        self.weight_format = "mxfp4"
+        self._few = {}
+
+    # set_weights takes tiled weights and scales (tile_mxfp4_weights)
+
+    def set_weights_fnuz(self, *args):
+        raise ValueError("E4M3FNUZ weights are row-scaled FP8 experts (weight_format='fp8row')")
+
+    def quantize_weights(self, w13: torch.Tensor, w2: torch.Tensor):
+        """fp32 or bf16 weights [E, 2I, H] and [E, H, I], quantized and tiled on the device."""
+        self.w13, self.s13 = tile_mxfp4_weights(*quant_mxfp4(w13))
+        self.w2, self.s2 = tile_mxfp4_weights(*quant_mxfp4(w2))
+
+    def buffers(self, T: int) -> dict:
+        b = self._bufs.get(T)
+        if b is None:
+            H, I, E, k, d = self.H, self.I, self.E, self.k, self.device
+            R = T * k
+
+            def u8(*shape):
+                return torch.empty(*shape, dtype=torch.uint8, device=d)
+
+            def bf16(*shape):
+                return torch.empty(*shape, dtype=torch.bfloat16, device=d)
+
+            b = {
+                "logits": torch.empty(T, E, dtype=torch.float32, device=d),
+                "ids": torch.empty(T, k, dtype=torch.int32, device=d),
+                "w": torch.empty(T, k, dtype=torch.float32, device=d),
+                "plan": torch.empty((moe_plan_size(E, R) + 3) // 4, dtype=torch.int32, device=d),
+                "x_q": u8(T, H // 2), "x_s": u8(T, H // 32), "h": bf16(R, I),
+                "h_q": u8(R, I // 2), "h_s": u8(R, I // 32), "o": bf16(R, H), "y": bf16(T, H),
+            }
+            if self.ws13 is not None:
+                b["sh_h"], b["shared"] = bf16(T, self.ws2.shape[1]), bf16(T, H)
+            self._bufs[T] = b
+        return b
+
+    def _front(self, x, logits, b, step):
+        """(logits, the shared experts' output or None)"""
+        if logits is None:
+            if self.w_router is None:
+                raise ValueError("logits=None needs router weights (set_router)")
+            logits = step("router", moe_router_logits, x, self.w_router, out=b["logits"])
+        if self.ws13 is None:
+            return logits, None
+        if x.dtype != torch.bfloat16:
+            raise TypeError("shared experts take bfloat16 x")
+        step("shared_gate_up", moe_shared_gemm_bf16, x, self.ws13, EPI_SILU_MUL, out=b["sh_h"])
+        return logits, step("shared_down", moe_shared_gemm_bf16, b["sh_h"], self.ws2, EPI_NONE,
+                            out=b["shared"])
+
+    @staticmethod
+    def _steps(events):
+        def step(name, fn, *args, **kw):
+            if events is None:
+                return fn(*args, **kw)
+            s, e = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            s.record()
+            r = fn(*args, **kw)
+            e.record()
+            events.append((name, s, e))
+            return r
+        return step
+
+    def forward(self, x: torch.Tensor, logits: Optional[torch.Tensor] = None,
+                bias: Optional[torch.Tensor] = None, return_all: bool = False,
+                events: Optional[list] = None):
+        b, step = self.buffers(x.shape[0]), self._steps(events)
+        logits, shared = self._front(x, logits, b, step)
+        step("route", moe_route_topk, logits, self.k, bias, self.renormalize, ids=b["ids"],
+             weights=b["w"])
+        step("quant_x", quant_mxfp4, x, q=b["x_q"], scale=b["x_s"])
+        step("plan", moe_permute, b["ids"], self.E, plan=b["plan"])
+        step("gemm_gate_up", moe_grouped_gemm_mxfp4, b["x_q"], b["x_s"], b["plan"], self.w13,
+             self.s13, epilogue=EPI_SILU_MUL, topk=self.k, out=b["h"])
+        step("quant_h", quant_mxfp4, b["h"], q=b["h_q"], scale=b["h_s"])
+        step("gemm_down", moe_grouped_gemm_mxfp4, b["h_q"], b["h_s"], b["plan"], self.w2, self.s2,
+             out=b["o"])
+        step("combine", moe_combine, b["o"], b["plan"], b["w"], shared, y=b["y"], E=self.E)
+        return b if return_all else b["y"]
+
+    def forward_few(self, x: torch.Tensor, logits: Optional[torch.Tensor] = None,
+                    bias: Optional[torch.Tensor] = None, return_all: bool = False,
+                    events: Optional[list] = None):
+        """forward() for at most 16 tokens of bf16 x in two kernels, activations in bf16."""
+        T = x.shape[0]
+        step = self._steps(events)
+        needs = logits is None or self.ws13 is not None
+        logits, shared = self._front(x, logits, self.buffers(T) if needs else None, step)
+        # (buffers of its own: the workspace belongs to this layer's calls)
+        self._few[T] = o = step("few", moe_layer_mxfp4_few, logits, x, self.w13, self.s13, self.w2,
+                                self.s2, self.k, bias=bias, renormalize=self.renormalize,
+                                shared=shared, out=self._few.get(T))
+        return o if return_all else o["y"]
 
     __call__ = forward

@@ -34,7 +34,11 @@ namespace {
 constexpr int kFewThreads = 256;
 constexpr int kFewMaxRows = 2 * kWave;        // routed rows: 16 tokens x 8 experts
 static_assert(kFewTokens * MOEQ_MAX_TOPK <= kFewMaxRows, "two ballots cover the routed rows");
-constexpr int kStageRows = 4;                 // rows of activations staged in LDS
+// Activation rows staged in LDS: at most four, in at most 17 KB (two rows of 4096
+// elements): with more, fewer workgroups fit a CU (T = 4 at 4096 x 2048, gate/up:
+// 53.4 us with 33 KB against 49.4 us with 17 KB, before the other steps below)
+// for rows that are rarely there; an expert with more rows reads them from memory.
+constexpr int kStageRows = 4, kStageBytes = 17 << 10;
 
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 
@@ -63,117 +67,128 @@ __device__ __forceinline__ FewRows find_rows(int e_lo, int e_hi, int R, int r, i
   return f;
 }
 
-// The activations of an expert's rows as the second operand: from LDS (rows
-// staged by the workgroup) or from memory (more than the staged rows).
-struct FewAct {
-  const uint8_t* lds;       // this lane's row in LDS (bytes), rows G * 1024 + 16 apart
-  const uint16_t* mem;      // this lane's row in memory
-  bool staged, live;
-  int K;
-  // 8 elements m of block b (32 b + 8 m)
-  __device__ __forceinline__ uint4 get(int b, int m) const {
+// The activation rows of an expert, [n] rows of K bf16 elements of src (row i at
+// index rows[i]), padded in LDS to whole super-groups and 16 bytes (row_bytes).
+struct FewStage {
+  const uint16_t* src;
+  const int* rows;
+  uint8_t* lds;
+  int n, K, per_row, row_bytes;
+  __device__ __forceinline__ FewStage(const uint16_t* src, const int* rows, uint8_t* lds, int K)
+      : src(src), rows(rows), lds(lds), n(0), K(K), per_row(mx_supers(K) * (kMxSuper / 8)),
+        row_bytes(per_row * 16 + 16) {}
+  // piece p (8 elements) of source row `row`; pieces past K are 0
+  __device__ __forceinline__ uint4 piece(int row, int p) const {
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (!live) return v;
-    if (staged) v = *reinterpret_cast<const uint4*>(lds + b * 64 + m * 16);
-    else if (b * kMxBlock < K) v = *reinterpret_cast<const uint4*>(mem + b * kMxBlock + m * 8);
+    if (p * 8 < K) v = *reinterpret_cast<const uint4*>(src + int64_t(row) * K + p * 8);
     return v;
+  }
+  __device__ __forceinline__ void put(int i, int p, const uint4& v) const {
+    *reinterpret_cast<uint4*>(lds + i * row_bytes + p * 16) = v;
   }
 };
 
-// acc += W A over one super-group
-__device__ __forceinline__ void few_mac(const MxFrag& f0, const MxFrag& f1, const FewAct& act,
-                                        int sg, int kb, mx_v4f (&acc)[2]) {
+// A row whose index is known ahead of the expert's others (the workgroup's own
+// row, which is activation row 0 when the workgroup owns its expert): its first
+// pieces are loaded at the top of the kernel and parked in LDS later.
+constexpr int kEarly = 2;                     // pieces per thread: rows of <= 4096 elements
+struct EarlyRow {
+  uint4 v[kEarly];
+  __device__ __forceinline__ void load(const FewStage& st, int row, int tid) {
+#pragma unroll
+    for (int i = 0; i < kEarly; ++i)
+      if (tid + i * kFewThreads < st.per_row) v[i] = st.piece(row, tid + i * kFewThreads);
+  }
+  __device__ __forceinline__ void store(const FewStage& st, int row, int tid) const {
+#pragma unroll
+    for (int i = 0; i < kEarly; ++i)
+      if (tid + i * kFewThreads < st.per_row) st.put(0, tid + i * kFewThreads, v[i]);
+    for (int p = tid + kEarly * kFewThreads; p < st.per_row; p += kFewThreads)
+      st.put(0, p, st.piece(row, p));
+  }
+};
+
+// the two 16-row weight blocks of column unit u of one expert, and the K quarter
+// of this wave
+template <typename BlkF>
+struct FewWeights {
+  const uint8_t *w, *ws;
+  BlkF blk;
+  int G, g0, gn;
+  __device__ __forceinline__ FewWeights(const uint8_t* w, const uint8_t* ws, int64_t e, int64_t blocks,
+                                        int K, int q, BlkF blk)
+      : blk(blk), G(mx_supers(K)), g0(quarter_g0(G, q)), gn(quarter_groups(G, q)) {
+    this->w = w + e * blocks * G * kMxCodeBytes;
+    this->ws = ws + e * blocks * G * kMxScaleBytes;
+  }
+  __device__ __forceinline__ void load(int u, int i, int lane, MxFrag (&f)[2]) const {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int64_t at = int64_t(blk(u, b)) * G;
+      f[b] = load_weights<kCpStream>(w + at * kMxCodeBytes, ws + at * kMxScaleBytes, g0 + i, lane);
+    }
+  }
+};
+
+// acc += W A over one super-group: a lane's four steps take the activation
+// blocks 4 kb .. 4 kb + 3 of the super-group, 256 consecutive bytes at `act`.
+// kPartial: the row ends inside the super-group, `left` bytes on.
+template <bool kPartial>
+__device__ __forceinline__ void few_mac(const MxFrag (&f)[2], const uint8_t* act, int left,
+                                        mx_v4f (&acc)[2]) {
   static_for<kMxSteps>([&](auto j) {
-    const float sc0 = u2f((f0.s << (23 - 8 * j > 0 ? 23 - 8 * j : 0) >> (8 * j > 23 ? 8 * j - 23 : 0)) & 0x7F800000u);
-    const float sc1 = u2f((f1.s << (23 - 8 * j > 0 ? 23 - 8 * j : 0) >> (8 * j > 23 ? 8 * j - 23 : 0)) & 0x7F800000u);
-    const uint32_t c0[4] = {f0.c[j].x, f0.c[j].y, f0.c[j].z, f0.c[j].w};
-    const uint32_t c1[4] = {f1.c[j].x, f1.c[j].y, f1.c[j].z, f1.c[j].w};
+    float sc[2];                              // byte j of the scale dword in the exponent field
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+      sc[b] = u2f((j < 3 ? f[b].s << (j < 3 ? 23 - 8 * j : 0) : f[b].s >> 1) & 0x7F800000u);
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-      const uint4 a = act.get(16 * sg + 4 * kb + j, m);
-      acc[0] = mfma_bf16(mx_bf16x8(c0[m], sc0), a, acc[0]);
-      acc[1] = mfma_bf16(mx_bf16x8(c1[m], sc1), a, acc[1]);
+      uint4 a = make_uint4(0u, 0u, 0u, 0u);
+      if (!kPartial || j * 64 < left) a = *reinterpret_cast<const uint4*>(act + j * 64 + m * 16);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const uint32_t c = m == 0 ? f[b].c[j].x : m == 1 ? f[b].c[j].y : m == 2 ? f[b].c[j].z : f[b].c[j].w;
+        acc[b] = mfma_bf16(mx_bf16x8(c, sc[b]), a, acc[b]);
+      }
     }
   });
 }
 
-// 16-byte pieces of the expert's activation rows into LDS: piece c of the
-// flattened (row, piece of a row padded to G super-groups); pieces past K are 0
-struct FewStage {
-  const uint16_t* src;      // [.., K] rows
-  const int* rows;          // row of src of each activation row
-  int n, K, per_row, row_bytes;
-  __device__ __forceinline__ bool load(int c, uint4& v) const {
-    const int row = c / per_row, p = c - row * per_row;
-    v = make_uint4(0u, 0u, 0u, 0u);
-    if (row >= n) return false;
-    if (p * 8 < K) v = *reinterpret_cast<const uint4*>(src + int64_t(rows[row]) * K + p * 8);
-    return true;
-  }
-  __device__ __forceinline__ void store(uint8_t* lds, int c, const uint4& v) const {
-    const int row = c / per_row, p = c - row * per_row;
-    *reinterpret_cast<uint4*>(lds + row * row_bytes + p * 16) = v;
-  }
-};
-
-// The column units u0 .. u1 - 1 of one expert: unit u multiplies the 16-row
-// weight blocks blk0(u), blk1(u) by the rows' activations; wave q sweeps K quarter
-// q, the quarters meet in LDS in the fixed order s0 + (s1 + (s2 + s3)), and wave 0
-// calls done(u, sums) (every wave calls done; only wave 0's sums are whole).
-// The next item's weights are loaded before this one's are used.
-template <typename BlkF, typename DoneF>
-__device__ __forceinline__ void few_units(const uint8_t* w, const uint8_t* ws, int K, int u0,
-                                          int u1, const FewStage& st, uint8_t* lds, bool staged,
-                                          mx_v4f* red, BlkF&& blk, DoneF&& done) {
+// The column units u0 .. u1 - 1 of one expert.  A unit is a product of two 16-row
+// weight blocks with the rows' activations; wave q sweeps K quarter q, the
+// quarters meet in LDS in the fixed order s0 + (s1 + (s2 + s3)), and wave 0 calls
+// done(u, sums).  The sweep runs over items (unit, super-group of the quarter)
+// with two register sets, so the next item's weights are in flight while one is
+// multiplied; the first item's are already in `f0`.
+//
+// kStaged: the rows are in LDS; lanes past the last row read the last one (their
+// columns of the result are never used).  Otherwise they are read from memory.
+template <bool kStaged, typename WeightsT, typename DoneF>
+__device__ __forceinline__ void few_units(const WeightsT& wt, int u0, int u1, const FewStage& st,
+                                          MxFrag (&f0)[2], mx_v4f* red, DoneF&& done) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int q = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int ln = lane & 15, kb = lane >> 4;
-  const int G = mx_supers(K);
-  const int g0 = quarter_g0(G, q), gn = quarter_groups(G, q);
+  const int row = min(lane & 15, st.n - 1), kb = lane >> 4;
+  const uint8_t* act = (kStaged ? st.lds + row * st.row_bytes
+                                : reinterpret_cast<const uint8_t*>(st.src + int64_t(st.rows[row]) * st.K)) +
+                       kb * 256;
+  const int per_unit = max(wt.gn, 1);                   // a wave without K still joins the sums
+  const int items = (u1 - u0) * per_unit;
+  mx_v4f acc[2] = {mx_v4f{0.f, 0.f, 0.f, 0.f}, mx_v4f{0.f, 0.f, 0.f, 0.f}};
+  int u = u0, i = 0;                                    // the current item
+  int lu = u0, li = 0;                                  // the last item loaded
 
-  auto load = [&](int u, int sg, MxFrag& f0, MxFrag& f1) {
-    const int64_t b0 = blk(u, 0), b1 = blk(u, 1);
-    f0 = load_weights<kCpStream>(w + b0 * G * kMxCodeBytes, ws + b0 * G * kMxScaleBytes, sg, lane);
-    f1 = load_weights<kCpStream>(w + b1 * G * kMxCodeBytes, ws + b1 * G * kMxScaleBytes, sg, lane);
+  auto load_next = [&](MxFrag (&f)[2]) {
+    if (++li == per_unit) { li = 0; ++lu; }
+    if (lu < u1 && wt.gn > 0) wt.load(lu, li, lane, f);
   };
-
-  // the first pieces of the activations go out ahead of the weights, and are
-  // written to LDS while those are in flight
-  constexpr int kAhead = 4;
-  uint4 piece[kAhead];
-  bool have[kAhead];
-  if (staged) {
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) have[i] = st.load(tid + i * kFewThreads, piece[i]);
-  }
-  MxFrag f0, f1;
-  if (gn > 0) load(u0, g0, f0, f1);
-  if (staged) {
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (have[i]) st.store(lds, tid + i * kFewThreads, piece[i]);
-    uint4 v;
-    for (int c = tid + kAhead * kFewThreads; c < st.n * st.per_row; c += kFewThreads)
-      if (st.load(c, v)) st.store(lds, c, v);
-  }
-  lds_barrier();
-  FewAct act;
-  act.live = ln < st.n;
-  act.staged = staged;
-  act.K = K;
-  act.lds = lds + (act.live ? ln : 0) * st.row_bytes;
-  act.mem = st.src + int64_t(st.rows[act.live ? ln : 0]) * K;
-
-  for (int u = u0; u < u1; ++u) {
-    mx_v4f acc[2] = {mx_v4f{0.f, 0.f, 0.f, 0.f}, mx_v4f{0.f, 0.f, 0.f, 0.f}};
-    for (int i = 0; i < gn; ++i) {
-      MxFrag n0 = f0, n1 = f1;
-      const bool more = i + 1 < gn;
-      if (more || u + 1 < u1) load(more ? u : u + 1, more ? g0 + i + 1 : g0, n0, n1);
-      few_mac(f0, f1, act, g0 + i, kb, acc);
-      f0 = n0;
-      f1 = n1;
+  auto step = [&](MxFrag (&f)[2]) {
+    if (wt.gn > 0) {
+      const int at = (wt.g0 + i) * 1024;
+      if (kStaged) few_mac<false>(f, act + at, 0, acc);
+      else few_mac<true>(f, act + at, st.K * 2 - at - kb * 256, acc);
     }
+    if (++i < per_unit) return;
     // one half of red per unit parity: a unit's sums are read before the barrier
     // of the next, and overwritten after it
     mx_v4f* half = red + (u & 1) * (3 * 2 * kWave);
@@ -189,69 +204,176 @@ __device__ __forceinline__ void few_units(const uint8_t* w, const uint8_t* ws, i
                            (half[(2 + j) * kWave + lane] + half[(4 + j) * kWave + lane]));
       done(u, acc);
     }
+    acc[0] = acc[1] = mx_v4f{0.f, 0.f, 0.f, 0.f};
+    i = 0;
+    ++u;
+  };
+  if constexpr (kStaged) {
+    MxFrag f1[2];
+    load_next(f1);
+    for (int it = 0; it < items; it += 2) {
+      step(f0);
+      if (it + 1 == items) break;
+      load_next(f0);
+      step(f1);
+      load_next(f1);
+    }
+  } else {
+    // one register set, loaded anew: activations straight from memory take the room
+    // of the second, and the first item's early copy need not stay live for this path
+    MxFrag f[2];
+    li = -1;
+    for (int it = 0; it < items; ++it) {
+      load_next(f);
+      step(f);
+    }
+  }
+}
+
+// Stages the rows after row 0 (which is in LDS) if all fit, and runs the units.
+template <typename WeightsT, typename DoneF>
+__device__ __forceinline__ void few_run(const WeightsT& wt, int u0, int u1, const FewStage& st,
+                                        int stage_rows, MxFrag (&f0)[2], mx_v4f* red, DoneF&& done) {
+  if (st.n <= stage_rows) {
+    if (st.n > 1) {
+      for (int i = 1; i < st.n; ++i)
+        for (int p = threadIdx.x; p < st.per_row; p += kFewThreads) st.put(i, p, st.piece(st.rows[i], p));
+      lds_barrier();
+    }
+    few_units<true>(wt, u0, u1, st, f0, red, done);
+  } else {
+    few_units<false>(wt, u0, u1, st, f0, red, done);
   }
 }
 
 // -------------------------------------------------------------- kernel 1
+// One token's biased scores as order-preserving keys (front.hpp), expert e in lane
+// e % 64, slot e / 64; 0 past E.
 template <int NS>
-__global__ void __launch_bounds__(kFewThreads)
+struct Scores {
+  uint32_t key[NS];
+  __device__ __forceinline__ void load(const float* row, const float* bias, int E, int lane) {
+    float s[NS];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) s[i] = row[min(i * kWave + lane, E - 1)];
+    if (bias) {
+#pragma unroll
+      for (int i = 0; i < NS; ++i) s[i] = s[i] + bias[min(i * kWave + lane, E - 1)];
+    }
+#pragma unroll
+    for (int i = 0; i < NS; ++i) key[i] = i * kWave + lane < E ? score_key(s[i]) : 0u;
+  }
+  // the expert of rank j (0 the best): j + 1 rounds of a wave-wide argmax, as in
+  // route_token_values
+  __device__ __forceinline__ int at_rank(int j, int lane) const {
+    uint32_t rest[NS];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) rest[i] = key[i];
+    int e = 0;
+    for (int round = 0; round <= j; ++round) {
+      uint32_t ck = 0, bk;
+      int ci = 0x7FFFFFFF;
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+        if (rest[i] > ck) { ck = rest[i]; ci = i * kWave + lane; }
+      e = wave_best(ck, ci, &bk);
+#pragma unroll
+      for (int i = 0; i < NS; ++i)
+        if (i * kWave + lane == e) rest[i] = 0u;
+    }
+    return __builtin_amdgcn_readfirstlane(e);
+  }
+  // the rank of expert e: the number of experts ahead of it in the same order
+  __device__ __forceinline__ int rank_of(int e, int lane) const {
+    uint32_t ke = 0;
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+      if (i == (e >> 6)) ke = uint32_t(readlane(int(key[i]), e & 63));
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+      n += __popcll(__ballot(key[i] > ke || (key[i] == ke && i * kWave + lane < e)));
+    return n;
+  }
+};
+
+template <int NS>
+__global__ void __launch_bounds__(kFewThreads, NS > 8 ? 2 : 4)    // waves per SIMD
 few_gate_up_kernel(const float* logits, const float* bias, int T, int E, int k, int renormalize,
                    const uint16_t* x, int H, const uint8_t* w13, const uint8_t* ws13, int I,
                    int units_per_wg, int stage_rows, int32_t* ids, float* topk_w, uint16_t* h,
                    uint32_t* counters, int n_counters) {
   extern __shared__ __align__(16) uint8_t lds[];
   __shared__ mx_v4f red[2 * 3 * 2 * kWave];
-  __shared__ int sel[kFewMaxRows];
-  __shared__ int rows[kFewTokens], tokens[kFewTokens];
+  __shared__ int ranks[kFewTokens], rows[kFewTokens], tokens[kFewTokens];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int R = T * k;
+  const int units = I / 16;
+  const int runs = (units + units_per_wg - 1) / units_per_wg;
+  const int r = blockIdx.x / runs, run = blockIdx.x - r * runs;
+  const int u0 = run * units_per_wg, u1 = min(u0 + units_per_wg, units);
+  const int t = r / k, j = r - t * k;
 
-  for (int t = wave; t < T; t += kFewThreads / kWave) {
-    float wt;
-    const int e = route_token_values<NS>(logits + int64_t(t) * E, bias, E, k, renormalize, lane, wt);
+  // one workgroup per token writes its routing
+  constexpr int kWaves = kFewThreads / kWave, kMine = kFewTokens / kWaves;
+  if (run == 0 && j == 0 && wave == kWaves - 1) {
+    float w;
+    const int id = route_token_values<NS>(logits + int64_t(t) * E, bias, E, k, renormalize, lane, w);
+    const int best = readlane(id, 0);
+    const float s0 = logits[int64_t(t) * E + best] + (bias ? bias[best] : 0.0f);
     if (lane < k) {
-      sel[t * k + lane] = e;
-      if (blockIdx.x == 0) {
-        // a token whose best score is -inf has no weights (0/0): it gets zeros
-        const int best = readlane(e, 0);
-        const float s0 = logits[int64_t(t) * E + best] + (bias ? bias[best] : 0.0f);
-        ids[t * k + lane] = e;
-        topk_w[t * k + lane] = s0 == -INFINITY ? 0.0f : wt;
-      }
+      ids[t * k + lane] = id;
+      // a token whose best score is -inf has no weights (0/0): it gets zeros
+      topk_w[t * k + lane] = s0 == -INFINITY ? 0.0f : w;
     }
   }
+
+  // Routing.  The row's expert is the j-th best of its token (each wave finds it);
+  // wave w then ranks it among the scores of tokens w, w + 4, ...: another token
+  // has a row for it exactly if its rank there is below k.  (Ranking costs a few
+  // ballots, against k argmax rounds for routing every token.)  The token's own
+  // row of x is read alongside, and the expert's first weights go out as soon as
+  // the expert is known, ahead of the rest: a workgroup that then turns out not to
+  // own its expert has read one item in vain.
+  Scores<NS> own, mine[kMine];
+  own.load(logits + int64_t(t) * E, bias, E, lane);
+  FewStage st(x, tokens, lds, H);
+  EarlyRow early;
+  if (stage_rows > 0) early.load(st, t, tid);
+#pragma unroll
+  for (int i = 0; i < kMine; ++i)
+    if (wave + i * kWaves < T) mine[i].load(logits + int64_t(wave + i * kWaves) * E, bias, E, lane);
+  const int e = own.at_rank(j, lane);
+  auto blk = [I](int u, int b) { return u + b * (I / 16); };
+  const FewWeights<decltype(blk)> wt(w13, ws13, e, (2 * I) / 16, H, wave, blk);
+  MxFrag f0[2];
+  if (wt.gn > 0) wt.load(u0, 0, lane, f0);
+#pragma unroll
+  for (int i = 0; i < kMine; ++i)
+    if (wave + i * kWaves < T) {
+      const int rank = mine[i].rank_of(e, lane);
+      if (lane == 0) ranks[wave + i * kWaves] = rank;
+    }
+  if (stage_rows > 0) early.store(st, t, tid);
   if (blockIdx.x == 0)
     for (int i = tid; i < n_counters; i += kFewThreads) counters[i] = 0;
   lds_barrier();
-  const int units = I / 16;
-  const int runs = (units + units_per_wg - 1) / units_per_wg;
-  const int r = blockIdx.x / runs;
-  const int u0 = (blockIdx.x - r * runs) * units_per_wg, u1 = min(u0 + units_per_wg, units);
-  const int e_lo = sel[min(lane, R - 1)], e_hi = sel[min(lane + kWave, R - 1)];
-  const FewRows f = find_rows(e_lo, e_hi, R, r, lane, rows);    // (every wave writes the same)
-  if (!f.owner) return;                                         // workgroup-uniform
-  const int e = __builtin_amdgcn_readfirstlane(sel[r]);
-  if (lane < f.n) tokens[lane] = rows[lane] / k;
-  lds_barrier();
-
-  FewStage st;
-  st.src = x;
-  st.rows = tokens;
-  st.n = f.n;
-  st.K = H;
-  st.per_row = mx_supers(H) * (kMxSuper / 8);
-  st.row_bytes = st.per_row * 16 + 16;
-  const int64_t blocks = int64_t(2 * I) / 16, G = mx_supers(H);
+  const int rank = ranks[min(lane, T - 1)];
+  const uint64_t members = __ballot(lane < T && rank < k);
+  if (__ffsll(static_cast<unsigned long long>(members)) - 1 != t) return;   // workgroup-uniform
+  const int n = __popcll(members);
+  if (members >> lane & 1) {                            // (every wave writes the same)
+    const int at = __popcll(members & ((uint64_t(1) << lane) - 1));
+    tokens[at] = lane;
+    rows[at] = lane * k + rank;
+  }
+  if (n > 1) lds_barrier();
+  st.n = n;
   const int ln = lane & 15, kb = lane >> 4;
-  few_units(w13 + e * blocks * G * kMxCodeBytes, ws13 + e * blocks * G * kMxScaleBytes, H, u0, u1,
-            st, lds, f.n <= stage_rows, red,
-            [&](int u, int j) { return u + j * (I / 16); },
-            [&](int u, const mx_v4f (&v)[2]) {
-              if (ln >= f.n) return;
-              const mx_v4f hv = silu_mul4(v[0], v[1]);
-              store4(h, 0, int64_t(rows[ln]) * I + 16 * u + 4 * kb, hv);
-            });
+  auto done = [&](int u, const mx_v4f (&v)[2]) {
+    if (ln < n) store4(h, 0, int64_t(rows[ln]) * I + 16 * u + 4 * kb, silu_mul4(v[0], v[1]));
+  };
+  few_run(wt, u0, u1, st, stage_rows, f0, red, done);
 }
 
 // -------------------------------------------------------------- kernel 2
@@ -266,7 +388,7 @@ __device__ __forceinline__ float2 load_through(const float* p) {
   return make_float2(u2f(uint32_t(v)), u2f(uint32_t(v >> 32)));
 }
 
-__global__ void __launch_bounds__(kFewThreads)
+__global__ void __launch_bounds__(kFewThreads, 4)
 few_down_kernel(const int32_t* ids, const float* topk_w, const uint16_t* h, int T, int E, int k,
                 const uint8_t* w2, const uint8_t* ws2, int H, int I, int units_per_wg,
                 int stage_rows, float* o, uint32_t* counters, const uint16_t* shared, uint16_t* y) {
@@ -281,80 +403,82 @@ few_down_kernel(const int32_t* ids, const float* topk_w, const uint16_t* h, int 
   const int r = blockIdx.x / runs;
   const int u0 = (blockIdx.x - r * runs) * units_per_wg, u1 = min(u0 + units_per_wg, units);
   const int e_lo = ids[min(lane, R - 1)], e_hi = ids[min(lane + kWave, R - 1)];
+  FewStage st(h, rows, lds, I);
+  EarlyRow early;
+  if (stage_rows > 0) early.load(st, r, tid);
+  // (ids come from the first kernel of the call; clamped all the same)
+  const int e = min(max(__builtin_amdgcn_readfirstlane(ids[r]), 0), E - 1);
+  auto blk = [](int u, int b) { return 2 * u + b; };
+  const FewWeights<decltype(blk)> wt(w2, ws2, e, H / 16, I, wave, blk);
+  MxFrag f0[2];
+  if (wt.gn > 0) wt.load(u0, 0, lane, f0);
+  if (stage_rows > 0) early.store(st, r, tid);
   const FewRows f = find_rows(e_lo, e_hi, R, r, lane, rows);
   const int ln = lane & 15, kb = lane >> 4;
 
-  // The wave that completes unit u forms y there: T tokens x 8 column quads.
-  auto arrive = [&](int u) {
-    // this wave's stores have reached memory before its arrival does
+  // Wave 0, after its stores: one arrival per unit of the run, then y where this
+  // was the last one (T tokens x 8 column quads per unit).
+  auto arrive = [&]() {
+    // the stores have reached memory before the arrivals are counted
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     uint32_t before = 0;
-    if (lane == 0)
-      before = __hip_atomic_fetch_add(counters + u, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    before = __builtin_amdgcn_readfirstlane(before);
+    if (lane < u1 - u0)
+      before = __hip_atomic_fetch_add(counters + u0 + lane, 1u, __ATOMIC_RELAXED,
+                                      __HIP_MEMORY_SCOPE_AGENT);
+    uint64_t last = __ballot(lane < u1 - u0 && before + 1 == uint32_t(R));
     asm volatile("" ::: "memory");
-    if (before + 1 != uint32_t(R)) return;
-    for (int i = lane; i < T * 8; i += kWave) {
-      const int t = i >> 3, c = 32 * u + 4 * (i & 7);
-      float2 p[MOEQ_MAX_TOPK][2];
-      float wt[MOEQ_MAX_TOPK];
+    for (; last; last &= last - 1) {
+      const int u = u0 + __ffsll(static_cast<unsigned long long>(last)) - 1;
+      for (int i = lane; i < T * 8; i += kWave) {
+        const int t = i >> 3, c = 32 * u + 4 * (i & 7);
+        float2 p[MOEQ_MAX_TOPK][2];
+        float wt[MOEQ_MAX_TOPK];
 #pragma unroll
-      for (int j = 0; j < MOEQ_MAX_TOPK; ++j) {
-        const int s = t * k + min(j, k - 1);
-        p[j][0] = load_through(o + int64_t(s) * H + c);
-        p[j][1] = load_through(o + int64_t(s) * H + c + 2);
-        wt[j] = topk_w[s];
-      }
-      mx_v4f acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int j = 0; j < MOEQ_MAX_TOPK; ++j) {
-        if (j < k) {
-          acc[0] = fmaf(wt[j], p[j][0].x, acc[0]);
-          acc[1] = fmaf(wt[j], p[j][0].y, acc[1]);
-          acc[2] = fmaf(wt[j], p[j][1].x, acc[2]);
-          acc[3] = fmaf(wt[j], p[j][1].y, acc[3]);
+        for (int j = 0; j < MOEQ_MAX_TOPK; ++j) {
+          const int s = t * k + min(j, k - 1);
+          p[j][0] = load_through(o + int64_t(s) * H + c);
+          p[j][1] = load_through(o + int64_t(s) * H + c + 2);
+          wt[j] = topk_w[s];
         }
+        mx_v4f acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < MOEQ_MAX_TOPK; ++j) {
+          if (j < k) {
+            acc[0] = fmaf(wt[j], p[j][0].x, acc[0]);
+            acc[1] = fmaf(wt[j], p[j][0].y, acc[1]);
+            acc[2] = fmaf(wt[j], p[j][1].x, acc[2]);
+            acc[3] = fmaf(wt[j], p[j][1].y, acc[3]);
+          }
+        }
+        if (shared) {
+          const uint2 sh = *reinterpret_cast<const uint2*>(shared + int64_t(t) * H + c);
+          acc[0] += u2f(sh.x << 16);
+          acc[1] += u2f(sh.x & 0xFFFF0000u);
+          acc[2] += u2f(sh.y << 16);
+          acc[3] += u2f(sh.y & 0xFFFF0000u);
+        }
+        store4(y, 0, int64_t(t) * H + c, acc);
       }
-      if (shared) {
-        const uint2 sh = *reinterpret_cast<const uint2*>(shared + int64_t(t) * H + c);
-        acc[0] += u2f(sh.x << 16);
-        acc[1] += u2f(sh.x & 0xFFFF0000u);
-        acc[2] += u2f(sh.y << 16);
-        acc[3] += u2f(sh.y & 0xFFFF0000u);
-      }
-      store4(y, 0, int64_t(t) * H + c, acc);
     }
   };
 
   if (!f.owner) {                               // its expert's rows are another workgroup's
-    if (wave == 0)
-      for (int u = u0; u < u1; ++u) arrive(u);
+    if (wave == 0) arrive();
     return;
   }
-  // (ids come from the first kernel of the call; clamped all the same)
-  const int e = __builtin_amdgcn_readfirstlane(min(max(ids[r], 0), E - 1));
   lds_barrier();
-
-  FewStage st;
-  st.src = h;
-  st.rows = rows;
   st.n = f.n;
-  st.K = I;
-  st.per_row = mx_supers(I) * (kMxSuper / 8);
-  st.row_bytes = st.per_row * 16 + 16;
-  const int64_t blocks = H / 16, G = mx_supers(I);
-  few_units(w2 + e * blocks * G * kMxCodeBytes, ws2 + e * blocks * G * kMxScaleBytes, I, u0, u1, st,
-            lds, f.n <= stage_rows, red, [&](int u, int j) { return 2 * u + j; },
-            [&](int u, const mx_v4f (&v)[2]) {
-              if (ln < f.n) {
-                float* p = o + int64_t(rows[ln]) * H + 32 * u + 4 * kb;
-                store_through(p, v[0][0], v[0][1]);
-                store_through(p + 2, v[0][2], v[0][3]);
-                store_through(p + 16, v[1][0], v[1][1]);
-                store_through(p + 18, v[1][2], v[1][3]);
-              }
-              arrive(u);
-            });
+  auto done = [&](int u, const mx_v4f (&v)[2]) {
+    if (ln < f.n) {
+      float* p = o + int64_t(rows[ln]) * H + 32 * u + 4 * kb;
+      store_through(p, v[0][0], v[0][1]);
+      store_through(p + 2, v[0][2], v[0][3]);
+      store_through(p + 16, v[1][0], v[1][1]);
+      store_through(p + 18, v[1][2], v[1][3]);
+    }
+  };
+  few_run(wt, u0, u1, st, stage_rows, f0, red, done);
+  if (wave == 0) arrive();
 }
 
 size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
@@ -362,12 +486,24 @@ size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 // rows staged in LDS for rows of K elements, and the bytes they take
 int few_stage_rows(int T, int K) {
   const int row_bytes = mx_supers(K) * (kMxSuper * 2) + 16;
-  const int fit = (64 << 10) / row_bytes;
+  const int fit = kStageBytes / row_bytes;
   int n = T < kStageRows ? T : kStageRows;
   return n < fit ? n : fit;
 }
 unsigned few_stage_bytes(int T, int K) {
   return unsigned(few_stage_rows(T, K) * (mx_supers(K) * (kMxSuper * 2) + 16));
+}
+
+// Column units per workgroup.  One unit each lets the dispatcher balance the CUs,
+// several spread the routing and the joins over more weights; the launch is to
+// hold about 3072 workgroups (four per CU, three rounds).  Measured at 4096 x
+// 2048, top-6 of 256 (gate/up, down; us): T = 1: 13.8, 8.3 with one unit, 14.8,
+// 10.2 with two; T = 4: 36.9, 20.6 with one, 37.5, 22.2 with two, 37.9, 24.6 with
+// four; T = 16: 142.5, 76.9 with one, 115.3, 67.8 with two, 105.8, 66.8 with four,
+// 112.5, 76.3 with six.
+int few_units_per_wg(int R, int units) {
+  const int64_t n = int64_t(R) * units / 3072;
+  return n < 1 ? 1 : n > 4 ? 4 : int(n);
 }
 
 }  // namespace
@@ -388,7 +524,7 @@ hipError_t launch_layer_mxfp4_few(const float* logits, const float* bias, int T,
   uint32_t* counters = reinterpret_cast<uint32_t*>(base);
   uint16_t* h = reinterpret_cast<uint16_t*>(base + align256(size_t(H / 32) * 4));
   float* o = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(h) + align256(size_t(R) * I * 2));
-  const int upw1 = 1, upw2 = 1;
+  const int upw1 = few_units_per_wg(R, I / 16), upw2 = few_units_per_wg(R, H / 32);
   const int runs1 = (I / 16 + upw1 - 1) / upw1, runs2 = (H / 32 + upw2 - 1) / upw2;
   with_route_slots(E, [&](auto ns) {
     hipLaunchKernelGGL((few_gate_up_kernel<decltype(ns)::value>), dim3(unsigned(R * runs1)),

@@ -7,14 +7,12 @@ call runs on the current stream of its tensors' device.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import Optional, Tuple
 
 import torch
 
-from . import (EPI_NONE, EPI_SILU_MUL, MAX_TOPK, MOEQ_BF16, MOEQ_F32, _check, _check_plan, _out,
-               _ptr, _req, _stream, lib)
+from . import EPI_NONE, EPI_SILU_MUL, MAX_TOPK, MOEQ_BF16, MOEQ_F32, _check, _plan_shape_ok, lib
 
 __all__ = ["MX_BLOCK", "FEW_TOKENS", "MX_SYMBOLS", "quant_mxfp4", "dequant_mxfp4",
            "tile_mxfp4_weights", "moe_grouped_gemm_mxfp4", "moe_layer_mxfp4_few",
@@ -41,41 +39,70 @@ for _name, (_res, _args) in _SIGNATURES.items():
     _fn.restype, _fn.argtypes = _res, _args
 
 
-def _on(device: torch.device):
-    """Makes device the current one for the launch, if it is not."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+_F = {torch.bfloat16: MOEQ_BF16, torch.float32: MOEQ_F32}
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _same_device(dev: torch.device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the call runs on {dev}")
+def _launch(name: str, index: int, *args):
+    """Calls lib.name(*args, stream) on device `index` and its current stream.  (A decode step's
+    calls take a few microseconds of GPU time, so this path creates no stream or pointer objects.)"""
+    fn = getattr(lib, name)
+    if index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
+    if status:
+        _check(name, status)
 
 
 def _float_dtype(dtype, name: str) -> int:
-    if dtype == torch.bfloat16:
-        return MOEQ_BF16
-    if dtype == torch.float32:
-        return MOEQ_F32
-    raise TypeError(f"{name} must be float32 or bfloat16, got {dtype}")
+    dt = _F.get(dtype)
+    if dt is None:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {dtype}")
+    return dt
 
 
-def _checked_out(t: Optional[torch.Tensor], name: str, shape, dtype, dev) -> torch.Tensor:
-    return _out({name: t}, name, tuple(shape), dtype, dev)
+def _tensor(t: torch.Tensor, name: str, dtype, ndim: int, index: int = -1) -> int:
+    """Checks a contiguous device tensor of ndim dims, on device `index` if one is given; returns
+    its device's index."""
+    try:
+        i = t.get_device()
+        if t.dtype is dtype and t.dim() == ndim and t.is_contiguous() and i >= 0 and \
+                (i == index or index < 0):
+            return i
+    except AttributeError:
+        raise TypeError(f"{name} must be a tensor") from None
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got {t.dim()}")
+    if i < 0:
+        raise ValueError(f"{name} must be a device tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} is on device {i}, the call runs on device {index}")
 
 
-def _codes(q: torch.Tensor, scale: torch.Tensor, name: str) -> int:
-    """K of MXFP4 rows: codes [..., K/2], scales [..., K/32]."""
-    _req(q, name, torch.uint8)
-    _req(scale, name + " scales", torch.uint8)
-    if q.dim() < 1 or q.dim() != scale.dim() or q.shape[:-1] != scale.shape[:-1] or \
-            q.shape[-1] != 16 * scale.shape[-1]:
+def _output(t: Optional[torch.Tensor], name: str, shape: tuple, dtype, index: int) -> torch.Tensor:
+    """The caller's tensor, checked against what the call writes, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                         f"device {index}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t
+
+
+def _codes(q: torch.Tensor, scale: torch.Tensor, name: str, ndim: int) -> Tuple[int, int]:
+    """K and the device of MXFP4 rows: codes [..., K/2], scales [..., K/32]."""
+    index = _tensor(q, name, torch.uint8, ndim)
+    _tensor(scale, name + " scales", torch.uint8, ndim, index)
+    qs, ss = q.shape, scale.shape
+    if not qs or qs[:-1] != ss[:-1] or qs[-1] != 16 * ss[-1]:
         raise ValueError(f"{name}: codes [..., K/2] and scales [..., K/32] do not match: "
-                         f"{tuple(q.shape)}, {tuple(scale.shape)}")
-    _same_device(q.device, **{name + " scales": scale})
-    return 2 * q.shape[-1]
+                         f"{tuple(qs)}, {tuple(ss)}")
+    return 2 * qs[-1], index
 
 
 def quant_mxfp4(x: torch.Tensor, q: Optional[torch.Tensor] = None,
@@ -83,69 +110,64 @@ def quant_mxfp4(x: torch.Tensor, q: Optional[torch.Tensor] = None,
     """x [..., K] fp32/bf16 -> (codes [..., K/2], scales [..., K/32]).  x is contiguous, or a
     2-D tensor whose rows are (columns of a wider matrix)."""
     dt = _float_dtype(x.dtype, "x")
-    if not x.is_cuda:
+    dev = x.get_device()
+    if dev < 0:
         raise ValueError("x must be a device tensor")
-    if x.dim() < 1:
+    shape = x.shape
+    if not shape:
         raise ValueError("x must have rows")
-    K = x.shape[-1]
+    K = shape[-1]
     if x.is_contiguous():
         ld = K
-    elif x.dim() == 2 and x.stride(1) == 1 and x.stride(0) >= K:
+    elif len(shape) == 2 and x.stride(1) == 1 and x.stride(0) >= K:
         ld = x.stride(0)
     else:
         raise ValueError("x must be contiguous, or 2-D with contiguous rows")
     M = x.numel() // K if K else 0
-    lead = tuple(x.shape[:-1])
-    q = _checked_out(q, "q", lead + (K // 2,), torch.uint8, x.device)
-    scale = _checked_out(scale, "scale", lead + (K // MX_BLOCK,), torch.uint8, x.device)
-    with _on(x.device):
-        _check("quant_mxfp4", lib.quant_mxfp4(_ptr(x), dt, M, K, ld, _ptr(q), _ptr(scale),
-                                              _stream(x.device)))
+    q = _output(q, "q", shape[:-1] + (K // 2,), torch.uint8, dev)
+    scale = _output(scale, "scale", shape[:-1] + (K // MX_BLOCK,), torch.uint8, dev)
+    _launch("quant_mxfp4", dev, x.data_ptr(), dt, M, K, ld, q.data_ptr(), scale.data_ptr())
     return q, scale
 
 
 def dequant_mxfp4(q: torch.Tensor, scale: torch.Tensor, out: Optional[torch.Tensor] = None,
                   dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """The values [..., K] of MXFP4 rows, exact, in `dtype` (or out's)."""
-    K = _codes(q, scale, "q")
+    K, dev = _codes(q, scale, "q", q.dim())
     dtype = dtype if out is None else out.dtype
     dt = _float_dtype(dtype, "out")
-    out = _checked_out(out, "out", tuple(q.shape[:-1]) + (K,), dtype, q.device)
+    out = _output(out, "out", q.shape[:-1] + (K,), dtype, dev)
     M = out.numel() // K if K else 0
-    with _on(q.device):
-        _check("dequant_mxfp4", lib.dequant_mxfp4(_ptr(q), _ptr(scale), M, K, _ptr(out), dt,
-                                                  _stream(q.device)))
+    _launch("dequant_mxfp4", dev, q.data_ptr(), scale.data_ptr(), M, K, out.data_ptr(), dt)
     return out
 
 
 def tile_mxfp4_weights(q: torch.Tensor, scale: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     """Weights [E, N, K] in rows (codes [E, N, K/2], scales [E, N, K/32]) -> the products'
     tiled order (codes [E, N/16, G, 4, 64, 16], scales [E, N/16, G, 64, 4], G = ceil(K / 512))."""
-    K = _codes(q, scale, "q")
-    if q.dim() != 3 or q.shape[1] % 16 != 0 or K == 0:
-        raise ValueError("weights are [E, N, K] with N a multiple of 16")
+    K, dev = _codes(q, scale, "q", 3)
     E, N = q.shape[:2]
+    if N % 16 != 0 or K == 0:
+        raise ValueError("weights are [E, N, K] with N a multiple of 16")
     G = (K + _SUPER - 1) // _SUPER
     w = torch.empty(E, N // 16, G, 4, 64, 16, dtype=torch.uint8, device=q.device)
     ws = torch.empty(E, N // 16, G, 64, 4, dtype=torch.uint8, device=q.device)
-    with _on(q.device):
-        _check("moe_tile_mxfp4_weights", lib.moe_tile_mxfp4_weights(
-            _ptr(q), _ptr(scale), E * N, K, _ptr(w), _ptr(ws), _stream(q.device)))
+    _launch("moe_tile_mxfp4_weights", dev, q.data_ptr(), scale.data_ptr(), E * N, K,
+            w.data_ptr(), ws.data_ptr())
     return w, ws
 
 
-def _tiled(w: torch.Tensor, ws: torch.Tensor, K: int, name: str, dev) -> Tuple[int, int]:
+def _tiled(w: torch.Tensor, ws: torch.Tensor, K: int, name: str, dev: int) -> Tuple[int, int]:
     """(E, N) of tiled weights of K columns."""
-    if not isinstance(w, torch.Tensor) or w.dim() != 6 or tuple(w.shape[3:]) != (4, 64, 16):
+    if not isinstance(w, torch.Tensor) or w.dim() != 6:
         raise ValueError(f"{name} must be in the tiled order [E, N/16, ceil(K/512), 4, 64, 16] "
                          "(tile_mxfp4_weights)")
-    _req(w, name, torch.uint8)
-    _req(ws, name + " scales", torch.uint8)
-    E, nb, G = w.shape[:3]
-    if G != (K + _SUPER - 1) // _SUPER or tuple(ws.shape) != (E, nb, G, 64, 4):
-        raise ValueError(f"{name} does not hold weights of K = {K} with their scales: "
+    _tensor(w, name, torch.uint8, 6, dev)
+    _tensor(ws, name + " scales", torch.uint8, 5, dev)
+    E, nb, G, *lanes = w.shape
+    if lanes != [4, 64, 16] or G != (K + _SUPER - 1) // _SUPER or ws.shape != (E, nb, G, 64, 4):
+        raise ValueError(f"{name} does not hold tiled weights of K = {K} with their scales: "
                          f"{tuple(w.shape)}, {tuple(ws.shape)}")
-    _same_device(dev, **{name: w, name + " scales": ws})
     return E, 16 * nb
 
 
@@ -156,24 +178,19 @@ def moe_grouped_gemm_mxfp4(a_q: torch.Tensor, a_s: torch.Tensor, plan: torch.Ten
     """Grouped GEMM with MXFP4 activations and (tiled) MXFP4 weights.  topk = 0: a holds the
     routed rows in plan order; topk = k: a holds the tokens and routed row r reads row r // k.
     Returns [R, N] (EPI_NONE) or [R, N/2] bf16 (EPI_SILU_MUL)."""
-    K = _codes(a_q, a_s, "a_q")
-    if a_q.dim() != 2:
-        raise ValueError("a_q must have 2 dims")
+    K, dev = _codes(a_q, a_s, "a_q", 2)
     if not 0 <= topk <= MAX_TOPK:
         raise ValueError(f"topk must be 0 .. {MAX_TOPK}")
-    dev = a_q.device
     E, N = _tiled(w, w_scale, K, "w", dev)
-    R = a_q.shape[0] * max(topk, 1)
-    _check_plan(plan, E, R)
-    _same_device(dev, plan=plan)
-    silu = epilogue == EPI_SILU_MUL
+    R = a_q.shape[0] * (topk or 1)
+    _tensor(plan, "plan", torch.int32, 1, dev)
+    _plan_shape_ok(plan, E, R)
     dtype = out_dtype if out is None else out.dtype
     dt = _float_dtype(dtype, "out")
-    out = _checked_out(out, "out", (R, N // 2 if silu else N), dtype, dev)
-    with _on(dev):
-        _check("moe_grouped_gemm_mxfp4", lib.moe_grouped_gemm_mxfp4(
-            _ptr(a_q), _ptr(a_s), topk, _ptr(plan), plan.numel() * 4, E, R, _ptr(w),
-            _ptr(w_scale), N, K, epilogue, _ptr(out), dt, _stream(dev)))
+    out = _output(out, "out", (R, N // 2 if epilogue == EPI_SILU_MUL else N), dtype, dev)
+    _launch("moe_grouped_gemm_mxfp4", dev, a_q.data_ptr(), a_s.data_ptr(), topk,
+            plan.data_ptr(), plan.numel() * 4, E, R, w.data_ptr(), w_scale.data_ptr(), N, K,
+            epilogue, out.data_ptr(), dt)
     return out
 
 
@@ -189,45 +206,41 @@ def moe_layer_mxfp4_few(logits: torch.Tensor, x: torch.Tensor, w13: torch.Tensor
     """A whole layer for up to FEW_TOKENS tokens in two kernels: tiled MXFP4 weights, bf16
     activations.  Returns a dict with ids [T, k], w [T, k], y [T, H] and the workspace ws
     (reusing out's tensors; calls that may overlap need a ws of their own)."""
-    _req(logits, "logits", torch.float32, 2)
-    _req(x, "x", torch.bfloat16, 2)
-    T, E = logits.shape
-    H = x.shape[1]
-    dev = x.device
-    if x.shape[0] != T:
-        raise ValueError(f"x has {x.shape[0]} rows, logits {T}")
+    dev = _tensor(logits, "logits", torch.float32, 2)
+    _tensor(x, "x", torch.bfloat16, 2, dev)
+    T, H = x.shape
+    E = logits.shape[1]
+    if logits.shape[0] != T:
+        raise ValueError(f"x has {T} rows, logits {logits.shape[0]}")
     E13, N13 = _tiled(w13, w13_scale, H, "w13", dev)
     I = N13 // 2
     E2, N2 = _tiled(w2, w2_scale, I, "w2", dev)
     if E13 != E or E2 != E or N2 != H:
         raise ValueError("w13 [E, 2I, H] and w2 [E, H, I] do not fit logits [T, E] and x [T, H]")
     if bias is not None:
-        _req(bias, "bias", torch.float32, 1)
+        _tensor(bias, "bias", torch.float32, 1, dev)
         if bias.shape[0] != E:
             raise ValueError("bias must be [E]")
     if shared is not None:
-        _req(shared, "shared", torch.bfloat16, 2)
-        if tuple(shared.shape) != (T, H):
+        _tensor(shared, "shared", torch.bfloat16, 2, dev)
+        if shared.shape != (T, H):
             raise ValueError("shared must be [T, H]")
-    _same_device(dev, logits=logits, bias=bias, shared=shared)
     if T > FEW_TOKENS or not 1 <= k <= min(E, MAX_TOPK):
         raise ValueError(f"takes at most {FEW_TOKENS} tokens and 1 .. min(E, {MAX_TOPK}) experts "
                          f"per token, got T = {T}, k = {k}")
-    nbytes = lib.moe_layer_mxfp4_few_ws_size(T, k, H, I)
     o = dict(out) if out is not None else {}
-    _out(o, "ids", (T, k), torch.int32, dev)
-    _out(o, "w", (T, k), torch.float32, dev)
-    _out(o, "y", (T, H), torch.bfloat16, dev)
+    ids = o["ids"] = _output(o.get("ids"), "out['ids']", (T, k), torch.int32, dev)
+    w = o["w"] = _output(o.get("w"), "out['w']", (T, k), torch.float32, dev)
+    y = o["y"] = _output(o.get("y"), "out['y']", (T, H), torch.bfloat16, dev)
     ws = o.get("ws")
     if ws is None:
-        ws = o["ws"] = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        ws = o["ws"] = torch.empty(lib.moe_layer_mxfp4_few_ws_size(T, k, H, I), dtype=torch.uint8,
+                                   device=x.device)
     else:
-        _req(ws, "out['ws']", torch.uint8, 1)
-        _same_device(dev, **{"out['ws']": ws})
-    with _on(dev):
-        _check("moe_layer_mxfp4_few", lib.moe_layer_mxfp4_few(
-            _ptr(logits), _ptr(bias), T, E, k, 1 if renormalize else 0, _ptr(x), H, _ptr(w13),
-            _ptr(w13_scale), _ptr(w2), _ptr(w2_scale), I, _ptr(shared), _ptr(o["ids"]),
-            _ptr(o["w"]), _ptr(o["y"]), _ptr(ws), ws.numel(), _stream(dev)))
+        _tensor(ws, "out['ws']", torch.uint8, 1, dev)
+    _launch("moe_layer_mxfp4_few", dev, logits.data_ptr(),
+            None if bias is None else bias.data_ptr(), T, E, k, 1 if renormalize else 0,
+            x.data_ptr(), H, w13.data_ptr(), w13_scale.data_ptr(), w2.data_ptr(),
+            w2_scale.data_ptr(), I, None if shared is None else shared.data_ptr(), ids.data_ptr(),
+            w.data_ptr(), y.data_ptr(), ws.data_ptr(), ws.numel())
     return o
-

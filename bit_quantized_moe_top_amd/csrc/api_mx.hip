@@ -56,7 +56,7 @@ int quant_mxfp4(const void* x, int x_dtype, int64_t M, int K, int64_t ld_x, uint
   if (!dtype_ok(x_dtype) || ld_x < K) return MOEQ_ERR_INVALID_ARG;
   if (ld_x % 8 != 0) return MOEQ_ERR_UNSUPPORTED;
   if (M == 0) return MOEQ_OK;
-  if (!x || !q || !scale || !aligned16(x) || !aligned_to(q, 8)) return MOEQ_ERR_INVALID_ARG;
+  if (!x || !q || !scale || !aligned16(x) || !aligned16(q)) return MOEQ_ERR_INVALID_ARG;
   if (int rc = check_device()) return rc;
   return launch_status(moeq::launch_quant_mxfp4(x, x_dtype, M, K, ld_x, q, scale, as_stream(stream)));
 }

@@ -39,7 +39,7 @@ extern "C" {
  *   x [M, K] fp32 or bf16 (x_dtype), row stride ld_x elements
  *   q [M, K/2] (out)     scale [M, K/32] (out), both contiguous
  * Limits: M >= 0, K % 32 == 0, ld_x >= K, ld_x % 8 == 0, M * K <= 2^40;
- * x 16-byte, q 8-byte aligned; outputs do not overlap x.
+ * x and q 16-byte aligned; outputs do not overlap x.
  */
 int quant_mxfp4(const void* x, int x_dtype, int64_t M, int K, int64_t ld_x, uint8_t* q,
                 uint8_t* scale, void* stream);

@@ -150,6 +150,8 @@ GEMM_CASES = [
     (16, 2, 8, 256, 256, None), (17, 1, 2, 32, 1440, 0), (64, 1, 3, 32, 512, 1),
     (65, 2, 4, 160, 1024, 3), (100, 4, 5, 288, 2048, 0), (230, 3, 7, 96, 1056, 1),
     (300, 2, 40, 512, 640, None), (256, 1, 1, 544, 4096, 0), (700, 6, 16, 256, 512, 5),
+    # enough row tiles and columns for the 256-row weight tiles, ragged in every direction
+    (600, 4, 60, 2080, 160, 7), (900, 3, 24, 2336, 544, 5),
 ]
 
 

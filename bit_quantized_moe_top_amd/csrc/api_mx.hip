@@ -14,8 +14,8 @@ static_assert(MOEQ_FEW_TOKENS == moeq::kFewTokens, "header and library agree");
 
 namespace {
 
-constexpr int64_t kMaxElements = int64_t(1) << 40;
-constexpr int64_t kMaxGrid = 0x7FFFFFFF;
+constexpr int64_t kMaxElements = int64_t(1) << 35;
+constexpr int64_t kMaxGrid = 0xFFFFFF;         // workgroups of 256 threads in one launch
 
 bool dtype_ok(int d) { return d == MOEQ_F32 || d == MOEQ_BF16; }
 
@@ -98,8 +98,7 @@ int moe_grouped_gemm_mxfp4(const uint8_t* a_q, const uint8_t* a_s, int a_topk, c
     return MOEQ_ERR_INVALID_ARG;
   if (a_topk > MOEQ_MAX_TOPK) return MOEQ_ERR_UNSUPPORTED;
   if (a_topk > 0 && R % a_topk != 0) return MOEQ_ERR_INVALID_ARG;
-  if (R > 0x3FFFFFFF || int64_t(moeq::plan_max_tiles(E, R)) * (N / 32) > kMaxGrid)
-    return MOEQ_ERR_UNSUPPORTED;
+  if (R > 0x3FFFFFFF || moeq::mxfp4_gemm_grid(E, R, N) > kMaxGrid) return MOEQ_ERR_UNSUPPORTED;
   if (R == 0) return MOEQ_OK;
   if (!a_q || !a_s || !plan || !w || !ws || !out) return MOEQ_ERR_INVALID_ARG;
   if (!aligned16(a_q) || !aligned_to(a_s, 4) || !aligned16(w) || !aligned16(ws) || !aligned16(out))

@@ -35,9 +35,10 @@ constexpr int kFewThreads = 256;
 constexpr int kFewMaxRows = 2 * kWave;        // routed rows: 16 tokens x 8 experts
 static_assert(kFewTokens * MOEQ_MAX_TOPK <= kFewMaxRows, "two ballots cover the routed rows");
 // Activation rows staged in LDS: at most four, in at most 17 KB (two rows of 4096
-// elements): with more, fewer workgroups fit a CU (T = 4 at 4096 x 2048, gate/up:
-// 53.4 us with 33 KB against 49.4 us with 17 KB, before the other steps below)
-// for rows that are rarely there; an expert with more rows reads them from memory.
+// elements).  With more, fewer workgroups fit a CU for rows that are rarely there
+// (gate/up at 4096 x 2048, top-6 of 256 experts, four tokens, an earlier build:
+// 53.4 us with four rows, 49.4 us with two); an expert with more rows reads them
+// from memory.
 constexpr int kStageRows = 4, kStageBytes = 17 << 10;
 
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
@@ -248,7 +249,9 @@ __device__ __forceinline__ void few_run(const WeightsT& wt, int u0, int u1, cons
 
 // -------------------------------------------------------------- kernel 1
 // One token's biased scores as order-preserving keys (front.hpp), expert e in lane
-// e % 64, slot e / 64; 0 past E.
+// e % 64, slot e / 64; 0 past E and at least 1 before it (one NaN has key 0), so that
+// every expert has a rank and at_rank and rank_of invert each other whatever the
+// scores hold: each routed row is computed by exactly one workgroup per unit.
 template <int NS>
 struct Scores {
   uint32_t key[NS];
@@ -261,7 +264,7 @@ struct Scores {
       for (int i = 0; i < NS; ++i) s[i] = s[i] + bias[min(i * kWave + lane, E - 1)];
     }
 #pragma unroll
-    for (int i = 0; i < NS; ++i) key[i] = i * kWave + lane < E ? score_key(s[i]) : 0u;
+    for (int i = 0; i < NS; ++i) key[i] = i * kWave + lane < E ? max(score_key(s[i]), 1u) : 0u;
   }
   // the expert of rank j (0 the best): j + 1 rounds of a wave-wide argmax, as in
   // route_token_values
@@ -318,7 +321,8 @@ few_gate_up_kernel(const float* logits, const float* bias, int T, int E, int k, 
   constexpr int kWaves = kFewThreads / kWave, kMine = kFewTokens / kWaves;
   if (run == 0 && j == 0 && wave == kWaves - 1) {
     float w;
-    const int id = route_token_values<NS>(logits + int64_t(t) * E, bias, E, k, renormalize, lane, w);
+    const int id = min(
+        route_token_values<NS>(logits + int64_t(t) * E, bias, E, k, renormalize, lane, w), E - 1);
     const int best = readlane(id, 0);
     const float s0 = logits[int64_t(t) * E + best] + (bias ? bias[best] : 0.0f);
     if (lane < k) {
@@ -443,7 +447,8 @@ few_down_kernel(const int32_t* ids, const float* topk_w, const uint16_t* h, int 
         mx_v4f acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < MOEQ_MAX_TOPK; ++j) {
-          if (j < k) {
+          // (a weight of 0, a masked expert's, adds nothing whatever its row holds)
+          if (j < k && wt[j] != 0.0f) {
             acc[0] = fmaf(wt[j], p[j][0].x, acc[0]);
             acc[1] = fmaf(wt[j], p[j][0].y, acc[1]);
             acc[2] = fmaf(wt[j], p[j][1].x, acc[2]);

@@ -166,6 +166,9 @@ hipError_t launch_grouped_gemm_mxfp4(const uint8_t* a_q, const uint8_t* a_s, int
                                      const uint8_t* ws, int N, int K, int epilogue, void* out,
                                      int out_dtype, hipStream_t stream);
 
+// its workgroups
+int64_t mxfp4_gemm_grid(int E, int R, int N);
+
 // a whole layer for at most kFewTokens tokens (few.hip)
 constexpr int kFewTokens = 16;
 size_t few_ws_bytes(int T, int k, int H, int I);

@@ -341,7 +341,31 @@ gemm_mx_tile_kernel(const uint8_t* a_q, const uint8_t* a_s, int a_topk, const in
   else body(std::integral_constant<int, kCpStream>());
 }
 
+// Which kernel takes R rows over E experts of N weight rows, and its grid.
+//
+// Few rows per expert: the K-split units, otherwise the tile kernel.  Measured on
+// the gate/up product (K-split against tile kernel, us): E = 256 experts: R = 1536
+// rows 350 / 360, 2046 rows 371 / 356; E = 64: 512 rows 26.3 / 27.7, 1024 33.2 / 29.7;
+// E = 16: 128 rows 25.6 / 26.4, 256 30.5 / 26.6; E = 4: 128 rows 13.0 / 15.3, 256 22.0 /
+// 16.8; E = 1: 128 rows 10.3 / 15.1, 512 26.2 / 17.7.
+// Tiles of 256 weight rows if they make two workgroups per CU, which is what fits,
+// else of 128: E = 4, 256 rows each: 24.2 us with 256 (320 items), 21.9 with 128;
+// E = 1, 2048 rows: 30.2 (528 items) and 41.2.
+struct MxShape {
+  int cb;               // weight blocks per wave of the tile kernel; 0: K-split units
+  int64_t grid;
+};
+MxShape mx_shape(int E, int R, int N) {
+  const int64_t tiles = plan_max_tiles(E, R);
+  if (R <= 7 * E || R <= 160) return {0, tiles * (N / 32)};
+  const int64_t wide = tiles * ((N + 255) / 256);
+  if (wide >= 512) return {4, wide};
+  return {2, tiles * ((N + 127) / 128)};
+}
+
 }  // namespace
+
+int64_t mxfp4_gemm_grid(int E, int R, int N) { return mx_shape(E, R, N).grid; }
 
 hipError_t launch_grouped_gemm_mxfp4(const uint8_t* a_q, const uint8_t* a_s, int a_topk,
                                      const void* plan, int E, int R, const uint8_t* w,
@@ -350,31 +374,16 @@ hipError_t launch_grouped_gemm_mxfp4(const uint8_t* a_q, const uint8_t* a_s, int
   if (R == 0) return hipSuccess;
   const int out_f32 = out_dtype == MOEQ_F32 ? 1 : 0;
   const int32_t* p = static_cast<const int32_t*>(plan);
-  const int max_tiles = plan_max_tiles(E, R);
+  const MxShape shape = mx_shape(E, R, N);
+  auto launch = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(unsigned(shape.grid)), dim3(kThreads), 0, stream, a_q, a_s,
+                       a_topk, p, E, R, w, ws, N, K, out, out_f32);
+  };
   auto go = [&](auto epi) {
     constexpr int EPI = decltype(epi)::value;
-    auto tile = [&](auto cb) {
-      constexpr int CB = decltype(cb)::value;
-      const int64_t grid = int64_t(max_tiles) * ((N / 16 + 4 * CB - 1) / (4 * CB));
-      hipLaunchKernelGGL((gemm_mx_tile_kernel<EPI, CB>), dim3(unsigned(grid)), dim3(kThreads), 0,
-                         stream, a_q, a_s, a_topk, p, E, R, w, ws, N, K, out, out_f32);
-    };
-    // Few rows per expert: the K-split units, otherwise the tile kernel.  Measured on
-    // the gate/up product (K-split against tile kernel, us) at R rows over E experts:
-    // E = 256: R = 1536 350 / 360, 2046 371 / 356; E = 64: 512 26.3 / 27.7, 1024 33.2 /
-    // 29.7; E = 16: 128 25.6 / 26.4, 256 30.5 / 26.6; E = 4: 128 13.0 / 15.3, 256 22.0 /
-    // 16.8; E = 1: 128 10.3 / 15.1, 512 26.2 / 17.7.
-    // Tiles of 256 weight rows if they make two workgroups per CU, which is what fits,
-    // else of 128: E = 4, 256 rows each: 24.2 us with 256 (320 items), 21.9 with 128;
-    // E = 1, 2048 rows: 30.2 (528 items) and 41.2.
-    if (R <= 7 * E || R <= 160)
-      hipLaunchKernelGGL(gemm_mx_wave_kernel<EPI>, dim3(unsigned(int64_t(max_tiles) * (N / 32))),
-                         dim3(kThreads), 0, stream, a_q, a_s, a_topk, p, E, R, w, ws, N, K, out,
-                         out_f32);
-    else if (int64_t(max_tiles) * ((N + 255) / 256) >= 512)
-      tile(std::integral_constant<int, 4>());
-    else
-      tile(std::integral_constant<int, 2>());
+    if (shape.cb == 0) launch(gemm_mx_wave_kernel<EPI>);
+    else if (shape.cb == 4) launch(gemm_mx_tile_kernel<EPI, 4>);
+    else launch(gemm_mx_tile_kernel<EPI, 2>);
   };
   if (epilogue == MOEQ_EPI_SILU_MUL) go(std::integral_constant<int, MOEQ_EPI_SILU_MUL>());
   else go(std::integral_constant<int, MOEQ_EPI_NONE>());

@@ -154,6 +154,7 @@ def tile_mxfp4_weights(q: torch.Tensor, scale: torch.Tensor) -> Tuple[torch.Tens
     ws = torch.empty(E, N // 16, G, 64, 4, dtype=torch.uint8, device=q.device)
     _launch("moe_tile_mxfp4_weights", dev, q.data_ptr(), scale.data_ptr(), E * N, K,
             w.data_ptr(), ws.data_ptr())
+    w._moeq_k = K              # the shape alone tells K only to whole super-groups
     return w, ws
 
 
@@ -168,6 +169,8 @@ def _tiled(w: torch.Tensor, ws: torch.Tensor, K: int, name: str, dev: int) -> Tu
     if lanes != [4, 64, 16] or G != (K + _SUPER - 1) // _SUPER or ws.shape != (E, nb, G, 64, 4):
         raise ValueError(f"{name} does not hold tiled weights of K = {K} with their scales: "
                          f"{tuple(w.shape)}, {tuple(ws.shape)}")
+    if getattr(w, "_moeq_k", K) != K:
+        raise ValueError(f"{name} holds weights of K = {w._moeq_k}, the call has {K}")
     return E, 16 * nb
 
 

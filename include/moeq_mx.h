@@ -38,7 +38,7 @@ extern "C" {
  *
  *   x [M, K] fp32 or bf16 (x_dtype), row stride ld_x elements
  *   q [M, K/2] (out)     scale [M, K/32] (out), both contiguous
- * Limits: M >= 0, K % 32 == 0, ld_x >= K, ld_x % 8 == 0, M * K <= 2^40;
+ * Limits: M >= 0, K % 32 == 0, ld_x >= K, ld_x % 8 == 0, M * K <= 2^35;
  * x and q 16-byte aligned; outputs do not overlap x.
  */
 int quant_mxfp4(const void* x, int x_dtype, int64_t M, int K, int64_t ld_x, uint8_t* q,
@@ -50,7 +50,7 @@ int quant_mxfp4(const void* x, int x_dtype, int64_t M, int K, int64_t ld_x, uint
  * quant_mxfp4 writes; 253 and 254 may overflow to infinity, 255 gives NaN.
  *
  *   q [M, K/2], scale [M, K/32]   out [M, K] fp32 or bf16 (out_dtype)
- * Limits: M >= 0, K % 32 == 0, M * K <= 2^40; q 4-byte, out 16-byte aligned.
+ * Limits: M >= 0, K % 32 == 0, M * K <= 2^35; q 4-byte, out 16-byte aligned.
  */
 int dequant_mxfp4(const uint8_t* q, const uint8_t* scale, int64_t M, int K, void* out,
                   int out_dtype, void* stream);
@@ -67,7 +67,7 @@ int dequant_mxfp4(const uint8_t* q, const uint8_t* scale, int64_t M, int K, void
  *
  *   q [rows, K/2], scale [rows, K/32]
  *   w [rows/16 * G * 4096] bytes (out)   ws [rows/16 * G * 256] bytes (out)
- * Limits: rows % 16 == 0, K % 32 == 0, K <= MOEQ_MX_MAX_K, rows/16 * G < 2^31;
+ * Limits: rows % 16 == 0, K % 32 == 0, K <= MOEQ_MX_MAX_K, rows/16 * G < 2^24;
  * all but scale 16-byte aligned; outputs do not overlap inputs.
  */
 int moe_tile_mxfp4_weights(const uint8_t* q, const uint8_t* scale, int64_t rows, int K, uint8_t* w,
@@ -89,8 +89,9 @@ int moe_tile_mxfp4_weights(const uint8_t* q, const uint8_t* scale, int64_t rows,
  *   plan, plan_bytes -- from moe_permute with the same E and R (read only)
  *   w, ws -- [E, N, K] weights in the order of moe_tile_mxfp4_weights
  * Limits: N % 32 == 0, K % 32 == 0, K <= MOEQ_MX_MAX_K, 1 <= E <=
- * MOEQ_MAX_EXPERTS, 0 <= a_topk <= MOEQ_MAX_TOPK, R % a_topk == 0; a_q, w, ws
- * and out 16-byte, a_s 4-byte aligned.
+ * MOEQ_MAX_EXPERTS, 0 <= a_topk <= MOEQ_MAX_TOPK, R % a_topk == 0, fewer than 2^24
+ * workgroups (with T = ceil(R / 64) + min(E, R) row tiles: T * N / 32 of them at
+ * most); a_q, w, ws and out 16-byte, a_s 4-byte aligned.
  */
 int moe_grouped_gemm_mxfp4(const uint8_t* a_q, const uint8_t* a_s, int a_topk, const void* plan,
                            size_t plan_bytes, int E, int R, const uint8_t* w, const uint8_t* ws,
@@ -107,7 +108,9 @@ size_t moe_layer_mxfp4_few_ws_size(int T, int k, int H, int I);
  *   y_t = bf16( sum_j topk_w[t, j] * (W2_e h_j) + shared_t )  (fp32 sums in slot order)
  * Nothing is quantized but the weights.  Scores of -inf mark masked experts and
  * get weight 0; a token whose k best scores are all -inf gets weights 0 (y_t =
- * shared_t, or 0).  Other scores are finite.
+ * shared_t, or 0).  An expert of weight 0 adds nothing, whatever its weights hold.
+ * Other scores are finite (with a NaN score the ids stay inside [0, E) and the
+ * token's outputs mean nothing).
  *
  *   logits [T, E] fp32, bias [E] fp32 or NULL, x [T, H] bf16
  *   w13, ws13 -- [E, 2I, H] (gate rows, then up rows), w2, ws2 -- [E, H, I], both in

@@ -245,6 +245,9 @@ def test_grouped_gemm_no_rows_and_wrong_shapes():
     with pytest.raises(ValueError, match="K = 1056"):
         b_q, b_s = mq.quant_mxfp4(torch.zeros(4, 1056, device=DEV))
         mq.moe_grouped_gemm_mxfp4(b_q, b_s, plan, w, ws)
+    with pytest.raises(ValueError, match="K = 64"):
+        c_q, c_s = mq.quant_mxfp4(torch.zeros(4, 96, device=DEV))      # as many super-groups
+        mq.moe_grouped_gemm_mxfp4(c_q, c_s, plan, w, ws)
     with pytest.raises(ValueError, match="tiled"):
         mq.moe_grouped_gemm_mxfp4(a_q, a_s, plan, a_q, a_s)
     with pytest.raises(mq.MoeqError):
@@ -342,6 +345,32 @@ def test_few_layer_masked_experts():
     f.check(got)
     assert torch.equal(got["y"][0].cpu(), f.shared[0]) and (got["w"][0] == 0).all()
     assert got["w"][1].tolist() == [1.0, 0.0, 0.0]
+
+
+def test_few_layer_masked_experts_may_hold_anything():
+    f = Few(5, 4, 8, 96, 64, 30)
+    f.logits[:, 0] = float("-inf")
+    f.logits[2, 2:] = float("-inf")                # one expert left: masked ones fill its slots
+    clean = f.run()["y"].clone()
+    f.w13[1][0].fill_(255)                         # expert 0: every block a NaN
+    f.w2[1][0].fill_(255)
+    got = f.run()
+    assert (got["ids"][2] == 0).any() and torch.equal(got["y"], clean)
+    f.w13v[0] = f.w2v[0] = 0.0
+    f.check(got)
+
+
+@pytest.mark.parametrize("bits", [0x7FC00000, -0x400000, -1])          # NaNs of either sign
+def test_few_layer_nan_scores_stay_inside(bits):
+    f = Few(4, 3, 6, 64, 32, 31)
+    nan = torch.full((6,), bits, dtype=torch.int32).view(torch.float32)
+    clean = f.run(out={"ws": torch.full((1 << 16,), 255, dtype=torch.uint8, device=DEV)})
+    f.logits[1] = nan
+    f.logits[3, 2] = nan[0]
+    got = f.run(out={"ws": torch.full((1 << 16,), 255, dtype=torch.uint8, device=DEV)})
+    assert ((got["ids"] >= 0) & (got["ids"] < 6)).all()
+    for name in ("ids", "w", "y"):                  # the other tokens are as they were
+        assert torch.equal(got[name][[0, 2]], clean[name][[0, 2]]), name
 
 
 def test_few_layer_every_token_on_one_expert():

@@ -93,6 +93,7 @@ def test_grouped_gemm_refusals():
         assert call(**{name: at((1 << 20) + 8)}) == INVALID, name
     assert call(a_s=at((1 << 20) + 2)) == INVALID and call(plan=at((1 << 20) + 2)) == INVALID
     assert call(plan_bytes=pb - 4) == WORKSPACE
+    assert call(R=1 << 29, N=1 << 14, plan_bytes=1 << 40) == UNSUPPORTED   # too many workgroups
     assert call(R=0, a_q=N, w=N, out=N) == OK
 
 

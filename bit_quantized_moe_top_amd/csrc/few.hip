@@ -6,10 +6,11 @@
 //   few_down_kernel     o_j = W2 h_j;  y = sum_j w_j o_j (+ shared)
 //
 // Sums: W = e2m1 * 2^s converts exactly to bf16 (2 significant bits), products
-// and sums run in fp32 on v_mfma_f32_16x16x32_bf16.  h is rounded once to bf16,
-// the second product's operand type (2^-9 of each element, uncorrelated over the
-// I summands; the layer's 8-bit and 16-bit paths round h the same way).  o stays
-// fp32; y is rounded once.
+// and sums run in fp32 on v_mfma_f32_16x16x32_bf16.  h enters the second product as
+// the sum of two bf16 values, hi = bf16(h) and lo = bf16(h - hi), which keeps 16 of
+// its bits: the matrix units have the time (the weights are converted once for
+// both), and y is as close to the exact value as its one rounding to bf16 allows
+// (rounding h to bf16 alone made its error 1.5 times as large).  o stays fp32.
 //
 // Work units.  A workgroup belongs to one routed row r = t k + j and a run of
 // column units.  It routes all T tokens itself (gate/up; 4 T E bytes from L2), so
@@ -23,7 +24,19 @@
 // arrival counter per column unit; the one that arrives last has all T k rows of
 // its 32 columns and forms y in slot order j, so results do not depend on the
 // arrival order.  Nobody waits for anybody.  The gate/up kernel clears the
-// counters, so a call leaves no state that the next one needs.
+// counters, so a call leaves no state that the next one needs.  (The stores are
+// agent-scope atomic stores, written through to where every XCD sees them; the wave
+// waits for them before it counts, so a count that completes a unit stands for
+// finished stores.  A release fence instead would write back an XCD's whole L2 in
+// every workgroup.)
+//
+// Bound by HBM plus some 4 us per kernel that no load covers (launch, routing or
+// ids, first bytes; reduction, join).  4096 x 2048, top-6 of 256 experts, gate/up +
+// down in us, against the weights at the 6.28 TB/s of a pure read: one token 13.9 +
+// 8.5 (8.5 + 4.3), four tokens 37.5 + 20.7 (32.8 + 16.4), sixteen 105 + 70 (114 +
+// 57; some of the weights still lie in the memory-side cache).  On the way: routing
+// every token in every workgroup 55.9 (four tokens, gate/up) -> ranks instead of k
+// argmax rounds 53.4 -> unconditional LDS reads and no register spills 36.9.
 #include "front.hpp"
 #include "mx.hpp"
 
@@ -34,13 +47,16 @@ namespace {
 constexpr int kFewThreads = 256;
 constexpr int kFewMaxRows = 2 * kWave;        // routed rows: 16 tokens x 8 experts
 static_assert(kFewTokens * MOEQ_MAX_TOPK <= kFewMaxRows, "two ballots cover the routed rows");
-// Activation rows staged in LDS: at most four, in at most 17 KB (two rows of 4096
-// elements).  With more, fewer workgroups fit a CU for rows that are rarely there
-// (gate/up at 4096 x 2048, top-6 of 256 experts, four tokens, an earlier build:
-// 53.4 us with four rows, 49.4 us with two); an expert with more rows reads them
-// from memory.
-constexpr int kStageRows = 4, kStageBytes = 17 << 10;
+// Activation rows staged in LDS: at most four, in at most 17 KB for T <= 4 tokens
+// (two rows of 4096 elements, or of 2048 in two planes), 25 KB above.  More would
+// leave fewer workgroups on a CU for rows that are rarely there; an expert with more
+// rows reads them from memory.  4096 x 2048, top-6 of 256 experts, gate/up and down in
+// us with 17, 25 and 33 KB: four tokens 37.6, 20.8 / 38.1, 22.2 / 40.7, 24.6; sixteen
+// 108.2, 71.4 / 105.1, 70.2 / 107.9, 69.4.
+constexpr int kStageRows = 4;
+__host__ constexpr int few_stage_limit(int T) { return (T > 4 ? 25 : 17) << 10; }
 
+constexpr int kDppRowRor8 = 0x128;            // lane i of 16 takes lane (i + 8) % 16
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 
 __device__ __forceinline__ mx_v4f mfma_bf16(const uint4& w, const uint4& a, const mx_v4f& c) {
@@ -68,44 +84,57 @@ __device__ __forceinline__ FewRows find_rows(int e_lo, int e_hi, int R, int r, i
   return f;
 }
 
-// The activation rows of an expert, [n] rows of K bf16 elements of src (row i at
-// index rows[i]), padded in LDS to whole super-groups and 16 bytes (row_bytes).
+// The activation rows of an expert: row i is row rows[i] of src, kPlanes planes of
+// K bf16 elements each whose sum is the row's value.  In LDS plane p of row i lies at
+// (i kPlanes + p) * plane_bytes, padded to whole super-groups and 16 bytes.
+template <int kPlanes>
 struct FewStage {
   const uint16_t* src;
   const int* rows;
   uint8_t* lds;
-  int n, K, per_row, row_bytes;
+  int n, K, per_plane, plane_bytes;
   __device__ __forceinline__ FewStage(const uint16_t* src, const int* rows, uint8_t* lds, int K)
-      : src(src), rows(rows), lds(lds), n(0), K(K), per_row(mx_supers(K) * (kMxSuper / 8)),
-        row_bytes(per_row * 16 + 16) {}
-  // piece p (8 elements) of source row `row`; pieces past K are 0
-  __device__ __forceinline__ uint4 piece(int row, int p) const {
+      : src(src), rows(rows), lds(lds), n(0), K(K), per_plane(mx_supers(K) * (kMxSuper / 8)),
+        plane_bytes(per_plane * 16 + 16) {}
+  // piece p (8 elements) of a plane of source row `row`; pieces past K are 0
+  __device__ __forceinline__ uint4 piece(int row, int plane, int p) const {
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (p * 8 < K) v = *reinterpret_cast<const uint4*>(src + int64_t(row) * K + p * 8);
+    if (p * 8 < K)
+      v = *reinterpret_cast<const uint4*>(src + (int64_t(row) * kPlanes + plane) * K + p * 8);
     return v;
   }
-  __device__ __forceinline__ void put(int i, int p, const uint4& v) const {
-    *reinterpret_cast<uint4*>(lds + i * row_bytes + p * 16) = v;
+  __device__ __forceinline__ void put(int i, int plane, int p, const uint4& v) const {
+    *reinterpret_cast<uint4*>(lds + (i * kPlanes + plane) * plane_bytes + p * 16) = v;
+  }
+  // copies pieces first, first + kFewThreads, ... of row i's planes
+  __device__ __forceinline__ void copy(int i, int row, int first) const {
+#pragma unroll
+    for (int plane = 0; plane < kPlanes; ++plane)
+      for (int p = first; p < per_plane; p += kFewThreads) put(i, plane, p, piece(row, plane, p));
   }
 };
 
 // A row whose index is known ahead of the expert's others (the workgroup's own
 // row, which is activation row 0 when the workgroup owns its expert): its first
 // pieces are loaded at the top of the kernel and parked in LDS later.
-constexpr int kEarly = 2;                     // pieces per thread: rows of <= 4096 elements
+template <int kPlanes>
 struct EarlyRow {
-  uint4 v[kEarly];
-  __device__ __forceinline__ void load(const FewStage& st, int row, int tid) {
+  static constexpr int kEarly = 2 / kPlanes;  // pieces per thread and plane
+  uint4 v[kPlanes][kEarly];
+  __device__ __forceinline__ void load(const FewStage<kPlanes>& st, int row, int tid) {
 #pragma unroll
-    for (int i = 0; i < kEarly; ++i)
-      if (tid + i * kFewThreads < st.per_row) v[i] = st.piece(row, tid + i * kFewThreads);
+    for (int plane = 0; plane < kPlanes; ++plane)
+#pragma unroll
+      for (int i = 0; i < kEarly; ++i)
+        if (tid + i * kFewThreads < st.per_plane) v[plane][i] = st.piece(row, plane, tid + i * kFewThreads);
   }
-  __device__ __forceinline__ void store(const FewStage& st, int row, int tid) const {
+  __device__ __forceinline__ void store(const FewStage<kPlanes>& st, int row, int tid) const {
 #pragma unroll
-    for (int i = 0; i < kEarly; ++i)
-      if (tid + i * kFewThreads < st.per_row) st.put(0, tid + i * kFewThreads, v[i]);
-    for (int p = tid + kEarly * kFewThreads; p < st.per_row; p += kFewThreads)
-      st.put(0, p, st.piece(row, p));
+    for (int plane = 0; plane < kPlanes; ++plane)
+#pragma unroll
+      for (int i = 0; i < kEarly; ++i)
+        if (tid + i * kFewThreads < st.per_plane) st.put(0, plane, tid + i * kFewThreads, v[plane][i]);
+    st.copy(0, row, tid + kEarly * kFewThreads);
   }
 };
 
@@ -133,10 +162,11 @@ struct FewWeights {
 
 // acc += W A over one super-group: a lane's four steps take the activation
 // blocks 4 kb .. 4 kb + 3 of the super-group, 256 consecutive bytes at `act`.
-// kPartial: the row ends inside the super-group, `left` bytes on.
-template <bool kPartial>
-__device__ __forceinline__ void few_mac(const MxFrag (&f)[2], const uint8_t* act, int left,
-                                        mx_v4f (&acc)[2]) {
+// Further planes of the rows follow `plane` bytes apart.  kPartial: the row ends
+// inside the super-group, `left` bytes on.
+template <int kPlanes, bool kPartial>
+__device__ __forceinline__ void few_mac(const MxFrag (&f)[2], const uint8_t* act, int64_t plane,
+                                        int left, mx_v4f (&acc)[2]) {
   static_for<kMxSteps>([&](auto j) {
     float sc[2];                              // byte j of the scale dword in the exponent field
 #pragma unroll
@@ -144,12 +174,19 @@ __device__ __forceinline__ void few_mac(const MxFrag (&f)[2], const uint8_t* act
       sc[b] = u2f((j < 3 ? f[b].s << (j < 3 ? 23 - 8 * j : 0) : f[b].s >> 1) & 0x7F800000u);
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-      uint4 a = make_uint4(0u, 0u, 0u, 0u);
-      if (!kPartial || j * 64 < left) a = *reinterpret_cast<const uint4*>(act + j * 64 + m * 16);
+      uint4 a[kPlanes];
+#pragma unroll
+      for (int p = 0; p < kPlanes; ++p) {
+        a[p] = make_uint4(0u, 0u, 0u, 0u);
+        if (!kPartial || j * 64 < left)
+          a[p] = *reinterpret_cast<const uint4*>(act + p * plane + j * 64 + m * 16);
+      }
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         const uint32_t c = m == 0 ? f[b].c[j].x : m == 1 ? f[b].c[j].y : m == 2 ? f[b].c[j].z : f[b].c[j].w;
-        acc[b] = mfma_bf16(mx_bf16x8(c, sc[b]), a, acc[b]);
+        const uint4 wv = mx_bf16x8(c, sc[b]);
+#pragma unroll
+        for (int p = 0; p < kPlanes; ++p) acc[b] = mfma_bf16(wv, a[p], acc[b]);
       }
     }
   });
@@ -163,16 +200,23 @@ __device__ __forceinline__ void few_mac(const MxFrag (&f)[2], const uint8_t* act
 // multiplied; the first item's are already in `f0`.
 //
 // kStaged: the rows are in LDS; lanes past the last row read the last one (their
-// columns of the result are never used).  Otherwise they are read from memory.
-template <bool kStaged, typename WeightsT, typename DoneF>
-__device__ __forceinline__ void few_units(const WeightsT& wt, int u0, int u1, const FewStage& st,
+// columns of the result are never used).  Two planes then share one product: at
+// most kStageRows rows leave columns free, so the lanes of columns 8 .. 15 read the
+// second plane of rows 0 .. 7 and the two halves are added at the end.  Otherwise
+// (more rows) they are read from memory, plane by plane.
+template <bool kStaged, int kPlanes, typename WeightsT, typename DoneF>
+__device__ __forceinline__ void few_units(const WeightsT& wt, int u0, int u1, const FewStage<kPlanes>& st,
                                           MxFrag (&f0)[2], mx_v4f* red, DoneF&& done) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int q = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int row = min(lane & 15, st.n - 1), kb = lane >> 4;
-  const uint8_t* act = (kStaged ? st.lds + row * st.row_bytes
-                                : reinterpret_cast<const uint8_t*>(st.src + int64_t(st.rows[row]) * st.K)) +
-                       kb * 256;
+  constexpr bool kHalves = kStaged && kPlanes == 2;
+  static_assert(kStageRows <= 8 && kPlanes <= 2, "a half of the 16 columns per plane");
+  const int ln = lane & 15, kb = lane >> 4;
+  const int row = min(kHalves ? ln & 7 : ln, st.n - 1);
+  const uint8_t* act =
+      (kStaged ? st.lds + (row * kPlanes + (kHalves ? ln >> 3 : 0)) * st.plane_bytes
+               : reinterpret_cast<const uint8_t*>(st.src + int64_t(st.rows[row]) * kPlanes * st.K)) +
+      kb * 256;
   const int per_unit = max(wt.gn, 1);                   // a wave without K still joins the sums
   const int items = (u1 - u0) * per_unit;
   mx_v4f acc[2] = {mx_v4f{0.f, 0.f, 0.f, 0.f}, mx_v4f{0.f, 0.f, 0.f, 0.f}};
@@ -186,8 +230,8 @@ __device__ __forceinline__ void few_units(const WeightsT& wt, int u0, int u1, co
   auto step = [&](MxFrag (&f)[2]) {
     if (wt.gn > 0) {
       const int at = (wt.g0 + i) * 1024;
-      if (kStaged) few_mac<false>(f, act + at, 0, acc);
-      else few_mac<true>(f, act + at, st.K * 2 - at - kb * 256, acc);
+      if (kStaged) few_mac<1, false>(f, act + at, 0, 0, acc);
+      else few_mac<kPlanes, true>(f, act + at, int64_t(st.K) * 2, st.K * 2 - at - kb * 256, acc);
     }
     if (++i < per_unit) return;
     // one half of red per unit parity: a unit's sums are read before the barrier
@@ -203,6 +247,12 @@ __device__ __forceinline__ void few_units(const WeightsT& wt, int u0, int u1, co
       for (int j = 0; j < 2; ++j)
         acc[j] = acc[j] + (half[j * kWave + lane] +
                            (half[(2 + j) * kWave + lane] + half[(4 + j) * kWave + lane]));
+      if (kHalves) {                                    // column n + 8 to column n
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[j][v] += dpp<kDppRowRor8>(acc[j][v], acc[j][v]);
+      }
       done(u, acc);
     }
     acc[0] = acc[1] = mx_v4f{0.f, 0.f, 0.f, 0.f};
@@ -232,13 +282,12 @@ __device__ __forceinline__ void few_units(const WeightsT& wt, int u0, int u1, co
 }
 
 // Stages the rows after row 0 (which is in LDS) if all fit, and runs the units.
-template <typename WeightsT, typename DoneF>
-__device__ __forceinline__ void few_run(const WeightsT& wt, int u0, int u1, const FewStage& st,
+template <int kPlanes, typename WeightsT, typename DoneF>
+__device__ __forceinline__ void few_run(const WeightsT& wt, int u0, int u1, const FewStage<kPlanes>& st,
                                         int stage_rows, MxFrag (&f0)[2], mx_v4f* red, DoneF&& done) {
   if (st.n <= stage_rows) {
     if (st.n > 1) {
-      for (int i = 1; i < st.n; ++i)
-        for (int p = threadIdx.x; p < st.per_row; p += kFewThreads) st.put(i, p, st.piece(st.rows[i], p));
+      for (int i = 1; i < st.n; ++i) st.copy(i, st.rows[i], threadIdx.x);
       lds_barrier();
     }
     few_units<true>(wt, u0, u1, st, f0, red, done);
@@ -341,8 +390,8 @@ few_gate_up_kernel(const float* logits, const float* bias, int T, int E, int k, 
   // own its expert has read one item in vain.
   Scores<NS> own, mine[kMine];
   own.load(logits + int64_t(t) * E, bias, E, lane);
-  FewStage st(x, tokens, lds, H);
-  EarlyRow early;
+  FewStage<1> st(x, tokens, lds, H);
+  EarlyRow<1> early;
   if (stage_rows > 0) early.load(st, t, tid);
 #pragma unroll
   for (int i = 0; i < kMine; ++i)
@@ -375,7 +424,17 @@ few_gate_up_kernel(const float* logits, const float* bias, int T, int E, int k, 
   st.n = n;
   const int ln = lane & 15, kb = lane >> 4;
   auto done = [&](int u, const mx_v4f (&v)[2]) {
-    if (ln < n) store4(h, 0, int64_t(rows[ln]) * I + 16 * u + 4 * kb, silu_mul4(v[0], v[1]));
+    if (ln >= n) return;
+    const mx_v4f hv = silu_mul4(v[0], v[1]);
+    mx_v4f hi, lo;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      hi[c] = static_cast<float>(static_cast<__bf16>(hv[c]));
+      lo[c] = fabsf(hi[c]) < INFINITY ? hv[c] - hi[c] : 0.0f;   // (no inf - inf)
+    }
+    const int64_t at = int64_t(rows[ln]) * 2 * I + 16 * u + 4 * kb;
+    store4(h, 0, at, hi);
+    store4(h, 0, at + I, lo);
   };
   few_run(wt, u0, u1, st, stage_rows, f0, red, done);
 }
@@ -407,8 +466,8 @@ few_down_kernel(const int32_t* ids, const float* topk_w, const uint16_t* h, int 
   const int r = blockIdx.x / runs;
   const int u0 = (blockIdx.x - r * runs) * units_per_wg, u1 = min(u0 + units_per_wg, units);
   const int e_lo = ids[min(lane, R - 1)], e_hi = ids[min(lane + kWave, R - 1)];
-  FewStage st(h, rows, lds, I);
-  EarlyRow early;
+  FewStage<2> st(h, rows, lds, I);
+  EarlyRow<2> early;
   if (stage_rows > 0) early.load(st, r, tid);
   // (ids come from the first kernel of the call; clamped all the same)
   const int e = min(max(__builtin_amdgcn_readfirstlane(ids[r]), 0), E - 1);
@@ -488,26 +547,26 @@ few_down_kernel(const int32_t* ids, const float* topk_w, const uint16_t* h, int 
 
 size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
-// rows staged in LDS for rows of K elements, and the bytes they take
-int few_stage_rows(int T, int K) {
-  const int row_bytes = mx_supers(K) * (kMxSuper * 2) + 16;
-  const int fit = kStageBytes / row_bytes;
-  int n = T < kStageRows ? T : kStageRows;
+// rows staged in LDS for rows of `planes` planes of K elements, and their bytes
+int few_row_bytes(int planes, int K) { return planes * (mx_supers(K) * (kMxSuper * 2) + 16); }
+int few_stage_rows(int T, int planes, int K) {
+  const int fit = few_stage_limit(T) / few_row_bytes(planes, K);
+  const int n = T < kStageRows ? T : kStageRows;
   return n < fit ? n : fit;
 }
-unsigned few_stage_bytes(int T, int K) {
-  return unsigned(few_stage_rows(T, K) * (mx_supers(K) * (kMxSuper * 2) + 16));
+unsigned few_stage_bytes(int T, int planes, int K) {
+  return unsigned(few_stage_rows(T, planes, K) * few_row_bytes(planes, K));
 }
 
 // Column units per workgroup.  One unit each lets the dispatcher balance the CUs,
-// several spread the routing and the joins over more weights; the launch is to
-// hold about 3072 workgroups (four per CU, three rounds).  Measured at 4096 x
-// 2048, top-6 of 256 (gate/up, down; us): T = 1: 13.8, 8.3 with one unit, 14.8,
-// 10.2 with two; T = 4: 36.9, 20.6 with one, 37.5, 22.2 with two, 37.9, 24.6 with
-// four; T = 16: 142.5, 76.9 with one, 115.3, 67.8 with two, 105.8, 66.8 with four,
-// 112.5, 76.3 with six.
-int few_units_per_wg(int R, int units) {
-  const int64_t n = int64_t(R) * units / 3072;
+// several spread the routing and the joins over more weights; a launch is to hold
+// about `launch` workgroups (some rounds of the four that fit a CU).  Measured at 4096
+// x 2048, top-6 of 256 experts (gate/up, down; us): one token 13.8, 8.3 with one unit,
+// 14.8, 10.2 with two; four 36.9, 20.6 with one, 37.5, 22.2 with two, 37.9, 24.6 with
+// four; sixteen 142.5, 83.0 with one, 115.3, 71.8 with two, 110.6, 70.6 with three,
+// 105.8, 73.4 with four, 112.5, 84.2 with six.
+int few_units_per_wg(int R, int units, int launch) {
+  const int64_t n = int64_t(R) * units / launch;
   return n < 1 ? 1 : n > 4 ? 4 : int(n);
 }
 
@@ -515,7 +574,7 @@ int few_units_per_wg(int R, int units) {
 
 size_t few_ws_bytes(int T, int k, int H, int I) {
   const size_t R = size_t(T) * k;
-  return align256(size_t(H / 32) * 4) + align256(R * I * 2) + align256(R * H * 4);
+  return align256(size_t(H / 32) * 4) + align256(R * I * 4) + align256(R * H * 4);
 }
 
 hipError_t launch_layer_mxfp4_few(const float* logits, const float* bias, int T, int E, int k,
@@ -528,20 +587,20 @@ hipError_t launch_layer_mxfp4_few(const float* logits, const float* bias, int T,
   uint8_t* base = static_cast<uint8_t*>(ws);
   uint32_t* counters = reinterpret_cast<uint32_t*>(base);
   uint16_t* h = reinterpret_cast<uint16_t*>(base + align256(size_t(H / 32) * 4));
-  float* o = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(h) + align256(size_t(R) * I * 2));
-  const int upw1 = few_units_per_wg(R, I / 16), upw2 = few_units_per_wg(R, H / 32);
+  float* o = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(h) + align256(size_t(R) * I * 4));
+  const int upw1 = few_units_per_wg(R, I / 16, 3072), upw2 = few_units_per_wg(R, H / 32, 4096);
   const int runs1 = (I / 16 + upw1 - 1) / upw1, runs2 = (H / 32 + upw2 - 1) / upw2;
   with_route_slots(E, [&](auto ns) {
     hipLaunchKernelGGL((few_gate_up_kernel<decltype(ns)::value>), dim3(unsigned(R * runs1)),
-                       dim3(kFewThreads), few_stage_bytes(T, H), stream, logits, bias, T, E, k,
-                       renormalize, x, H, w13, ws13, I, upw1, few_stage_rows(T, H), ids, topk_w, h,
+                       dim3(kFewThreads), few_stage_bytes(T, 1, H), stream, logits, bias, T, E, k,
+                       renormalize, x, H, w13, ws13, I, upw1, few_stage_rows(T, 1, H), ids, topk_w, h,
                        counters, H / 32);
   });
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   hipLaunchKernelGGL(few_down_kernel, dim3(unsigned(R * runs2)), dim3(kFewThreads),
-                     few_stage_bytes(T, I), stream, ids, topk_w, h, T, E, k, w2, ws2, H, I, upw2,
-                     few_stage_rows(T, I), o, counters, shared, y);
+                     few_stage_bytes(T, 2, I), stream, ids, topk_w, h, T, E, k, w2, ws2, H, I, upw2,
+                     few_stage_rows(T, 2, I), o, counters, shared, y);
   return hipGetLastError();
 }
 

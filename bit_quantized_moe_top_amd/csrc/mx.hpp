@@ -126,14 +126,18 @@ __device__ __forceinline__ MxFrag load_weights(const uint8_t* w, const uint8_t* 
   return f;
 }
 
+// two fp32 values as bf16 (nearest even; infinities and NaNs kept)
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  return __builtin_bit_cast(uint32_t, mx_bf2{static_cast<__bf16>(a), static_cast<__bf16>(b)});
+}
+
 // four consecutive output columns of one row: bf16 (rounded to nearest even) or fp32
 __device__ __forceinline__ void store4(void* out, int out_f32, int64_t at, const mx_v4f& v) {
   if (out_f32) {
     *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = make_float4(v[0], v[1], v[2], v[3]);
   } else {
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) =
-        make_uint2(uint32_t(f32_to_bf16(v[0])) | (uint32_t(f32_to_bf16(v[1])) << 16),
-                   uint32_t(f32_to_bf16(v[2])) | (uint32_t(f32_to_bf16(v[3])) << 16));
+        make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
   }
 }
 

@@ -4,10 +4,19 @@
 // row(p) = p (activations in plan order) or sorted_rows[p] / topk (activations in
 // token order, read in place: no gathered copy of the k rows per token).
 //
-// K-split kernel: one workgroup per unit (plan tile of <= 64 rows, two 16-row
-// weight blocks -- 32 output columns, or 16 gate rows with their 16 up rows);
-// wave q sweeps the super-groups of K quarter q, the four partial sums meet in
-// LDS in the fixed order s0 + (s1 + (s2 + s3)).
+// Two kernels (which one: mx_shape below):
+//  * K-split units, for few rows per expert: one workgroup per (plan tile of <= 64
+//    rows, two 16-row weight blocks -- 32 output columns, or 16 gate rows with
+//    their 16 up rows); wave q sweeps the super-groups of K quarter q, the four
+//    partial sums meet in LDS in the fixed order s0 + (s1 + (s2 + s3)).  Every load
+//    goes straight to registers.  Bound by HBM: 4 tokens, top-6 of 256 experts,
+//    4096 x 4096 gate/up in 33.6 us, 6.1 TB/s of weights (a pure read: 6.28).
+//  * Tiles, for many: 64 plan rows x 64 CB weight rows, activations shared through
+//    LDS, weights straight to registers.  2048 tokens, top-6 of 256, 4096 x 4096
+//    gate/up in 386 us, 6.0 TB/s of HBM (95% of a pure read); Zipf-popular experts,
+//    4096 x 2048 down 237 us, 5.3 TB/s (equal items per XCD, but not equal weight
+//    streams); one expert of 8192 rows 2.5 PFLOP/s, bound by the weights' way from
+//    L2 (64 B per clock and CU feed a 64-row tile at the matrix rate).
 #include "front.hpp"
 #include "mx.hpp"
 
@@ -151,14 +160,25 @@ __device__ __forceinline__ TileItem tile_item(const PlanView& pv, int E, int R, 
   return it;
 }
 
-// LDS position of 16-byte piece p of an activation row: pieces are XOR-swizzled
-// so that the 32 lanes that LDS serves together (16 rows, two values of kb: bit 2
-// of p) read 32 different 16-byte banks
+// LDS position of 16-byte piece p of an activation row: pieces are XOR-swizzled so
+// that the 16 rows of two values of kb (bit 2 of p) read 32 different 16-byte units
+// mod 512 bytes.  (Counters still show 4.6 conflict cycles per read; a swizzle with
+// half as many measured the same time on every shape.)
 __device__ __forceinline__ int swizzle(int row, int p) {
   const int m = (row & 15) >> 1;
   return p ^ ((m & 3) | ((m & 4) << 1));
 }
 
+// One workgroup per work item; XCD x takes a contiguous run of them (workgroups go
+// to the XCDs round-robin), so the row tiles that read one weight slice run side by
+// side on one XCD and share it through its L2.  Measured and not kept (gate/up of
+// 2048 tokens, 390 us): N-tiles dealt over the XCDs, each reading a share of every
+// expert, 415; persistent workgroups whose loads run across items, 403.
+//
+// A wave keeps one super-group of its CB weight blocks in registers (16 KB in flight
+// for CB = 4) and reloads a step's registers as soon as its products are issued.
+// Two super-groups (CB = 2) cost the third wave per SIMD: 18.6 us against 14.4 at
+// 2331 rows of 1440, 12 experts of 1504 columns.
 template <int EPI, int CB>
 __global__ void __launch_bounds__(kThreads, 2)
 gemm_mx_tile_kernel(const uint8_t* a_q, const uint8_t* a_s, int a_topk, const int32_t* plan, int E,

@@ -34,24 +34,25 @@ _SIGNATURES = {
                                  _P, _P, _SZ, _P]),
 }
 MX_SYMBOLS = tuple(_SIGNATURES)
+_CALL = {}
 for _name, (_res, _args) in _SIGNATURES.items():
-    _fn = getattr(lib, _name)
-    _fn.restype, _fn.argtypes = _res, _args
+    _CALL[_name] = getattr(lib, _name)
+    _CALL[_name].restype, _CALL[_name].argtypes = _res, _args
 
 
 _F = {torch.bfloat16: MOEQ_BF16, torch.float32: MOEQ_F32}
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def _launch(name: str, index: int, *args):
     """Calls lib.name(*args, stream) on device `index` and its current stream.  (A decode step's
     calls take a few microseconds of GPU time, so this path creates no stream or pointer objects.)"""
-    fn = getattr(lib, name)
-    if index == torch.cuda.current_device():
-        status = fn(*args, _raw_stream(index))
+    if index == _current_device():
+        status = _CALL[name](*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
-            status = fn(*args, _raw_stream(index))
+            status = _CALL[name](*args, _raw_stream(index))
     if status:
         _check(name, status)
 

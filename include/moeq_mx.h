@@ -104,9 +104,9 @@ size_t moe_layer_mxfp4_few_ws_size(int T, int k, int H, int I);
  * moe_layer_mxfp4_few -- a whole expert layer for T <= MOEQ_FEW_TOKENS tokens in
  * two kernels, with MXFP4 weights and bf16 activations:
  *   topk_ids, topk_w    as moe_route_topk (logits, bias, k, renormalize)
- *   h_j = silu(Wg_e x_t) * (Wu_e x_t),  e = topk_ids[t, j]   (rounded to bf16)
+ *   h_j = silu(Wg_e x_t) * (Wu_e x_t),  e = topk_ids[t, j]   (16 bits of it kept)
  *   y_t = bf16( sum_j topk_w[t, j] * (W2_e h_j) + shared_t )  (fp32 sums in slot order)
- * Nothing is quantized but the weights.  Scores of -inf mark masked experts and
+ * Nothing is quantized but the weights; y is rounded once.  Scores of -inf mark masked experts and
  * get weight 0; a token whose k best scores are all -inf gets weights 0 (y_t =
  * shared_t, or 0).  An expert of weight 0 adds nothing, whatever its weights hold.
  * Other scores are finite (with a NaN score the ids stay inside [0, E) and the

@@ -21,6 +21,7 @@ __all__ = ["MX_BLOCK", "FEW_TOKENS", "MX_SYMBOLS", "quant_mxfp4", "dequant_mxfp4
 MX_BLOCK = 32                # elements per scale
 FEW_TOKENS = 16              # MOEQ_FEW_TOKENS
 _SUPER = 512                 # K of one super-group of the tiled order
+_INT_MAX = 0x7FFFFFFF
 
 _P, _I, _I64, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
 # name -> (restype, argtypes); the exact list of entry points in include/moeq_mx.h
@@ -64,19 +65,18 @@ def _float_dtype(dtype, name: str) -> int:
     return dt
 
 
-def _tensor(t: torch.Tensor, name: str, dtype, ndim: int, index: int = -1) -> int:
-    """Checks a contiguous device tensor of ndim dims, on device `index` if one is given; returns
-    its device's index."""
-    try:
-        i = t.get_device()
-        if t.dtype is dtype and t.dim() == ndim and t.is_contiguous() and i >= 0 and \
-                (i == index or index < 0):
-            return i
-    except AttributeError:
-        raise TypeError(f"{name} must be a tensor") from None
+def _tensor(t: torch.Tensor, name: str, dtype, ndim: int = 0, index: int = -1) -> int:
+    """Checks a contiguous device tensor (of ndim dims, on device `index`, if given); returns its
+    device's index."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    i = t.get_device()
+    if t.dtype is dtype and (t.dim() == ndim or not ndim) and t.is_contiguous() and i >= 0 and \
+            (i == index or index < 0):
+        return i
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != ndim:
+    if ndim and t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dims, got {t.dim()}")
     if i < 0:
         raise ValueError(f"{name} must be a device tensor")
@@ -95,7 +95,7 @@ def _output(t: Optional[torch.Tensor], name: str, shape: tuple, dtype, index: in
     return t
 
 
-def _codes(q: torch.Tensor, scale: torch.Tensor, name: str, ndim: int) -> Tuple[int, int]:
+def _codes(q: torch.Tensor, scale: torch.Tensor, name: str, ndim: int = 0) -> Tuple[int, int]:
     """K and the device of MXFP4 rows: codes [..., K/2], scales [..., K/32]."""
     index = _tensor(q, name, torch.uint8, ndim)
     _tensor(scale, name + " scales", torch.uint8, ndim, index)
@@ -103,6 +103,8 @@ def _codes(q: torch.Tensor, scale: torch.Tensor, name: str, ndim: int) -> Tuple[
     if not qs or qs[:-1] != ss[:-1] or qs[-1] != 16 * ss[-1]:
         raise ValueError(f"{name}: codes [..., K/2] and scales [..., K/32] do not match: "
                          f"{tuple(qs)}, {tuple(ss)}")
+    if qs[-1] > _INT_MAX // 2:
+        raise ValueError(f"{name}: rows of {2 * qs[-1]} elements are too long")
     return 2 * qs[-1], index
 
 
@@ -110,6 +112,8 @@ def quant_mxfp4(x: torch.Tensor, q: Optional[torch.Tensor] = None,
                 scale: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """x [..., K] fp32/bf16 -> (codes [..., K/2], scales [..., K/32]).  x is contiguous, or a
     2-D tensor whose rows are (columns of a wider matrix)."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a tensor")
     dt = _float_dtype(x.dtype, "x")
     dev = x.get_device()
     if dev < 0:
@@ -118,6 +122,8 @@ def quant_mxfp4(x: torch.Tensor, q: Optional[torch.Tensor] = None,
     if not shape:
         raise ValueError("x must have rows")
     K = shape[-1]
+    if K > _INT_MAX:
+        raise ValueError(f"x: rows of {K} elements are too long")
     if x.is_contiguous():
         ld = K
     elif len(shape) == 2 and x.stride(1) == 1 and x.stride(0) >= K:
@@ -134,7 +140,7 @@ def quant_mxfp4(x: torch.Tensor, q: Optional[torch.Tensor] = None,
 def dequant_mxfp4(q: torch.Tensor, scale: torch.Tensor, out: Optional[torch.Tensor] = None,
                   dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """The values [..., K] of MXFP4 rows, exact, in `dtype` (or out's)."""
-    K, dev = _codes(q, scale, "q", q.dim())
+    K, dev = _codes(q, scale, "q")
     dtype = dtype if out is None else out.dtype
     dt = _float_dtype(dtype, "out")
     out = _output(out, "out", q.shape[:-1] + (K,), dtype, dev)
@@ -187,6 +193,8 @@ def moe_grouped_gemm_mxfp4(a_q: torch.Tensor, a_s: torch.Tensor, plan: torch.Ten
         raise ValueError(f"topk must be 0 .. {MAX_TOPK}")
     E, N = _tiled(w, w_scale, K, "w", dev)
     R = a_q.shape[0] * (topk or 1)
+    if R > _INT_MAX:
+        raise ValueError(f"{R} rows are too many")
     _tensor(plan, "plan", torch.int32, 1, dev)
     _plan_shape_ok(plan, E, R)
     dtype = out_dtype if out is None else out.dtype

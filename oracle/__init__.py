@@ -10,6 +10,7 @@ Modules:
   formats -- OCP FP8 E4M3, bfloat16 and INT4 storage formats (encode/decode/pack)
   layer   -- routing, per-token FP8 quantization, permutation, grouped GEMMs,
              SiLU gating, combine, shared experts and the whole layer
+  mx      -- MXFP4: quantization, values, tiled weights, products, few-token layer
 
 Pinning: every function here is checked by ``tests/test_oracle_*.py`` against
 something other than itself (library casts, brute force, closed forms,

@@ -109,6 +109,32 @@ def test_quant_empty_and_shapes():
     assert torch.equal(q.reshape(6, 32), mq.quant_mxfp4(x.reshape(6, 64))[0])
 
 
+def test_rows_past_32_bits_are_refused():
+    q = torch.empty(1 << 30, dtype=torch.uint8, device=DEV)
+    s = torch.empty(1 << 26, dtype=torch.uint8, device=DEV)
+    with pytest.raises(ValueError, match="too long"):
+        mq.dequant_mxfp4(q, s)
+    with pytest.raises(ValueError, match="too many"):
+        a_q, a_s = q.view(-1, 16)[:1 << 26], s[:1 << 26].view(-1, 1)
+        w = torch.empty(1, 2, 1, 4, 64, 16, dtype=torch.uint8, device=DEV)
+        ws = torch.empty(1, 2, 1, 64, 4, dtype=torch.uint8, device=DEV)
+        plan = torch.empty(64, dtype=torch.int32, device=DEV)
+        mq.moe_grouped_gemm_mxfp4(a_q.repeat(5, 1), a_s.repeat(5, 1), plan, w, ws, topk=8)
+
+
+def test_quant_past_32_bits():
+    """2^31 + 64 elements: the last block lies past 32-bit element offsets."""
+    n = (1 << 31) + 64
+    x = torch.zeros(n // 32, 32, dtype=torch.bfloat16, device=DEV)
+    x[-1], x[-2], x[0] = 3.0, -0.5, 1.0
+    q, s = mq.quant_mxfp4(x)
+    assert s[-1].item() == 126 and s[-2].item() == 124 and s[0].item() == 125
+    assert s[1:-2].max().item() == 0 and q[1:-2].max().item() == 0
+    v = mq.dequant_mxfp4(q, s)
+    assert torch.equal(v[-2:], x[-2:]) and torch.equal(v[:2], x[:2])
+    assert int((v != 0).sum()) == 96
+
+
 @pytest.mark.parametrize("E,N,K", [(1, 16, 32), (3, 32, 512), (2, 48, 544), (2, 64, 1440), (1, 16, 4096)])
 def test_tile_every_byte(E, N, K):
     g = gen(E + N + K)
@@ -312,6 +338,9 @@ FEW_CASES = [
     (16, 1, 2, 1440, 64, False, True), (7, 4, 40, 2080, 320, True, True),
     (3, 2, 4, 4096, 2048, False, False), (2, 2, 3, 8192, 64, False, False),
     (6, 2, 3, 64, 4640, False, True),
+    # rows too long for LDS: one row staged, none (of x, of h)
+    (5, 2, 3, 64, 4640, False, False), (3, 2, 3, 64, 4640, False, False),
+    (2, 1, 2, 16896, 32, False, True),
 ]
 
 

@@ -13,11 +13,12 @@
 // (rounding h to bf16 alone made its error 1.5 times as large).  o stays fp32.
 //
 // Work units.  A workgroup belongs to one routed row r = t k + j and a run of
-// column units.  It routes all T tokens itself (gate/up; 4 T E bytes from L2), so
-// no launch is spent on routing, then finds with two ballots which rows share its
-// row's expert: the lowest of them owns the expert and computes all of them (an
-// expert has at most one row per token, so at most 16: one 16-column MFMA block),
-// the others' workgroups leave at once.  No plan is built or read.
+// column units.  In the gate/up kernel it finds its row's expert and the other
+// tokens' rows of that expert from the scores themselves (4 T E bytes, from L2), so
+// no launch is spent on routing; in the down kernel from the ids the first wrote.
+// The lowest row of an expert owns it and computes all of them (at most one per
+// token, so at most 16: one 16-column MFMA block); the other rows' workgroups leave
+// at once.  No plan is built or read.
 //
 // Joining the experts' outputs without a third launch: the down kernel's
 // workgroups store their fp32 o columns past the caches, then count up one
@@ -54,7 +55,7 @@ static_assert(kFewTokens * MOEQ_MAX_TOPK <= kFewMaxRows, "two ballots cover the 
 // us with 17, 25 and 33 KB: four tokens 37.6, 20.8 / 38.1, 22.2 / 40.7, 24.6; sixteen
 // 108.2, 71.4 / 105.1, 70.2 / 107.9, 69.4.
 constexpr int kStageRows = 4;
-__host__ constexpr int few_stage_limit(int T) { return (T > 4 ? 25 : 17) << 10; }
+constexpr int few_stage_limit(int T) { return (T > 4 ? 25 : 17) << 10; }
 
 constexpr int kDppRowRor8 = 0x128;            // lane i of 16 takes lane (i + 8) % 16
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
@@ -70,17 +71,20 @@ struct FewRows {
   int n;
   bool owner;
 };
+// (ids of one token differ, so there are at most kFewTokens; the bound keeps ids that
+// something else wrote from leaving the array)
 __device__ __forceinline__ FewRows find_rows(int e_lo, int e_hi, int R, int r, int lane, int* rows) {
   const int e = r < kWave ? readlane(e_lo, r & 63) : readlane(e_hi, r & 63);
   const uint64_t lo = __ballot(lane < R && e_lo == e);
   const uint64_t hi = __ballot(lane + kWave < R && e_hi == e);
   FewRows f;
-  f.n = __popcll(lo) + __popcll(hi);
+  f.n = min(__popcll(lo) + __popcll(hi), kFewTokens);
   f.owner = (lo ? __ffsll(static_cast<unsigned long long>(lo)) - 1
                 : kWave + __ffsll(static_cast<unsigned long long>(hi)) - 1) == r;
   const uint64_t below = (uint64_t(1) << lane) - 1;
-  if (lo >> lane & 1) rows[__popcll(lo & below)] = lane;
-  if (hi >> lane & 1) rows[__popcll(lo) + __popcll(hi & below)] = lane + kWave;
+  const int at_lo = __popcll(lo & below), at_hi = __popcll(lo) + __popcll(hi & below);
+  if ((lo >> lane & 1) && at_lo < kFewTokens) rows[at_lo] = lane;
+  if ((hi >> lane & 1) && at_hi < kFewTokens) rows[at_hi] = lane + kWave;
   return f;
 }
 
@@ -366,19 +370,15 @@ few_gate_up_kernel(const float* logits, const float* bias, int T, int E, int k, 
   const int u0 = run * units_per_wg, u1 = min(u0 + units_per_wg, units);
   const int t = r / k, j = r - t * k;
 
-  // one workgroup per token writes its routing
+  // one workgroup per token writes its weights
   constexpr int kWaves = kFewThreads / kWave, kMine = kFewTokens / kWaves;
   if (run == 0 && j == 0 && wave == kWaves - 1) {
     float w;
-    const int id = min(
-        route_token_values<NS>(logits + int64_t(t) * E, bias, E, k, renormalize, lane, w), E - 1);
-    const int best = readlane(id, 0);
+    const int id = route_token_values<NS>(logits + int64_t(t) * E, bias, E, k, renormalize, lane, w);
+    const int best = min(readlane(id, 0), E - 1);        // (no candidate: all scores NaN)
     const float s0 = logits[int64_t(t) * E + best] + (bias ? bias[best] : 0.0f);
-    if (lane < k) {
-      ids[t * k + lane] = id;
-      // a token whose best score is -inf has no weights (0/0): it gets zeros
-      topk_w[t * k + lane] = s0 == -INFINITY ? 0.0f : w;
-    }
+    // a token whose best score is -inf has no weights (0/0): it gets zeros
+    if (lane < k) topk_w[t * k + lane] = s0 == -INFINITY ? 0.0f : w;
   }
 
   // Routing.  The row's expert is the j-th best of its token (each wave finds it);
@@ -397,6 +397,7 @@ few_gate_up_kernel(const float* logits, const float* bias, int T, int E, int k, 
   for (int i = 0; i < kMine; ++i)
     if (wave + i * kWaves < T) mine[i].load(logits + int64_t(wave + i * kWaves) * E, bias, E, lane);
   const int e = own.at_rank(j, lane);
+  if (run == 0 && tid == 0) ids[r] = e;
   auto blk = [I](int u, int b) { return u + b * (I / 16); };
   const FewWeights<decltype(blk)> wt(w13, ws13, e, (2 * I) / 16, H, wave, blk);
   MxFrag f0[2];

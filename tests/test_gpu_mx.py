@@ -403,6 +403,20 @@ def test_few_layer_nan_scores_stay_inside(bits):
         assert torch.equal(got[name][[0, 2]], clean[name][[0, 2]]), name
 
 
+@pytest.mark.parametrize("bits", [0x7FC00000, -1])
+def test_few_layer_nan_token_among_sixteen(bits):
+    """A token without a candidate must not crowd the experts that the others share."""
+    f = Few(16, 8, 9, 96, 64, 32)
+    f.logits[:, 8] = 20.0                           # every token's first choice is the last expert
+    clean = f.run(out={"ws": torch.full((1 << 18,), 255, dtype=torch.uint8, device=DEV)})
+    f.logits[3] = torch.full((9,), bits, dtype=torch.int32).view(torch.float32)
+    got = f.run(out={"ws": torch.full((1 << 18,), 255, dtype=torch.uint8, device=DEV)})
+    assert sorted(set(got["ids"][3].tolist())) == sorted(got["ids"][3].tolist())
+    others = [t for t in range(16) if t != 3]
+    for name in ("ids", "w", "y"):
+        assert torch.equal(got[name][others], clean[name][others]), name
+
+
 def test_few_layer_every_token_on_one_expert():
     f = Few(16, 2, 6, 544, 96, 8)
     f.logits[:, 4] = 9.0

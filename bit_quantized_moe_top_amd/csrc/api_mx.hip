@@ -2,6 +2,7 @@
 // before any HIP call, the device check, and the launches on the caller's stream.
 #include "../../include/moeq_mx.h"
 #include "api.hpp"
+#include "mx_kernels.hpp"
 
 using moeq::aligned16;
 using moeq::aligned_to;

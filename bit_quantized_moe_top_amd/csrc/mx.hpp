@@ -24,6 +24,7 @@
 #pragma once
 
 #include "gemm.hpp"
+#include "mx_kernels.hpp"
 
 namespace moeq {
 

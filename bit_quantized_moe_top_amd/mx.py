@@ -100,12 +100,15 @@ def _codes(q: torch.Tensor, scale: torch.Tensor, name: str, ndim: int = 0) -> Tu
     index = _tensor(q, name, torch.uint8, ndim)
     _tensor(scale, name + " scales", torch.uint8, ndim, index)
     qs, ss = q.shape, scale.shape
-    if not qs or qs[:-1] != ss[:-1] or qs[-1] != 16 * ss[-1]:
+    n = len(qs)
+    if (qs[0] != ss[0] or len(ss) != 2 or qs[1] != 16 * ss[1]) if n == 2 else \
+            (not n or qs[:-1] != ss[:-1] or qs[-1] != 16 * ss[-1]):
         raise ValueError(f"{name}: codes [..., K/2] and scales [..., K/32] do not match: "
                          f"{tuple(qs)}, {tuple(ss)}")
-    if qs[-1] > _INT_MAX // 2:
-        raise ValueError(f"{name}: rows of {2 * qs[-1]} elements are too long")
-    return 2 * qs[-1], index
+    half = qs[n - 1]
+    if half > _INT_MAX // 2:
+        raise ValueError(f"{name}: rows of {2 * half} elements are too long")
+    return 2 * half, index
 
 
 def quant_mxfp4(x: torch.Tensor, q: Optional[torch.Tensor] = None,
@@ -172,8 +175,9 @@ def _tiled(w: torch.Tensor, ws: torch.Tensor, K: int, name: str, dev: int) -> Tu
                          "(tile_mxfp4_weights)")
     _tensor(w, name, torch.uint8, 6, dev)
     _tensor(ws, name + " scales", torch.uint8, 5, dev)
-    E, nb, G, *lanes = w.shape
-    if lanes != [4, 64, 16] or G != (K + _SUPER - 1) // _SUPER or ws.shape != (E, nb, G, 64, 4):
+    E, nb, G, steps, lanes, piece = w.shape
+    if (steps, lanes, piece) != (4, 64, 16) or G != (K + _SUPER - 1) // _SUPER or \
+            ws.shape != (E, nb, G, 64, 4):
         raise ValueError(f"{name} does not hold tiled weights of K = {K} with their scales: "
                          f"{tuple(w.shape)}, {tuple(ws.shape)}")
     if getattr(w, "_moeq_k", K) != K:

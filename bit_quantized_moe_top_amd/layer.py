@@ -261,7 +261,10 @@ class MxMoELayer(MoELayer):
         self.w2, self.s2 = tile_mxfp4_weights(*quant_mxfp4(w2))
 
     def buffers(self, T: int) -> dict:
-        b = self._bufs.get(T)
+        # the shared experts' width is part of the key: set_shared may come after a call, and the
+        # earlier buffers stay, since a captured graph may hold them
+        S = 0 if self.ws13 is None else self.ws2.shape[1]
+        b = self._bufs.get((T, S))
         if b is None:
             H, I, E, k, d = self.H, self.I, self.E, self.k, self.device
             R = T * k
@@ -281,8 +284,8 @@ class MxMoELayer(MoELayer):
                 "h_q": u8(R, I // 2), "h_s": u8(R, I // 32), "o": bf16(R, H), "y": bf16(T, H),
             }
             if self.ws13 is not None:
-                b["sh_h"], b["shared"] = bf16(T, self.ws2.shape[1]), bf16(T, H)
-            self._bufs[T] = b
+                b["sh_h"], b["shared"] = bf16(T, S), bf16(T, H)
+            self._bufs[T, S] = b
         return b
 
     def _front(self, x, logits, b, step):

@@ -529,3 +529,61 @@ def test_mx_layer_captured_and_replayed(T):
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(y, expect), rep
+
+
+def test_mx_layer_with_router_and_shared_experts():
+    T, k, E, H, I, S = 6, 2, 8, 256, 96, 128
+    g = gen(77)
+    layer = mq.MxMoELayer(H, I, E, k, device=DEV)
+    layer.quantize_weights((torch.randn(E, 2 * I, H, generator=g) * .1).to(DEV),
+                           (torch.randn(E, H, I, generator=g) * .1).to(DEV))
+    x = torch.randn(T, H, generator=g).to(torch.bfloat16).to(DEV)
+    with pytest.raises(ValueError, match="router"):
+        layer.forward(x)
+    with pytest.raises(ValueError, match="router"):
+        layer.forward_few(x)
+    layer.set_router((torch.randn(E, H, generator=g) / 16).to(DEV))
+    layer.set_shared((torch.randn(2 * S, H, generator=g) * .1).to(torch.bfloat16).to(DEV),
+                     (torch.randn(H, S, generator=g) * .1).to(torch.bfloat16).to(DEV))
+    logits = mq.moe_router_logits(x, layer.w_router)
+    shared = mq.moe_shared_gemm_bf16(mq.moe_shared_gemm_bf16(x, layer.ws13, mq.EPI_SILU_MUL), layer.ws2)
+    events = []
+    y = layer.forward(x, events=events).clone()
+    assert torch.equal(layer.forward(x, logits), y)
+    assert [e[0] for e in events] == ["router", "shared_gate_up", "shared_down", "route", "quant_x",
+                                      "plan", "gemm_gate_up", "quant_h", "gemm_down", "combine"]
+    few = layer.forward_few(x).clone()
+    direct = mq.moe_layer_mxfp4_few(logits, x, layer.w13, layer.s13, layer.w2, layer.s2, k,
+                                    shared=shared)
+    assert torch.equal(few, direct["y"])
+    plain = mq.moe_layer_mxfp4_few(logits, x, layer.w13, layer.s13, layer.w2, layer.s2, k)["y"]
+    assert not torch.equal(few, plain)
+    err = (few.double() - (plain.double() + shared.double())).abs()
+    assert (err <= 2.0 ** -8 * (plain.double().abs() + few.double().abs()) * 1.01).all()
+    with pytest.raises(ValueError):
+        layer.set_weights_fnuz(None, None, None, None)
+    with pytest.raises(TypeError):
+        layer.forward(x.float())                       # shared experts take bf16
+
+
+def test_mx_layer_shared_experts_of_another_width_after_a_call():
+    T, k, E, H, I = 5, 2, 8, 256, 96
+    g = gen(78)
+    layer = mq.MxMoELayer(H, I, E, k, device=DEV)
+    layer.quantize_weights((torch.randn(E, 2 * I, H, generator=g) * .1).to(DEV),
+                           (torch.randn(E, H, I, generator=g) * .1).to(DEV))
+    x = torch.randn(T, H, generator=g).to(torch.bfloat16).to(DEV)
+    logits = torch.randn(T, E, generator=g).to(DEV)
+    first = layer.forward(x, logits)                   # buffers without shared experts
+    alone = first.clone()
+    for S in (64, 128):
+        ws13 = (torch.randn(2 * S, H, generator=g) * .1).to(torch.bfloat16).to(DEV)
+        ws2 = (torch.randn(H, S, generator=g) * .1).to(torch.bfloat16).to(DEV)
+        layer.set_shared(ws13, ws2)
+        b = layer.forward(x, logits, return_all=True)
+        shared = mq.moe_shared_gemm_bf16(mq.moe_shared_gemm_bf16(x, ws13, mq.EPI_SILU_MUL), ws2)
+        assert torch.equal(b["shared"], shared)
+        assert torch.equal(b["y"], mq.moe_combine(b["o"], b["plan"], b["w"], shared, E=E))
+    layer.set_shared(None, None)
+    assert torch.equal(layer.forward(x, logits), alone)
+    assert first.data_ptr() == layer.forward(x, logits).data_ptr()

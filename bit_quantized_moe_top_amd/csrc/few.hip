@@ -589,7 +589,7 @@ hipError_t launch_layer_mxfp4_few(const float* logits, const float* bias, int T,
   uint32_t* counters = reinterpret_cast<uint32_t*>(base);
   uint16_t* h = reinterpret_cast<uint16_t*>(base + align256(size_t(H / 32) * 4));
   float* o = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(h) + align256(size_t(R) * I * 4));
-  const int upw1 = few_units_per_wg(R, I / 16, 3072), upw2 = few_units_per_wg(R, H / 32, 4096);
+  const int upw1 = few_units_per_wg(R, I / 16, 3000), upw2 = few_units_per_wg(R, H / 32, 4096);
   const int runs1 = (I / 16 + upw1 - 1) / upw1, runs2 = (H / 32 + upw2 - 1) / upw2;
   with_route_slots(E, [&](auto ns) {
     hipLaunchKernelGGL((few_gate_up_kernel<decltype(ns)::value>), dim3(unsigned(R * runs1)),

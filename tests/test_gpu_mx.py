@@ -587,3 +587,18 @@ def test_mx_layer_shared_experts_of_another_width_after_a_call():
     layer.set_shared(None, None)
     assert torch.equal(layer.forward(x, logits), alone)
     assert first.data_ptr() == layer.forward(x, logits).data_ptr()
+
+
+def test_mx_layer_no_tokens_and_too_many():
+    k, E, H, I = 2, 8, 256, 96
+    g = gen(79)
+    layer = mq.MxMoELayer(H, I, E, k, device=DEV)
+    layer.quantize_weights((torch.randn(E, 2 * I, H, generator=g) * .1).to(DEV),
+                           (torch.randn(E, H, I, generator=g) * .1).to(DEV))
+    x = torch.randn(17, H, generator=g).to(torch.bfloat16).to(DEV)
+    logits = torch.randn(17, E, generator=g).to(DEV)
+    assert layer.forward_few(x[:0], logits[:0]).shape == (0, H)
+    assert layer.forward(x[:0], logits[:0]).shape == (0, H)
+    with pytest.raises(ValueError, match="16 tokens"):
+        layer.forward_few(x, logits)
+    assert torch.equal(layer.forward(x, logits)[:16], layer.forward(x[:16], logits[:16]))

@@ -7,10 +7,11 @@
 //
 // Sums: W = e2m1 * 2^s converts exactly to bf16 (2 significant bits), products
 // and sums run in fp32 on v_mfma_f32_16x16x32_bf16.  h enters the second product as
-// the sum of two bf16 values, hi = bf16(h) and lo = bf16(h - hi), which keeps 16 of
-// its bits: the matrix units have the time (the weights are converted once for
-// both), and y is as close to the exact value as its one rounding to bf16 allows
-// (rounding h to bf16 alone made its error 1.5 times as large).  o stays fp32.
+// the sum of three bf16 values, 8 of fp32's 24 significant bits each, so nothing of
+// it is rounded away (split_bf16): the matrix units have the time, and the weights
+// are converted once for all three.  o stays fp32; y is rounded once.  (Two values,
+// 16 bits, took 0.2 us less at one token and 0.4 at four, and cost y a bf16 step in
+// one element of some hundreds.)
 //
 // Work units.  A workgroup belongs to one routed row r = t k + j and a run of
 // column units.  In the gate/up kernel it finds its row's expert and the other
@@ -34,7 +35,7 @@
 // Bound by HBM plus some 4 us per kernel that no load covers (launch, routing or
 // ids, first bytes; reduction, join).  4096 x 2048, top-6 of 256 experts, gate/up +
 // down in us, against the weights at the 6.28 TB/s of a pure read: one token 13.9 +
-// 8.5 (8.5 + 4.3), four tokens 37.5 + 20.7 (32.8 + 16.4), sixteen 105 + 70 (114 +
+// 8.8 (8.5 + 4.3), four tokens 37.7 + 21.3 (32.8 + 16.4), sixteen 105 + 70 (114 +
 // 57; some of the weights still lie in the memory-side cache).  On the way: routing
 // every token in every workgroup 55.9 (four tokens, gate/up) -> ranks instead of k
 // argmax rounds 53.4 -> unconditional LDS reads and no register spills 36.9.
@@ -49,7 +50,7 @@ constexpr int kFewThreads = 256;
 constexpr int kFewMaxRows = 2 * kWave;        // routed rows: 16 tokens x 8 experts
 static_assert(kFewTokens * MOEQ_MAX_TOPK <= kFewMaxRows, "two ballots cover the routed rows");
 // Activation rows staged in LDS: at most four, in at most 17 KB for T <= 4 tokens
-// (two rows of 4096 elements, or of 2048 in two planes), 25 KB above.  More would
+// (two rows of 4096 elements of x, one of 2048 of h in three planes), 25 KB above.  More would
 // leave fewer workgroups on a CU for rows that are rarely there; an expert with more
 // rows reads them from memory.  4096 x 2048, top-6 of 256 experts, gate/up and down in
 // us with 17, 25 and 33 KB: four tokens 37.6, 20.8 / 38.1, 22.2 / 40.7, 24.6; sixteen
@@ -58,11 +59,26 @@ constexpr int kStageRows = 4;
 constexpr int few_stage_limit(int T) { return (T > 4 ? 25 : 17) << 10; }
 
 constexpr int kDppRowRor8 = 0x128;            // lane i of 16 takes lane (i + 8) % 16
+constexpr int kDppRowRor12 = 0x12C;           // ... lane (i + 4) % 16
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 
 __device__ __forceinline__ mx_v4f mfma_bf16(const uint4& w, const uint4& a, const mx_v4f& c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, w),
                                                  __builtin_bit_cast(bf8, a), c, 0, 0, 0);
+}
+
+// v as the sum of three bf16 values: the top 8 significant bits (cut off, so the
+// largest finite values do not round up to infinity), the next 8, the last 8.  Each
+// difference is exact.  Bits below 2^-133, bf16's smallest step, are cut off.  The
+// rest of an infinity is 0 (not inf - inf), that of a NaN a NaN.
+constexpr int kHPlanes = 3;
+__device__ __forceinline__ void split_bf16(float v, uint32_t (&p)[kHPlanes]) {
+  p[0] = f2u(v) & 0xFFFF0000u;
+  const float r = fabsf(v) == INFINITY ? 0.0f : v - u2f(p[0]);
+  p[1] = f2u(r) & 0xFFFF0000u;
+  p[2] = f2u(r - u2f(p[1]));
+#pragma unroll
+  for (int i = 0; i < kHPlanes; ++i) p[i] >>= 16;
 }
 
 // rows of one expert among the routed rows: the routed row of activation row n
@@ -112,9 +128,13 @@ struct FewStage {
   }
   // copies pieces first, first + kFewThreads, ... of row i's planes
   __device__ __forceinline__ void copy(int i, int row, int first) const {
+    for (int p = first; p < per_plane; p += kFewThreads) {
+      uint4 v[kPlanes];
 #pragma unroll
-    for (int plane = 0; plane < kPlanes; ++plane)
-      for (int p = first; p < per_plane; p += kFewThreads) put(i, plane, p, piece(row, plane, p));
+      for (int plane = 0; plane < kPlanes; ++plane) v[plane] = piece(row, plane, p);
+#pragma unroll
+      for (int plane = 0; plane < kPlanes; ++plane) put(i, plane, p, v[plane]);
+    }
   }
 };
 
@@ -123,7 +143,7 @@ struct FewStage {
 // pieces are loaded at the top of the kernel and parked in LDS later.
 template <int kPlanes>
 struct EarlyRow {
-  static constexpr int kEarly = 2 / kPlanes;  // pieces per thread and plane
+  static constexpr int kEarly = 2;            // pieces per thread and plane
   uint4 v[kPlanes][kEarly];
   __device__ __forceinline__ void load(const FewStage<kPlanes>& st, int row, int tid) {
 #pragma unroll
@@ -204,21 +224,22 @@ __device__ __forceinline__ void few_mac(const MxFrag (&f)[2], const uint8_t* act
 // multiplied; the first item's are already in `f0`.
 //
 // kStaged: the rows are in LDS; lanes past the last row read the last one (their
-// columns of the result are never used).  Two planes then share one product: at
-// most kStageRows rows leave columns free, so the lanes of columns 8 .. 15 read the
-// second plane of rows 0 .. 7 and the two halves are added at the end.  Otherwise
-// (more rows) they are read from memory, plane by plane.
+// columns of the result are never used).  The planes then share one product: at
+// most kStageRows rows leave columns free, so the lanes of columns 4 p .. 4 p + 3
+// read plane p of rows 0 .. 3 (the last four the last plane once more, unused) and
+// the groups are added at the end.  Otherwise (more rows) they are read from
+// memory, plane by plane.
 template <bool kStaged, int kPlanes, typename WeightsT, typename DoneF>
 __device__ __forceinline__ void few_units(const WeightsT& wt, int u0, int u1, const FewStage<kPlanes>& st,
                                           MxFrag (&f0)[2], mx_v4f* red, DoneF&& done) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int q = __builtin_amdgcn_readfirstlane(tid >> 6);
-  constexpr bool kHalves = kStaged && kPlanes == 2;
-  static_assert(kStageRows <= 8 && kPlanes <= 2, "a half of the 16 columns per plane");
+  constexpr bool kGroups = kStaged && kPlanes > 1;
+  static_assert(kStageRows <= 4 && (kPlanes == 1 || kPlanes == 3), "four of the 16 columns per plane");
   const int ln = lane & 15, kb = lane >> 4;
-  const int row = min(kHalves ? ln & 7 : ln, st.n - 1);
+  const int row = min(kGroups ? ln & 3 : ln, st.n - 1);
   const uint8_t* act =
-      (kStaged ? st.lds + (row * kPlanes + (kHalves ? ln >> 3 : 0)) * st.plane_bytes
+      (kStaged ? st.lds + (row * kPlanes + (kGroups ? min(ln >> 2, kPlanes - 1) : 0)) * st.plane_bytes
                : reinterpret_cast<const uint8_t*>(st.src + int64_t(st.rows[row]) * kPlanes * st.K)) +
       kb * 256;
   const int per_unit = max(wt.gn, 1);                   // a wave without K still joins the sums
@@ -251,11 +272,12 @@ __device__ __forceinline__ void few_units(const WeightsT& wt, int u0, int u1, co
       for (int j = 0; j < 2; ++j)
         acc[j] = acc[j] + (half[j * kWave + lane] +
                            (half[(2 + j) * kWave + lane] + half[(4 + j) * kWave + lane]));
-      if (kHalves) {                                    // column n + 8 to column n
+      if (kGroups) {                                    // columns n + 4 and n + 8 to column n
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int v = 0; v < 4; ++v) acc[j][v] += dpp<kDppRowRor8>(acc[j][v], acc[j][v]);
+          for (int v = 0; v < 4; ++v)
+            acc[j][v] += dpp<kDppRowRor12>(acc[j][v], acc[j][v]) + dpp<kDppRowRor8>(acc[j][v], acc[j][v]);
       }
       done(u, acc);
     }
@@ -427,15 +449,14 @@ few_gate_up_kernel(const float* logits, const float* bias, int T, int E, int k, 
   auto done = [&](int u, const mx_v4f (&v)[2]) {
     if (ln >= n) return;
     const mx_v4f hv = silu_mul4(v[0], v[1]);
-    mx_v4f hi, lo;
+    uint32_t p[4][kHPlanes];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      hi[c] = static_cast<float>(static_cast<__bf16>(hv[c]));
-      lo[c] = fabsf(hi[c]) < INFINITY ? hv[c] - hi[c] : 0.0f;   // (no inf - inf)
-    }
-    const int64_t at = int64_t(rows[ln]) * 2 * I + 16 * u + 4 * kb;
-    store4(h, 0, at, hi);
-    store4(h, 0, at + I, lo);
+    for (int c = 0; c < 4; ++c) split_bf16(hv[c], p[c]);
+    uint16_t* at = h + int64_t(rows[ln]) * kHPlanes * I + 16 * u + 4 * kb;
+#pragma unroll
+    for (int i = 0; i < kHPlanes; ++i)
+      *reinterpret_cast<uint2*>(at + i * I) =
+          make_uint2(p[0][i] | p[1][i] << 16, p[2][i] | p[3][i] << 16);
   };
   few_run(wt, u0, u1, st, stage_rows, f0, red, done);
 }
@@ -467,8 +488,8 @@ few_down_kernel(const int32_t* ids, const float* topk_w, const uint16_t* h, int 
   const int r = blockIdx.x / runs;
   const int u0 = (blockIdx.x - r * runs) * units_per_wg, u1 = min(u0 + units_per_wg, units);
   const int e_lo = ids[min(lane, R - 1)], e_hi = ids[min(lane + kWave, R - 1)];
-  FewStage<2> st(h, rows, lds, I);
-  EarlyRow<2> early;
+  FewStage<kHPlanes> st(h, rows, lds, I);
+  EarlyRow<kHPlanes> early;
   if (stage_rows > 0) early.load(st, r, tid);
   // (ids come from the first kernel of the call; clamped all the same)
   const int e = min(max(__builtin_amdgcn_readfirstlane(ids[r]), 0), E - 1);
@@ -575,7 +596,7 @@ int few_units_per_wg(int R, int units, int launch) {
 
 size_t few_ws_bytes(int T, int k, int H, int I) {
   const size_t R = size_t(T) * k;
-  return align256(size_t(H / 32) * 4) + align256(R * I * 4) + align256(R * H * 4);
+  return align256(size_t(H / 32) * 4) + align256(R * I * (2 * kHPlanes)) + align256(R * H * 4);
 }
 
 hipError_t launch_layer_mxfp4_few(const float* logits, const float* bias, int T, int E, int k,
@@ -588,7 +609,7 @@ hipError_t launch_layer_mxfp4_few(const float* logits, const float* bias, int T,
   uint8_t* base = static_cast<uint8_t*>(ws);
   uint32_t* counters = reinterpret_cast<uint32_t*>(base);
   uint16_t* h = reinterpret_cast<uint16_t*>(base + align256(size_t(H / 32) * 4));
-  float* o = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(h) + align256(size_t(R) * I * 4));
+  float* o = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(h) + align256(size_t(R) * I * (2 * kHPlanes)));
   const int upw1 = few_units_per_wg(R, I / 16, 3000), upw2 = few_units_per_wg(R, H / 32, 4096);
   const int runs1 = (I / 16 + upw1 - 1) / upw1, runs2 = (H / 32 + upw2 - 1) / upw2;
   with_route_slots(E, [&](auto ns) {
@@ -600,8 +621,8 @@ hipError_t launch_layer_mxfp4_few(const float* logits, const float* bias, int T,
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   hipLaunchKernelGGL(few_down_kernel, dim3(unsigned(R * runs2)), dim3(kFewThreads),
-                     few_stage_bytes(T, 2, I), stream, ids, topk_w, h, T, E, k, w2, ws2, H, I, upw2,
-                     few_stage_rows(T, 2, I), o, counters, shared, y);
+                     few_stage_bytes(T, kHPlanes, I), stream, ids, topk_w, h, T, E, k, w2, ws2, H, I, upw2,
+                     few_stage_rows(T, kHPlanes, I), o, counters, shared, y);
   return hipGetLastError();
 }
 

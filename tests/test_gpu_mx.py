@@ -459,6 +459,69 @@ def test_few_layer_two_streams_with_their_own_workspaces():
         assert torch.equal(ya, ra) and torch.equal(yb, rb)
 
 
+# h between the two products: one expert per token (weight 1), so that y is W2 h alone.
+def one_expert(T, H, I, w13, w2):
+    """A Few whose only expert has the given weights (exact in MXFP4)."""
+    f = Few(T, 1, 1, H, I, 40)
+    f.w13v, f.w2v = w13[None], w2[None]
+    for name, v in (("w13", f.w13v), ("w2", f.w2v)):
+        q, s = X.quant_mxfp4(v)
+        np.testing.assert_array_equal(X.values(q, s), v)
+        setattr(f, name, mq.tile_mxfp4_weights(torch.from_numpy(q).to(DEV), torch.from_numpy(s).to(DEV)))
+    return f
+
+
+@pytest.mark.parametrize("T", [1, 2, 16])      # h staged in LDS, and read from memory
+def test_few_layer_h_keeps_fp32(T):
+    """y[c] = h[2c] - h[2c + 1], which differ by 2^-13 of themselves: a rounding of h to fewer bits
+    than fp32's shows.  Per column: g is one exact product, the same for both; u is one product
+    plus, for h[2c], a small one (2 u); h rounds once more (u each); the difference is a sum of the
+    parts that h is split into, three at most each (6 terms, 2 u each of the magnitudes).  So
+    |dy| <= 16 u |y| + (2 + 1 + 12) u (|h0| + |h1|), and y's own rounding."""
+    H, I = 64, 128
+    g = np.random.default_rng(50)
+    w13, w2 = np.zeros((2 * I, H)), np.zeros((H, I))
+    mags = np.array([1.0, 1.5, 2.0, 3.0])
+    for c in range(H):
+        a, b, d = g.integers(0, 32, 3)
+        gate, up, low = g.choice(mags), g.choice(mags), g.choice(mags) * 2.0 ** -13
+        for i in (2 * c, 2 * c + 1):
+            w13[i, a], w13[I + i, b] = gate, up
+        w13[I + 2 * c, 32 + d] = low
+        w2[c, 2 * c], w2[c, 2 * c + 1] = 1.0, -1.0
+    f = one_expert(T, H, I, w13, w2)
+    f.x = (torch.rand(T, H, generator=gen(51)) + 0.5).to(torch.bfloat16)
+    x = to_np(f.x).astype(np.float64)
+    gu = x @ w13.T
+    h = L.silu(gu[:, :I]) * gu[:, I:]
+    ref = h @ w2.T
+    d = 16 * U * np.abs(ref) + 15 * U * (np.abs(h) @ np.abs(w2).T)
+    err = np.abs(to_np(f.run()["y"]).astype(np.float64) - ref)
+    assert (err <= d + 2.0 ** -8 * (np.abs(ref) + d)).all(), (err / d).max()
+
+
+@pytest.mark.parametrize("T", [1, 16])
+def test_few_layer_h_up_to_the_largest_fp32(T):
+    """h = 0.9995 * 2^128, finite in fp32 and past bf16's largest value, of either sign."""
+    H, I = 64, 32
+    w13, w2 = np.zeros((2 * I, H)), np.zeros((H, I))
+    w13[:I, 0] = 1.0                               # g = 64: silu(g) = g in fp32
+    w13[I:, 1], w13[I:, 32] = 2.0 ** 62, 2.0 ** 60
+    w2[np.arange(H), np.arange(H) % I] = 2.0 ** -100
+    f = one_expert(T, H, I, w13, w2)
+    f.x = torch.zeros(T, H, dtype=torch.bfloat16)
+    sign = 1 - 2 * (torch.arange(T) % 2)
+    f.x[:, 0] = 64.0
+    f.x[:, 1], f.x[:, 32] = sign * 1.9921875 * 2.0 ** 59, sign * 1.75 * 2.0 ** 53
+    x = to_np(f.x).astype(np.float64)
+    gu = x @ w13.T
+    h = gu[:, :I] * gu[:, I:]
+    assert 2.0 ** 128 * (1 - 2.0 ** -9) < np.abs(h).min() and np.abs(h).max() < np.finfo(np.float32).max
+    ref = h @ w2.T
+    y = to_np(f.run()["y"]).astype(np.float64)
+    assert (np.abs(y - ref) <= (2.0 ** -8 + 32 * U) * np.abs(ref)).all()
+
+
 # --------------------------------------------------------------- whole layer ----
 def chain_reference(x, logits, bias, shared, w13v, w2v, k):
     """The layer as MxMoELayer.forward computes it, in float64 with its roundings: x and h in

@@ -36,7 +36,9 @@
 // ids, first bytes; reduction, join).  4096 x 2048, top-6 of 256 experts, gate/up +
 // down in us, against the weights at the 6.28 TB/s of a pure read: one token 13.9 +
 // 8.8 (8.5 + 4.3), four tokens 37.7 + 21.3 (32.8 + 16.4), sixteen 105 + 70 (114 +
-// 57; some of the weights still lie in the memory-side cache).  On the way: routing
+// 57; some of the weights still lie in the memory-side cache).  Where tokens share
+// experts the reads of their activations bind: sixteen tokens, top-2 of 8 experts,
+// 33.6 + 29.6 (11.2 + 5.6).  On the way: routing
 // every token in every workgroup 55.9 (four tokens, gate/up) -> ranks instead of k
 // argmax rounds 53.4 -> unconditional LDS reads and no register spills 36.9.
 #include "front.hpp"
@@ -50,13 +52,18 @@ constexpr int kFewThreads = 256;
 constexpr int kFewMaxRows = 2 * kWave;        // routed rows: 16 tokens x 8 experts
 static_assert(kFewTokens * MOEQ_MAX_TOPK <= kFewMaxRows, "two ballots cover the routed rows");
 // Activation rows staged in LDS: at most four, in at most 17 KB for T <= 4 tokens
-// (two rows of 4096 elements of x, one of 2048 of h in three planes), 25 KB above.  More would
-// leave fewer workgroups on a CU for rows that are rarely there; an expert with more
-// rows reads them from memory.  4096 x 2048, top-6 of 256 experts, gate/up and down in
-// us with 17, 25 and 33 KB: four tokens 37.6, 20.8 / 38.1, 22.2 / 40.7, 24.6; sixteen
-// 108.2, 71.4 / 105.1, 70.2 / 107.9, 69.4.
+// (two rows of 4096 elements of x, one of 2048 of h in three planes), 25 KB above; a
+// single row may take 40 KB.  More would leave fewer workgroups on a CU for rows that
+// are rarely there; an expert with more rows reads them from memory.  Measured, us:
+//   4096 x 2048, top-6 of 256 experts, gate/up with 17, 25, 33 KB: four tokens 37.6,
+//   38.1, 40.7; sixteen 108.2, 105.1, 107.9; down with 17, 25 KB: four tokens 21.2,
+//   22.4; with 25, 37 KB: eight 39.2, 46.7; sixteen 74.4, 73.8
+//   one row in 17, 25, 40, 65 KB: h of 2880, one token 12.4, 9.9, 10.1, 9.7; of 6144
+//   18.0, 18.1, 14.0, 13.9; of 8192, eight tokens 72.8, 71.4, 71.9, 79.8
 constexpr int kStageRows = 4;
 constexpr int few_stage_limit(int T) { return (T > 4 ? 25 : 17) << 10; }
+constexpr int kStageOne = 40 << 10;
+constexpr int kTurnBytes = 4096;              // LDS per wave for rows read from memory (MemoryAct)
 
 constexpr int kDppRowRor8 = 0x128;            // lane i of 16 takes lane (i + 8) % 16
 constexpr int kDppRowRor12 = 0x12C;           // ... lane (i + 4) % 16
@@ -87,14 +94,15 @@ struct FewRows {
   int n;
   bool owner;
 };
-// (ids of one token differ, so there are at most kFewTokens; the bound keeps ids that
-// something else wrote from leaving the array)
-__device__ __forceinline__ FewRows find_rows(int e_lo, int e_hi, int R, int r, int lane, int* rows) {
+// (ids of one token differ, so there are at most T; the bounds keep ids that something
+// else wrote from leaving the array)
+__device__ __forceinline__ FewRows find_rows(int e_lo, int e_hi, int T, int R, int r, int lane,
+                                             int* rows) {
   const int e = r < kWave ? readlane(e_lo, r & 63) : readlane(e_hi, r & 63);
   const uint64_t lo = __ballot(lane < R && e_lo == e);
   const uint64_t hi = __ballot(lane + kWave < R && e_hi == e);
   FewRows f;
-  f.n = min(__popcll(lo) + __popcll(hi), kFewTokens);
+  f.n = min(__popcll(lo) + __popcll(hi), T);
   f.owner = (lo ? __ffsll(static_cast<unsigned long long>(lo)) - 1
                 : kWave + __ffsll(static_cast<unsigned long long>(hi)) - 1) == r;
   const uint64_t below = (uint64_t(1) << lane) - 1;
@@ -184,35 +192,77 @@ struct FewWeights {
   }
 };
 
-// acc += W A over one super-group: a lane's four steps take the activation
-// blocks 4 kb .. 4 kb + 3 of the super-group, 256 consecutive bytes at `act`.
-// Further planes of the rows follow `plane` bytes apart.  kPartial: the row ends
-// inside the super-group, `left` bytes on.
-template <int kPlanes, bool kPartial>
-__device__ __forceinline__ void few_mac(const MxFrag (&f)[2], const uint8_t* act, int64_t plane,
-                                        int left, mx_v4f (&acc)[2]) {
+// Activations of one super-group as the 16 columns of the products take them: lane
+// (ln, kb) holds column ln's blocks 4 kb .. 4 kb + 3 (256 consecutive bytes), step j
+// and quarter m of it 16 bytes.  kSets columns sets share the weights.
+//
+// From LDS, where the rows are staged: one set, `at` the lane's column and kb.
+struct StagedAct {
+  static constexpr int kSets = 1;
+  const uint8_t* at;
+  uint4 v[1][4];
+  __device__ __forceinline__ void load(int sg, int j) {
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+      v[0][m] = *reinterpret_cast<const uint4*>(at + sg * 1024 + j * 64 + m * 16);
+  }
+};
+// From memory.  A load takes 64 consecutive bytes (one block) of 16 columns, lane l
+// piece l % 4 of column l / 4, so that it touches 16 lines and not 64; 4 KB of LDS
+// that belong to the wave turn the pieces round.  (`at`: the lane's column l / 4 of
+// each set, `turn`: the wave's LDS, XOR-swizzled so that the 16 columns of one kb
+// read different banks.)  Blocks past K are 0.  Down product, 4096 x 2048, 16 tokens,
+// in us: top-8 of 8 experts 80.4 with each lane loading its own pieces, 45.6 turned;
+// top-2 of 8 37.3, 29.6.
+template <int kColumnSets>
+struct MemoryAct {
+  static constexpr int kSets = kColumnSets;
+  const uint8_t* at[kSets];
+  uint8_t* turn;
+  int blocks, lane;
+  uint4 v[kSets][4];
+  __device__ __forceinline__ void load(int sg, int j) {
+#pragma unroll
+    for (int p = 0; p < kSets; ++p)
+#pragma unroll
+      for (int kb = 0; kb < 4; ++kb) {
+        const int b = 16 * sg + 4 * kb + j;
+        v[p][kb] = make_uint4(0u, 0u, 0u, 0u);
+        if (b < blocks) v[p][kb] = *reinterpret_cast<const uint4*>(at[p] + b * 64);
+      }
+    const int wc = lane >> 2, wm = lane & 3, ln = lane & 15, kb = lane >> 4;
+#pragma unroll
+    for (int p = 0; p < kSets; ++p) {
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        *reinterpret_cast<uint4*>(turn + ((b * 16 + wc) * 4 + (wm ^ (wc >> 2))) * 16) = v[p][b];
+      lds_wave_sync();
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+        v[p][m] = *reinterpret_cast<const uint4*>(turn + ((kb * 16 + ln) * 4 + (m ^ (ln >> 2))) * 16);
+      lds_wave_sync();
+    }
+  }
+};
+
+// acc += W A over one super-group
+template <typename ActT>
+__device__ __forceinline__ void few_mac(const MxFrag (&f)[2], ActT& act, int sg, mx_v4f (&acc)[2]) {
   static_for<kMxSteps>([&](auto j) {
     float sc[2];                              // byte j of the scale dword in the exponent field
 #pragma unroll
     for (int b = 0; b < 2; ++b)
       sc[b] = u2f((j < 3 ? f[b].s << (j < 3 ? 23 - 8 * j : 0) : f[b].s >> 1) & 0x7F800000u);
+    act.load(sg, j);
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      uint4 a[kPlanes];
-#pragma unroll
-      for (int p = 0; p < kPlanes; ++p) {
-        a[p] = make_uint4(0u, 0u, 0u, 0u);
-        if (!kPartial || j * 64 < left)
-          a[p] = *reinterpret_cast<const uint4*>(act + p * plane + j * 64 + m * 16);
-      }
+    for (int m = 0; m < 4; ++m)
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         const uint32_t c = m == 0 ? f[b].c[j].x : m == 1 ? f[b].c[j].y : m == 2 ? f[b].c[j].z : f[b].c[j].w;
         const uint4 wv = mx_bf16x8(c, sc[b]);
 #pragma unroll
-        for (int p = 0; p < kPlanes; ++p) acc[b] = mfma_bf16(wv, a[p], acc[b]);
+        for (int p = 0; p < ActT::kSets; ++p) acc[b] = mfma_bf16(wv, act.v[p][m], acc[b]);
       }
-    }
   });
 }
 
@@ -223,25 +273,35 @@ __device__ __forceinline__ void few_mac(const MxFrag (&f)[2], const uint8_t* act
 // with two register sets, so the next item's weights are in flight while one is
 // multiplied; the first item's are already in `f0`.
 //
-// kStaged: the rows are in LDS; lanes past the last row read the last one (their
-// columns of the result are never used).  The planes then share one product: at
-// most kStageRows rows leave columns free, so the lanes of columns 4 p .. 4 p + 3
-// read plane p of rows 0 .. 3 (the last four the last plane once more, unused) and
-// the groups are added at the end.  Otherwise (more rows) they are read from
-// memory, plane by plane.
-template <bool kStaged, int kPlanes, typename WeightsT, typename DoneF>
+// kStaged: the rows are in LDS, otherwise they are read from memory.  Columns past
+// the last row read the last one (their results are never used).  kGrouped (at most
+// kStageRows rows, which leaves columns free): the planes share one product, columns
+// 4 p .. 4 p + 3 read plane p of rows 0 .. 3 (the last four the last plane once more,
+// unused) and the groups are added at the end.  Otherwise a product per plane.
+template <bool kStaged, bool kGrouped, int kPlanes, typename WeightsT, typename DoneF>
 __device__ __forceinline__ void few_units(const WeightsT& wt, int u0, int u1, const FewStage<kPlanes>& st,
                                           MxFrag (&f0)[2], mx_v4f* red, DoneF&& done) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int q = __builtin_amdgcn_readfirstlane(tid >> 6);
-  constexpr bool kGroups = kStaged && kPlanes > 1;
   static_assert(kStageRows <= 4 && (kPlanes == 1 || kPlanes == 3), "four of the 16 columns per plane");
+  static_assert(!kStaged || kGrouped || kPlanes == 1, "staged rows are few");
+  constexpr bool kGroups = kGrouped && kPlanes > 1;
   const int ln = lane & 15, kb = lane >> 4;
-  const int row = min(kGroups ? ln & 3 : ln, st.n - 1);
-  const uint8_t* act =
-      (kStaged ? st.lds + (row * kPlanes + (kGroups ? min(ln >> 2, kPlanes - 1) : 0)) * st.plane_bytes
-               : reinterpret_cast<const uint8_t*>(st.src + int64_t(st.rows[row]) * kPlanes * st.K)) +
-      kb * 256;
+  const auto col_row = [&](int c) { return min(kGroups ? c & 3 : c, st.n - 1); };
+  const auto col_plane = [&](int c) { return kGroups ? min(c >> 2, kPlanes - 1) : 0; };
+  std::conditional_t<kStaged, StagedAct, MemoryAct<kGroups ? 1 : kPlanes>> act;
+  if constexpr (kStaged) {
+    act.at = st.lds + (col_row(ln) * kPlanes + col_plane(ln)) * st.plane_bytes + kb * 256;
+  } else {
+    const int c = lane >> 2;
+#pragma unroll
+    for (int p = 0; p < act.kSets; ++p)
+      act.at[p] = reinterpret_cast<const uint8_t*>(
+          st.src + (int64_t(st.rows[col_row(c)]) * kPlanes + col_plane(c) + p) * st.K + (lane & 3) * 8);
+    act.turn = st.lds + q * kTurnBytes;
+    act.blocks = st.K / kMxBlock;
+    act.lane = lane;
+  }
   const int per_unit = max(wt.gn, 1);                   // a wave without K still joins the sums
   const int items = (u1 - u0) * per_unit;
   mx_v4f acc[2] = {mx_v4f{0.f, 0.f, 0.f, 0.f}, mx_v4f{0.f, 0.f, 0.f, 0.f}};
@@ -253,11 +313,7 @@ __device__ __forceinline__ void few_units(const WeightsT& wt, int u0, int u1, co
     if (lu < u1 && wt.gn > 0) wt.load(lu, li, lane, f);
   };
   auto step = [&](MxFrag (&f)[2]) {
-    if (wt.gn > 0) {
-      const int at = (wt.g0 + i) * 1024;
-      if (kStaged) few_mac<1, false>(f, act + at, 0, 0, acc);
-      else few_mac<kPlanes, true>(f, act + at, int64_t(st.K) * 2, st.K * 2 - at - kb * 256, acc);
-    }
+    if (wt.gn > 0) few_mac(f, act, wt.g0 + i, acc);
     if (++i < per_unit) return;
     // one half of red per unit parity: a unit's sums are read before the barrier
     // of the next, and overwritten after it
@@ -316,9 +372,11 @@ __device__ __forceinline__ void few_run(const WeightsT& wt, int u0, int u1, cons
       for (int i = 1; i < st.n; ++i) st.copy(i, st.rows[i], threadIdx.x);
       lds_barrier();
     }
-    few_units<true>(wt, u0, u1, st, f0, red, done);
+    few_units<true, true>(wt, u0, u1, st, f0, red, done);
+  } else if (kPlanes > 1 && st.n <= kStageRows) {
+    few_units<false, true>(wt, u0, u1, st, f0, red, done);
   } else {
-    few_units<false>(wt, u0, u1, st, f0, red, done);
+    few_units<false, false>(wt, u0, u1, st, f0, red, done);
   }
 }
 
@@ -498,7 +556,7 @@ few_down_kernel(const int32_t* ids, const float* topk_w, const uint16_t* h, int 
   MxFrag f0[2];
   if (wt.gn > 0) wt.load(u0, 0, lane, f0);
   if (stage_rows > 0) early.store(st, r, tid);
-  const FewRows f = find_rows(e_lo, e_hi, R, r, lane, rows);
+  const FewRows f = find_rows(e_lo, e_hi, T, R, r, lane, rows);
   const int ln = lane & 15, kb = lane >> 4;
 
   // Wave 0, after its stores: one arrival per unit of the run, then y where this
@@ -574,10 +632,15 @@ int few_row_bytes(int planes, int K) { return planes * (mx_supers(K) * (kMxSuper
 int few_stage_rows(int T, int planes, int K) {
   const int fit = few_stage_limit(T) / few_row_bytes(planes, K);
   const int n = T < kStageRows ? T : kStageRows;
+  if (fit == 0) return few_row_bytes(planes, K) <= kStageOne ? 1 : 0;
   return n < fit ? n : fit;
 }
-unsigned few_stage_bytes(int T, int planes, int K) {
-  return unsigned(few_stage_rows(T, planes, K) * few_row_bytes(planes, K));
+// LDS of a launch: the staged rows, or what reading them from memory takes if an
+// expert may have more
+unsigned few_lds_bytes(int T, int planes, int K) {
+  const int rows = few_stage_rows(T, planes, K);
+  const int staged = rows * few_row_bytes(planes, K), turn = kTurnBytes * (kFewThreads / kWave);
+  return unsigned(rows < T && staged < turn ? turn : staged);
 }
 
 // Column units per workgroup.  One unit each lets the dispatcher balance the CUs,
@@ -614,14 +677,14 @@ hipError_t launch_layer_mxfp4_few(const float* logits, const float* bias, int T,
   const int runs1 = (I / 16 + upw1 - 1) / upw1, runs2 = (H / 32 + upw2 - 1) / upw2;
   with_route_slots(E, [&](auto ns) {
     hipLaunchKernelGGL((few_gate_up_kernel<decltype(ns)::value>), dim3(unsigned(R * runs1)),
-                       dim3(kFewThreads), few_stage_bytes(T, 1, H), stream, logits, bias, T, E, k,
+                       dim3(kFewThreads), few_lds_bytes(T, 1, H), stream, logits, bias, T, E, k,
                        renormalize, x, H, w13, ws13, I, upw1, few_stage_rows(T, 1, H), ids, topk_w, h,
                        counters, H / 32);
   });
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   hipLaunchKernelGGL(few_down_kernel, dim3(unsigned(R * runs2)), dim3(kFewThreads),
-                     few_stage_bytes(T, kHPlanes, I), stream, ids, topk_w, h, T, E, k, w2, ws2, H, I, upw2,
+                     few_lds_bytes(T, kHPlanes, I), stream, ids, topk_w, h, T, E, k, w2, ws2, H, I, upw2,
                      few_stage_rows(T, kHPlanes, I), o, counters, shared, y);
   return hipGetLastError();
 }

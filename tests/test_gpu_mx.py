@@ -459,6 +459,16 @@ def test_few_layer_two_streams_with_their_own_workspaces():
         assert torch.equal(ya, ra) and torch.equal(yb, rb)
 
 
+@pytest.mark.parametrize("T,k,E,H,I", [
+    # rows of an expert that do not fit in LDS: more than four; none, at most four of them and
+    # more; a last super-group that ends inside; all sixteen tokens on one expert
+    (7, 2, 2, 544, 1056), (16, 1, 1, 1056, 544), (3, 2, 3, 64, 6688), (9, 2, 2, 64, 6688),
+    (2, 1, 2, 20512, 32), (5, 1, 1, 20512, 32), (16, 2, 2, 96, 8224)])
+def test_few_layer_rows_from_memory(T, k, E, H, I):
+    f = Few(T, k, E, H, I, T + I, shared=True)
+    f.check(f.run())
+
+
 # h between the two products: one expert per token (weight 1), so that y is W2 h alone.
 def one_expert(T, H, I, w13, w2):
     """A Few whose only expert has the given weights (exact in MXFP4)."""

@@ -1,6 +1,7 @@
 // moe_combine kernel: one thread per 8 consecutive hidden columns of one token.
 // y[t, c] = bf16( sum_j w[t, j] * o[row_pos[t*k + j], c] + shared[t, c] ), fp32
-// accumulation in slot order j = 0..k-1, then the shared-expert addend.
+// accumulation in slot order j = 0..k-1 (slots of weight 0 left out), then the
+// shared-expert addend.
 #include "common.hpp"
 #include "kernels.hpp"
 
@@ -56,8 +57,9 @@ combine_kernel(const uint16_t* __restrict__ o, const int32_t* __restrict__ plan,
 #pragma unroll
   for (int j = 0; j < MOEQ_MAX_TOPK; ++j) {
     // slots past k, rows dropped by the permute (and positions outside o, which
-    // only a plan built for other sizes holds)
-    if (j >= k || pos[j] < 0 || pos[j] >= R) continue;
+    // only a plan built for other sizes holds), and slots of weight 0: a masked
+    // expert's row may hold anything
+    if (j >= k || pos[j] < 0 || pos[j] >= R || wt[j] == 0.0f) continue;
     float v[8];
     bf16x8_to_f32(raw[j], v);
 #pragma unroll

@@ -454,11 +454,8 @@ few_gate_up_kernel(const float* logits, const float* bias, int T, int E, int k, 
   constexpr int kWaves = kFewThreads / kWave, kMine = kFewTokens / kWaves;
   if (run == 0 && j == 0 && wave == kWaves - 1) {
     float w;
-    const int id = route_token_values<NS>(logits + int64_t(t) * E, bias, E, k, renormalize, lane, w);
-    const int best = min(readlane(id, 0), E - 1);        // (no candidate: all scores NaN)
-    const float s0 = logits[int64_t(t) * E + best] + (bias ? bias[best] : 0.0f);
-    // a token whose best score is -inf has no weights (0/0): it gets zeros
-    if (lane < k) topk_w[t * k + lane] = s0 == -INFINITY ? 0.0f : w;
+    route_token_values<NS>(logits + int64_t(t) * E, bias, E, k, renormalize, lane, w);
+    if (lane < k) topk_w[t * k + lane] = w;
   }
 
   // Routing.  The row's expert is the j-th best of its token (each wave finds it);

@@ -109,7 +109,8 @@ __device__ __forceinline__ int route_token_values(const float* row, const float*
 #pragma unroll
   for (int r = 1; r < MOEQ_MAX_TOPK; ++r)
     if (r == lane) { v = sel_v[r]; e = sel_e[r]; }
-  w_out = expf(v - smax) / den;
+  // a token whose scores are all -inf has no weights (0/0): it gets zeros
+  w_out = smax == -INFINITY ? 0.0f : expf(v - smax) / den;
   return e;
 }
 

@@ -243,6 +243,8 @@ class MxMoELayer(MoELayer):
     one quantized row, so no gathered copy is made.
     forward_few(): up to 16 tokens in two kernels, activations in bf16.  Its results are closer to
     the unquantized layer's than forward()'s, which rounds x and h to 4 bits.
+    In both, scores of -inf mask experts: weight 0 and nothing added, whatever the expert's weights
+    hold; a token with every expert masked gets the shared experts' output, or 0.
     """
 
     def __init__(self, H: int, I: int, E: int, k: int, renormalize: bool = True, device="cuda"):

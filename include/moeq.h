@@ -128,7 +128,10 @@ int moe_router_logits(const void* x, int x_dtype, int T, int H, const float* w_r
  * the sum over the k selected experts (renormalize != 0) or over all E experts
  * (renormalize == 0).
  *
- *   logits    [T, E] fp32, finite       bias  [E] fp32 or NULL
+ * A score of -inf marks a masked expert (weight 0); a token whose scores are all
+ * -inf gets weights 0.
+ *
+ *   logits    [T, E] fp32, finite or -inf   bias  [E] fp32 or NULL
  *   topk_ids  [T, k] int32 (out)        topk_w [T, k] fp32 (out)
  * Limits: 1 <= E <= MOEQ_MAX_EXPERTS, 1 <= k <= min(E, MOEQ_MAX_TOPK), T >= 0.
  */
@@ -499,7 +502,8 @@ int moe_expert_mlp_fp8row(const uint8_t* xp_q, const float* xp_s, const void* pl
  *
  * Not on the pages; the reading implemented (fp32 accumulation in slot order):
  *   y[t, c] = bf16( sum_{j=0}^{k-1} w[t, j] * o[row_pos[t*k + j], c] + shared[t, c] )
- * Rows dropped by moe_permute contribute nothing.
+ * Rows dropped by moe_permute contribute nothing, and neither does a row of weight
+ * 0, whatever it holds (a masked expert's).
  *
  *   o [R, H] bf16 in plan order (R = T*k)
  *   plan, plan_bytes -- from moe_permute with E and R = T*k (read only)

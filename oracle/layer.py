@@ -62,6 +62,7 @@ def route_topk(logits, k: int, bias=None, renormalize: bool = True):
     broken toward the lower expert index, listed best first.  Weights:
     renormalize=True  -> w_j = exp(s_j - s_max) / sum over the k selected
     renormalize=False -> w_j = exp(s_j - s_max) / sum over all E experts
+    A score of -inf (a masked expert) has weight 0; all -inf -> weights 0.
     Returns ids int32 [T, k] and weights float64 [T, k].
     """
     s = np.asarray(logits, dtype=np.float32)
@@ -76,9 +77,11 @@ def route_topk(logits, k: int, bias=None, renormalize: bool = True):
     ids = order[:, :k].astype(np.int32)
     sel = np.take_along_axis(s, ids.astype(np.int64), axis=1)
     smax = s.max(axis=1, keepdims=True)
+    none = smax == -np.inf
+    smax = np.where(none, 0.0, smax)
     num = np.exp(sel - smax)
     den = num.sum(axis=1, keepdims=True) if renormalize else np.exp(s - smax).sum(axis=1, keepdims=True)
-    return ids, num / den
+    return ids, num / np.where(none, 1.0, den)
 
 # ------------------------------------------------ a2 / a5: per-token FP8 quant
 

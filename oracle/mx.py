@@ -75,13 +75,8 @@ def grouped_rows(a, experts, w):
 
 def few_layer(logits, x, w13, w2, k, bias=None, renormalize=True, shared=None):
     """The few-token layer on weight values w13 [E, 2I, H], w2 [E, H, I], in float64 throughout
-    (h unrounded); tokens whose best score is -inf get weights 0."""
-    with np.errstate(invalid="ignore"):
-        ids, wt = L.route_topk(logits, k, bias, renormalize)
-    s = np.asarray(logits, dtype=np.float32)
-    if bias is not None:
-        s = s + np.asarray(bias, dtype=np.float32)[None, :]
-    wt = np.where(s.max(axis=1, keepdims=True) == -np.inf, 0.0, wt)
+    (h unrounded)."""
+    ids, wt = L.route_topk(logits, k, bias, renormalize)
     T, I = x.shape[0], w2.shape[2]
     y = np.zeros((T, w2.shape[1]))
     for t in range(T):

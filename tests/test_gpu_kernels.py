@@ -761,3 +761,46 @@ def test_read_bandwidth_probe_reads_every_word(nbytes):
     got = np.bitwise_xor.reduce(sink.cpu().numpy().view(np.uint32))
     assert int(got) == int(np.bitwise_xor.reduce(words))
 
+
+
+# ------------------------------------------------------------ masked experts ----
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("T", [3, 20])                 # one launch, and the separate calls
+def test_route_of_a_fully_masked_token(T, renorm):
+    """A token whose scores are all -inf gets weights 0 in either routing call, others as before."""
+    E, k, H = 12, 3, 128
+    g = torch.Generator().manual_seed(T)
+    logits = torch.randn(T, E, generator=g)
+    clean = logits.clone()
+    logits[1, :] = float("-inf")
+    bias = torch.randn(E, generator=g)
+    x = torch.randn(T, H, generator=g).to(_dev())
+    rid, rw = L.route_topk(logits.numpy(), k, bias.numpy(), renorm)
+    assert rid[1].tolist() == [0, 1, 2] and (rw[1] == 0).all()
+    cid, cw = mq.moe_route_topk(clean.to(_dev()), k, bias.to(_dev()), renorm)
+    fused = mq.moe_route_quant_permute(logits.to(_dev()), x, k, bias.to(_dev()), renorm)
+    for ids, w in (mq.moe_route_topk(logits.to(_dev()), k, bias.to(_dev()), renorm),
+                   tuple(fused[n] for n in ("ids", "w"))):
+        np.testing.assert_array_equal(ids.cpu().numpy(), rid)
+        assert (w[1] == 0).all()
+        rest = [t for t in range(T) if t != 1]
+        assert torch.equal(ids[rest], cid[rest]) and torch.equal(w[rest], cw[rest])
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_combine_leaves_out_rows_of_weight_zero(bad):
+    T, k, E, H = 5, 3, 6, 264
+    g = torch.Generator().manual_seed(3)
+    ids = torch.rand(T, E, generator=g).topk(k, dim=1).indices.to(torch.int32).to(_dev())
+    plan, _, _ = mq.moe_permute(ids, E)
+    o = torch.randn(T * k, H, generator=g).to(torch.bfloat16).to(_dev())
+    w = torch.rand(T, k, generator=g).to(_dev())
+    w[1, 2] = w[4, 0] = 0.0
+    shared = torch.randn(T, H, generator=g).to(torch.bfloat16).to(_dev())
+    clean = mq.moe_combine(o, plan, w, shared, E=E)
+    sorted_rows = L.permute_plan(ids.cpu().numpy(), E)["sorted_rows"]
+    for r in (1 * k + 2, 4 * k + 0):
+        o[int(np.nonzero(sorted_rows == r)[0][0])] = bad
+    assert torch.equal(mq.moe_combine(o, plan, w, shared, E=E), clean)
+    o[int(np.nonzero(sorted_rows == 0)[0][0])] = bad       # a row of another weight still counts
+    assert not torch.isfinite(mq.moe_combine(o, plan, w, shared, E=E)[0]).any()

@@ -675,3 +675,40 @@ def test_mx_layer_no_tokens_and_too_many():
     with pytest.raises(ValueError, match="16 tokens"):
         layer.forward_few(x, logits)
     assert torch.equal(layer.forward(x, logits)[:16], layer.forward(x[:16], logits[:16]))
+
+
+@pytest.mark.parametrize("T", [6, 40])
+@pytest.mark.parametrize("shared", [False, True])
+def test_mx_layer_masked_experts_and_tokens(T, shared):
+    """Both forms follow one rule: a token whose scores are all -inf gets weights 0 and keeps the
+    shared experts' part; an expert of weight 0 adds nothing, whatever its weights hold."""
+    k, E, H, I, S = 3, 8, 256, 96, 64
+    g = gen(T)
+    layer = mq.MxMoELayer(H, I, E, k, device=DEV)
+    layer.quantize_weights((torch.randn(E, 2 * I, H, generator=g) * .1).to(DEV),
+                           (torch.randn(E, H, I, generator=g) * .1).to(DEV))
+    if shared:
+        layer.set_shared((torch.randn(2 * S, H, generator=g) * .1).to(torch.bfloat16).to(DEV),
+                         (torch.randn(H, S, generator=g) * .1).to(torch.bfloat16).to(DEV))
+    x = torch.randn(T, H, generator=g).to(torch.bfloat16).to(DEV)
+    logits = torch.randn(T, E, generator=g)
+    logits[:, 0] = float("-inf")                     # expert 0 is masked for every token
+    logits[1, 2:] = float("-inf")                    # one expert left: masked ones fill the slots
+    logits[T - 1, :] = float("-inf")                 # none left
+    logits = logits.to(DEV)
+    forms = [layer.forward] + ([layer.forward_few] if T <= mq.FEW_TOKENS else [])
+    clean = [fn(x, logits).clone() for fn in forms]
+    ids = [fn(x, logits, return_all=True)["ids"].clone() for fn in forms]
+    assert (ids[0][1] == 0).any() and (ids[0][T - 1] == 0).any()
+    layer.s13[0].fill_(255)                          # expert 0: every block a NaN
+    layer.s2[0].fill_(255)
+    own = torch.zeros(H, dtype=torch.bfloat16, device=DEV)
+    if shared:
+        own = mq.moe_shared_gemm_bf16(mq.moe_shared_gemm_bf16(x, layer.ws13, mq.EPI_SILU_MUL),
+                                      layer.ws2)[T - 1]
+    for fn, before, i in zip(forms, clean, ids):
+        b = fn(x, logits, return_all=True)
+        assert torch.equal(b["ids"], ids[0]) and torch.equal(i, ids[0])
+        assert b["w"][1].tolist() == [1.0, 0.0, 0.0] and b["w"][T - 1].tolist() == [0.0] * k
+        assert torch.isfinite(before).all() and torch.equal(b["y"], before)
+        assert torch.equal(b["y"][T - 1], own)

@@ -518,3 +518,12 @@ def test_layer_fp8row_variant_runs_and_is_close():
     ref = L.unquantized_layer(inp["x"].float().numpy(), inp["logits"].numpy(), cfg.k,
                               inp["w13"].numpy(), inp["w2"].numpy())
     assert np.linalg.norm(res["y"] - ref) / np.linalg.norm(ref) < 0.1
+
+
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_routing_of_masked_experts(renormalize):
+    s = np.array([[-np.inf, 1.0, -np.inf, 0.0], [-np.inf] * 4, [-np.inf, -np.inf, 5.0, -np.inf]])
+    ids, w = L.route_topk(s, 3, renormalize=renormalize)
+    assert ids.tolist() == [[1, 3, 0], [0, 1, 2], [2, 0, 1]]
+    e = np.exp(-1.0)
+    np.testing.assert_allclose(w, [[1 / (1 + e), e / (1 + e), 0], [0, 0, 0], [1, 0, 0]], rtol=1e-15)

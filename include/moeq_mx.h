@@ -104,7 +104,8 @@ size_t moe_layer_mxfp4_few_ws_size(int T, int k, int H, int I);
  * moe_layer_mxfp4_few -- a whole expert layer for T <= MOEQ_FEW_TOKENS tokens in
  * two kernels, with MXFP4 weights and bf16 activations:
  *   topk_ids, topk_w    as moe_route_topk (logits, bias, k, renormalize)
- *   h_j = silu(Wg_e x_t) * (Wu_e x_t),  e = topk_ids[t, j]   (fp32)
+ *   h_j = silu(Wg_e x_t) * (Wu_e x_t),  e = topk_ids[t, j]   (fp32; bits below 2^-133 are
+ *         cut off)
  *   y_t = bf16( sum_j topk_w[t, j] * (W2_e h_j) + shared_t )  (fp32 sums in slot order)
  * Nothing is quantized but the weights; y is rounded once.  Scores of -inf mark masked experts and
  * get weight 0; a token whose k best scores are all -inf gets weights 0 (y_t =

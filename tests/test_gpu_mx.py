@@ -442,6 +442,23 @@ def test_few_layer_empty_and_refusals():
         f.run()
 
 
+@pytest.mark.parametrize("T,k,E,H,I", [(1, 1, 1, 32, 32), (4, 2, 8, 512, 128), (16, 8, 9, 96, 544),
+                                       (16, 8, 200, 1440, 352)])
+def test_few_layer_stays_inside_its_workspace_and_outputs(T, k, E, H, I):
+    """Every buffer is a slice of a larger one, exactly as long as the call asks for."""
+    f = Few(T, k, E, H, I, T + E)
+    sizes = {"ws": mq.moe_layer_mxfp4_few_ws_size(T, k, H, I), "ids": T * k * 4, "w": T * k * 4,
+             "y": T * H * 2}
+    dtypes = {"ws": torch.uint8, "ids": torch.int32, "w": torch.float32, "y": torch.bfloat16}
+    bufs = {n: torch.full((256 + b + 256,), 0xA5, dtype=torch.uint8, device=DEV)
+            for n, b in sizes.items()}
+    out = {n: bufs[n][256:256 + b].view(dtypes[n]) for n, b in sizes.items()}
+    out["ids"], out["w"], out["y"] = out["ids"].view(T, k), out["w"].view(T, k), out["y"].view(T, H)
+    f.check(f.run(out=out))
+    for n, b in sizes.items():
+        assert (bufs[n][:256] == 0xA5).all() and (bufs[n][256 + b:] == 0xA5).all(), n
+
+
 def test_few_layer_two_streams_with_their_own_workspaces():
     a, b = Few(8, 4, 20, 512, 256, 20), Few(16, 3, 20, 1024, 96, 21)
     ra, rb = a.run()["y"].clone(), b.run()["y"].clone()
@@ -602,6 +619,43 @@ def test_mx_layer_captured_and_replayed(T):
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(y, expect), rep
+
+
+@pytest.mark.parametrize("T", [2, 16, 70])
+def test_mx_layer_replay_computes_every_step(T):
+    """Between the eager call and the replay every intermediate is filled from other inputs, so a
+    step missing from the graph shows."""
+    k, E, H, I, S = 3, 12, 512, 256, 64
+    g = gen(T + 1)
+    layer = mq.MxMoELayer(H, I, E, k, device=DEV)
+    layer.quantize_weights((torch.randn(E, 2 * I, H, generator=g) * .1).to(DEV),
+                           (torch.randn(E, H, I, generator=g) * .1).to(DEV))
+    layer.set_router((torch.randn(E, H, generator=g) / 16).to(DEV))
+    layer.set_shared((torch.randn(2 * S, H, generator=g) * .1).to(torch.bfloat16).to(DEV),
+                     (torch.randn(H, S, generator=g) * .1).to(torch.bfloat16).to(DEV))
+    new = lambda: torch.randn(T, H, generator=g).to(torch.bfloat16).to(DEV)  # noqa: E731
+    x = new()
+    for fn in [layer.forward] + ([layer.forward_few] if T <= mq.FEW_TOKENS else []):
+        fn(x)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            b = fn(x, return_all=True)
+        for rep in range(4):
+            wanted = new()
+            x.copy_(wanted)
+            expect = {n: t.clone() for n, t in fn(x, return_all=True).items()}
+            x.copy_(new())
+            fn(x)                                       # other values in every buffer
+            torch.cuda.synchronize()
+            assert not any(torch.equal(b[n], expect[n]) for n in b if n != "logits"), rep
+            b["y"].fill_(float("nan"))
+            x.copy_(wanted)
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            for n in ("ids", "w", "y"):
+                assert torch.equal(b[n], expect[n]), (rep, n)
 
 
 def test_mx_layer_with_router_and_shared_experts():

@@ -126,6 +126,15 @@ def test_few_layer_refusals():
     assert call(T=0, logits=N, x=N, ws=N) == OK
 
 
+@pytest.mark.parametrize("T,k,H,I", [(1, 1, 32, 32), (4, 2, 64, 96), (16, 8, 4096, 2048),
+                                     (16, 8, 1 << 20, 1 << 20), (3, 5, 1440, 544)])
+def test_few_layer_workspace_holds_every_part(T, k, H, I):
+    """h as three bf16 values, o in fp32 and a counter per 32 columns, each part on 256 bytes."""
+    R = T * k
+    parts = (R * I * 6, R * H * 4, H // 32 * 4)
+    assert mq.moe_layer_mxfp4_few_ws_size(T, k, H, I) == sum((n + 255) // 256 * 256 for n in parts)
+
+
 @pytest.mark.skipif(torch.cuda.is_available(), reason="would launch on fake pointers")
 def test_valid_calls_without_gpu_report_device_error():
     L = mq.lib

@@ -11,6 +11,7 @@ calls with the same token count, and every step is a C-ABI call into libmoeq.
 """
 from __future__ import annotations
 
+import functools
 from typing import Optional
 
 import torch
@@ -21,6 +22,19 @@ from . import (EPI_NONE, EPI_SILU_MUL, moe_combine, moe_expert_mlp_fp8row, moe_e
                moe_plan_size,
                moe_requant_fp8_fnuz, moe_route_quant_permute, moe_route_topk, moe_router_logits, moe_shared_gemm_bf16, pack_int4_g128,
                quant_fp8_per_token, quant_mxfp4, tile_mxfp4_weights)
+
+
+def _on_x_device(forward):
+    """Runs forward(self, x, ...) with x's device current: kernels are launched on the current
+    stream of the tensors' device, which has to be the current device for that."""
+    @functools.wraps(forward)
+    def call(self, x, *args, **kw):
+        i = x.get_device()
+        if i < 0 or i == torch.cuda.current_device():
+            return forward(self, x, *args, **kw)
+        with torch.cuda.device(i):
+            return forward(self, x, *args, **kw)
+    return call
 
 
 class MoELayer:
@@ -106,6 +120,7 @@ class MoELayer:
         return b
 
     # ---------------------------------------------------------------- forward
+    @_on_x_device
     def forward(self, x: torch.Tensor, logits: Optional[torch.Tensor] = None,
                 bias: Optional[torch.Tensor] = None,
                 return_all: bool = False, events: Optional[list] = None,
@@ -203,6 +218,7 @@ class HybridMoELayer(MoELayer):
                                   slab_of=self.cold_of)
         return out
 
+    @_on_x_device
     def forward(self, x: torch.Tensor, logits: Optional[torch.Tensor] = None,
                 bias: Optional[torch.Tensor] = None, return_all: bool = False,
                 events: Optional[list] = None, split_mlp: bool = True):
@@ -317,6 +333,7 @@ class MxMoELayer(MoELayer):
             return r
         return step
 
+    @_on_x_device
     def forward(self, x: torch.Tensor, logits: Optional[torch.Tensor] = None,
                 bias: Optional[torch.Tensor] = None, return_all: bool = False,
                 events: Optional[list] = None):
@@ -334,6 +351,7 @@ class MxMoELayer(MoELayer):
         step("combine", moe_combine, b["o"], b["plan"], b["w"], shared, y=b["y"], E=self.E)
         return b if return_all else b["y"]
 
+    @_on_x_device
     def forward_few(self, x: torch.Tensor, logits: Optional[torch.Tensor] = None,
                     bias: Optional[torch.Tensor] = None, return_all: bool = False,
                     events: Optional[list] = None):

@@ -647,6 +647,11 @@ unsigned few_lds_bytes(int T, int planes, int K) {
 // 14.8, 10.2 with two; four 36.9, 20.6 with one, 37.5, 22.2 with two, 37.9, 24.6 with
 // four; sixteen 142.5, 83.0 with one, 115.3, 71.8 with two, 110.6, 70.6 with three,
 // 105.8, 73.4 with four, 112.5, 84.2 with six.
+// R counts every routed row, those that leave at once too: they route before they
+// leave.  Sized by the rows that can stay, min(R, E): sixteen tokens, top-8 of 8,
+// 4096 x 2048, 102, 86 against 40, 46; top-4 of 32, 2880 x 2880, 88, 60 against 64, 60.
+// Launches of 1500 and 2048: sixteen tokens, top-2 of 8, 26.5, 25.8 against 33.5, 29.7,
+// but eight, top-6 of 256, 67.5, 42.6 against 67.0, 39.6.
 int few_units_per_wg(int R, int units, int launch) {
   const int64_t n = int64_t(R) * units / launch;
   return n < 1 ? 1 : n > 4 ? 4 : int(n);

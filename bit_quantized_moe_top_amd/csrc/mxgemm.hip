@@ -15,8 +15,11 @@
 //    LDS, weights straight to registers.  2048 tokens, top-6 of 256, 4096 x 4096
 //    gate/up in 386 us, 6.0 TB/s of HBM (95% of a pure read); Zipf-popular experts,
 //    4096 x 2048 down 237 us, 5.3 TB/s (equal items per XCD, but not equal weight
-//    streams); one expert of 8192 rows 2.5 PFLOP/s, bound by the weights' way from
-//    L2 (64 B per clock and CU feed a 64-row tile at the matrix rate).
+//    streams).  Experts of hundreds of rows are not bound by HBM: one of 8192 rows
+//    105 us, 2.6 PFLOP/s of the 8.0 that the matrix instruction reaches from registers
+//    (384 rows each of 256 experts: 2.5).  No unit is full there: matrix units busy
+//    0.33, VALU 0.42, L2 to each CU 27 B per clock, waves waiting 0.35 of their time;
+//    a weight is used for 64 rows, two waves share a SIMD and meet every 512 K.
 #include "front.hpp"
 #include "mx.hpp"
 

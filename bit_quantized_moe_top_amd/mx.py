@@ -154,7 +154,10 @@ def dequant_mxfp4(q: torch.Tensor, scale: torch.Tensor, out: Optional[torch.Tens
 
 def tile_mxfp4_weights(q: torch.Tensor, scale: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     """Weights [E, N, K] in rows (codes [E, N, K/2], scales [E, N, K/32]) -> the products'
-    tiled order (codes [E, N/16, G, 4, 64, 16], scales [E, N/16, G, 64, 4], G = ceil(K / 512))."""
+    tiled order (codes [E, N/16, G, 4, 64, 16], scales [E, N/16, G, 64, 4], G = ceil(K / 512)).
+    The shapes tell K only to whole super-groups of 512.  The codes' tensor remembers K, and a call
+    with another one is refused; a copy of it (.to, .clone, a loaded checkpoint) does not, and a
+    call with another K of as many super-groups then reads zeros for the rest."""
     K, dev = _codes(q, scale, "q", 3)
     E, N = q.shape[:2]
     if N % 16 != 0 or K == 0:

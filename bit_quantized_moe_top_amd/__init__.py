@@ -689,6 +689,8 @@ from .mx import *  # noqa: E402,F401,F403  (the MXFP4 calls)
 from .mx import __all__ as _mx_all  # noqa: E402
 from .route import *  # noqa: E402,F401,F403  (expert routing)
 from .route import __all__ as _route_all  # noqa: E402
+from .lora import *  # noqa: E402,F401,F403  (the shared projection with adapters)
+from .lora import __all__ as _lora_all  # noqa: E402
 from .layer import HybridMoELayer, MoELayer, MxMoELayer  # noqa: E402,F401  (composition of the calls above)
 
-__all__ += _mx_all + _route_all
+__all__ += _mx_all + _route_all + _lora_all

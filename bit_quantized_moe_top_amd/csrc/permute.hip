@@ -19,15 +19,25 @@
 //                       row_pos (place_gather_kernel: one workgroup per row,
 //                       which also copies the row's activation bytes and scale).
 #include "front.hpp"
+#include "lora_kernels.hpp"
 
 namespace moeq {
 
 namespace {
 
+// The expert of a routed row: its id as given (outside [0, E): dropped), or, in an adapter
+// plan (kOthers), the last group for every id outside [0, E - 1).
+template <bool kOthers>
+__device__ __forceinline__ int row_group(const int32_t* ids, int r, int E) {
+  const int e = ids[r];
+  return kOthers && (e < 0 || e >= E - 1) ? E - 1 : e;
+}
+
+template <bool kOthers>
 __global__ void __launch_bounds__(kPlanThreads)
 plan_kernel(const int32_t* __restrict__ ids, int T, int k, int E, int32_t* __restrict__ plan) {
   extern __shared__ int smem[];
-  plan_build_workgroup([&](int r) { return ids[r]; }, T, k, E, plan, smem);
+  plan_build_workgroup([&](int r) { return row_group<kOthers>(ids, r, E); }, T, k, E, plan, smem);
 }
 
 // one thread per 16-byte chunk of a destination row
@@ -48,6 +58,7 @@ gather_kernel(const uint8_t* __restrict__ x_q, const float* __restrict__ x_s, in
   if (ch == 0) xp_s[p] = x_s[t];
 }
 
+template <bool kOthers>
 __global__ void __launch_bounds__(kPlanThreads)
 chunk_rank_kernel(const int32_t* __restrict__ ids, int T, int k, int E, int32_t* __restrict__ plan) {
   extern __shared__ int wcnt[];           // [kPlanWaves][E]
@@ -58,7 +69,7 @@ chunk_rank_kernel(const int32_t* __restrict__ ids, int T, int k, int E, int32_t*
   for (int i = tid; i < kPlanWaves * E; i += kPlanThreads) wcnt[i] = 0;
   __syncthreads();
   const int r = c * kPlanChunk + tid;
-  int e = (r < R) ? ids[r] : -1;
+  int e = (r < R) ? row_group<kOthers>(ids, r, E) : -1;
   if (e >= E) e = -1;
   int gsize;
   const int rank = wave_rank(e, lane, &gsize);
@@ -129,8 +140,9 @@ plan_scan_kernel(int T, int k, int E, int32_t* __restrict__ plan) {
 
 // position of routed row r: its chunk's base for its expert plus its rank in
 // the chunk (parked in row_pos by chunk_rank_kernel); -1 for a dropped id
+template <bool kOthers>
 __device__ __forceinline__ int place_row(const int32_t* ids, int r, int E, PlanView& pv) {
-  const int e = ids[r];
+  const int e = row_group<kOthers>(ids, r, E);
   if (e < 0 || e >= E) return -1;
   const int pos = pv.scratch[(r / kPlanChunk) * E + e] + pv.row_pos[r];
   pv.sorted_rows[pos] = r;
@@ -139,12 +151,13 @@ __device__ __forceinline__ int place_row(const int32_t* ids, int r, int E, PlanV
 }
 
 // plan only: one thread per routed row
+template <bool kOthers>
 __global__ void __launch_bounds__(256)
 place_kernel(const int32_t* __restrict__ ids, int T, int k, int E, int32_t* __restrict__ plan) {
   const int R = T * k;
   PlanView pv = plan_view(plan, E, R);
   const int r = blockIdx.x * 256 + threadIdx.x;
-  if (r < R) place_row(ids, r, E, pv);
+  if (r < R) place_row<kOthers>(ids, r, E, pv);
 }
 
 // with the gather: one workgroup per routed row, 16 bytes per thread per step
@@ -157,7 +170,7 @@ place_gather_kernel(const int32_t* __restrict__ ids, int T, int k, int E,
   const int R = T * k;
   PlanView pv = plan_view(plan, E, R);
   const int r = blockIdx.x;
-  if (threadIdx.x == 0) s_pos = place_row(ids, r, E, pv);
+  if (threadIdx.x == 0) s_pos = place_row<false>(ids, r, E, pv);
   __syncthreads();
   const int pos = s_pos;
   if (pos < 0) return;
@@ -190,7 +203,7 @@ quant_scatter_kernel(const int32_t* __restrict__ ids, int T, int k, int E,
   RowQuant<XT, CPL> rq;
   rq.load(x + int64_t(t) * H, H, lane);
   int pos = -1;
-  if (lane < k) pos = kPlace ? place_row(ids, t * k + lane, E, pv) : pv.row_pos[t * k + lane];
+  if (lane < k) pos = kPlace ? place_row<false>(ids, t * k + lane, E, pv) : pv.row_pos[t * k + lane];
   rq.finish(H, lane);
   rq.store(x_q + int64_t(t) * H, H, lane);
   if (lane == 0) x_s[t] = rq.scale;
@@ -220,7 +233,7 @@ quant_scatter_quarter_kernel(const int32_t* __restrict__ ids, int T, int k, int 
   QuarterRowQuant<XT, CPQ> rq;
   rq.load(x + int64_t(t) * H, H, w, lane);
   if (w == 0 && lane < k)
-    s_pos[lane] = kPlace ? place_row(ids, t * k + lane, E, pv) : pv.row_pos[t * k + lane];
+    s_pos[lane] = kPlace ? place_row<false>(ids, t * k + lane, E, pv) : pv.row_pos[t * k + lane];
   rq.finish(w, lane, part);               // its barrier also publishes s_pos
   rq.store(x_q + int64_t(t) * H, lane);
   if (threadIdx.x == 0) x_s[t] = rq.scale;
@@ -247,8 +260,8 @@ hipError_t launch_permute(const int32_t* ids, int T, int k, int E, const uint8_t
   hipError_t err;
   if (R <= kPlanChunk) {
     const size_t lds = size_t(E) * (1 + kPlanWaves) * sizeof(int);
-    if ((err = set_lds(reinterpret_cast<const void*>(&plan_kernel), lds)) != hipSuccess) return err;
-    hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(kPlanThreads), lds, stream, ids, T, k, E, p);
+    if ((err = set_lds(reinterpret_cast<const void*>(&plan_kernel<false>), lds)) != hipSuccess) return err;
+    hipLaunchKernelGGL(plan_kernel<false>, dim3(1), dim3(kPlanThreads), lds, stream, ids, T, k, E, p);
     if ((err = hipGetLastError()) != hipSuccess || x_q == nullptr || R == 0) return err;
     const int64_t blocks = (int64_t(R) * (H / 16) + 255) / 256;
     hipLaunchKernelGGL(gather_kernel, dim3(unsigned(blocks)), dim3(256), 0, stream, x_q, x_s, H, k,
@@ -256,19 +269,42 @@ hipError_t launch_permute(const int32_t* ids, int T, int k, int E, const uint8_t
     return hipGetLastError();
   }
   const size_t lds_rank = size_t(E) * kPlanWaves * sizeof(int);
-  if ((err = set_lds(reinterpret_cast<const void*>(&chunk_rank_kernel), lds_rank)) != hipSuccess)
+  if ((err = set_lds(reinterpret_cast<const void*>(&chunk_rank_kernel<false>), lds_rank)) != hipSuccess)
     return err;
-  hipLaunchKernelGGL(chunk_rank_kernel, dim3(plan_chunks(R)), dim3(kPlanThreads), lds_rank, stream,
+  hipLaunchKernelGGL(chunk_rank_kernel<false>, dim3(plan_chunks(R)), dim3(kPlanThreads), lds_rank, stream,
                      ids, T, k, E, p);
   if ((err = hipGetLastError()) != hipSuccess) return err;
   hipLaunchKernelGGL(plan_scan_kernel, dim3(1), dim3(kPlanThreads), size_t(E) * sizeof(int), stream,
                      T, k, E, p);
   if ((err = hipGetLastError()) != hipSuccess) return err;
   if (x_q == nullptr)
-    hipLaunchKernelGGL(place_kernel, dim3((R + 255) / 256), dim3(256), 0, stream, ids, T, k, E, p);
+    hipLaunchKernelGGL(place_kernel<false>, dim3((R + 255) / 256), dim3(256), 0, stream, ids, T, k, E, p);
   else
     hipLaunchKernelGGL(place_gather_kernel, dim3(R), dim3(256), 0, stream, ids, T, k, E, p, x_q, x_s,
                        H, xp_q, xp_s);
+  return hipGetLastError();
+}
+
+hipError_t launch_adapter_plan(const int32_t* ids, int M, int L, void* plan, hipStream_t stream) {
+  const int E = L + 1;
+  int32_t* p = static_cast<int32_t*>(plan);
+  hipError_t err;
+  if (M <= kPlanChunk) {
+    const size_t lds = size_t(E) * (1 + kPlanWaves) * sizeof(int);
+    if ((err = set_lds(reinterpret_cast<const void*>(&plan_kernel<true>), lds)) != hipSuccess) return err;
+    hipLaunchKernelGGL(plan_kernel<true>, dim3(1), dim3(kPlanThreads), lds, stream, ids, M, 1, E, p);
+    return hipGetLastError();
+  }
+  const size_t lds_rank = size_t(E) * kPlanWaves * sizeof(int);
+  if ((err = set_lds(reinterpret_cast<const void*>(&chunk_rank_kernel<true>), lds_rank)) != hipSuccess)
+    return err;
+  hipLaunchKernelGGL(chunk_rank_kernel<true>, dim3(plan_chunks(M)), dim3(kPlanThreads), lds_rank, stream,
+                     ids, M, 1, E, p);
+  if ((err = hipGetLastError()) != hipSuccess) return err;
+  hipLaunchKernelGGL(plan_scan_kernel, dim3(1), dim3(kPlanThreads), size_t(E) * sizeof(int), stream,
+                     M, 1, E, p);
+  if ((err = hipGetLastError()) != hipSuccess) return err;
+  hipLaunchKernelGGL(place_kernel<true>, dim3((M + 255) / 256), dim3(256), 0, stream, ids, M, 1, E, p);
   return hipGetLastError();
 }
 
@@ -282,13 +318,13 @@ hipError_t launch_permute_quant(const int32_t* ids, int T, int k, int E, const v
   const bool place = R > kPlanChunk;
   if (!place) {
     const size_t lds = size_t(E) * (1 + kPlanWaves) * sizeof(int);
-    if ((err = set_lds(reinterpret_cast<const void*>(&plan_kernel), lds)) != hipSuccess) return err;
-    hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(kPlanThreads), lds, stream, ids, T, k, E, p);
+    if ((err = set_lds(reinterpret_cast<const void*>(&plan_kernel<false>), lds)) != hipSuccess) return err;
+    hipLaunchKernelGGL(plan_kernel<false>, dim3(1), dim3(kPlanThreads), lds, stream, ids, T, k, E, p);
   } else {
     const size_t lds_rank = size_t(E) * kPlanWaves * sizeof(int);
-    if ((err = set_lds(reinterpret_cast<const void*>(&chunk_rank_kernel), lds_rank)) != hipSuccess)
+    if ((err = set_lds(reinterpret_cast<const void*>(&chunk_rank_kernel<false>), lds_rank)) != hipSuccess)
       return err;
-    hipLaunchKernelGGL(chunk_rank_kernel, dim3(plan_chunks(R)), dim3(kPlanThreads), lds_rank,
+    hipLaunchKernelGGL(chunk_rank_kernel<false>, dim3(plan_chunks(R)), dim3(kPlanThreads), lds_rank,
                        stream, ids, T, k, E, p);
     if ((err = hipGetLastError()) != hipSuccess) return err;
     hipLaunchKernelGGL(plan_scan_kernel, dim3(1), dim3(kPlanThreads), size_t(E) * sizeof(int),

@@ -16,12 +16,15 @@ from typing import Optional
 
 import torch
 
-from . import (EPI_NONE, EPI_SILU_MUL, moe_combine, moe_expert_mlp_fp8row, moe_expert_mlp_w4a8,
+from . import (EPI_NONE, EPI_SILU_MUL, SCORE_SIGMOID, moe_combine, moe_expert_mlp_fp8row, moe_expert_mlp_w4a8,
                moe_grouped_gemm_aqlm, moe_grouped_gemm_fp8row, moe_grouped_gemm_nvfp4,
                moe_grouped_gemm_mxfp4, moe_grouped_gemm_w4a8, moe_layer_mxfp4_few, moe_permute,
                moe_plan_size,
-               moe_requant_fp8_fnuz, moe_route_quant_permute, moe_route_topk, moe_router_logits, moe_shared_gemm_bf16, pack_int4_g128,
+               moe_requant_fp8_fnuz, moe_route_experts, moe_route_quant_permute, moe_route_topk,
+               moe_router_logits, moe_shared_gemm_bf16, moe_shared_gemm_lora_bf16,
+               moe_shared_gemm_lora_ws_size, pack_int4_g128,
                quant_fp8_per_token, quant_mxfp4, tile_mxfp4_weights)
+from .route import _check_options
 
 
 def _on_x_device(forward):
@@ -56,7 +59,10 @@ class MoELayer:
         self.w13 = self.s13 = self.w2 = self.s2 = None
         self.ws13 = self.ws2 = None
         self.w_router = None
+        self.routing = None
+        self.adapters = None
         self._bufs = {}
+        self._adapter_ws = {}
 
     # --------------------------------------------------------------- weights
     def set_weights(self, w13, s13, w2, s2):
@@ -88,8 +94,28 @@ class MoELayer:
         them with moe_router_logits."""
         self.w_router = w_router
 
+    def set_routing(self, scoring: Optional[int] = SCORE_SIGMOID, n_group: int = 1,
+                    topk_group: int = 1, group_best: int = 1, scale: float = 1.0):
+        """Routing by moe_route_experts: scores, groups, weights times scale, and forward()'s bias
+        moves the choice of experts only.  scoring=None: back to moe_route_topk, where the bias is
+        part of the softmax."""
+        if scoring is None:
+            self.routing = None
+            return
+        _check_options(self.E, self.k, scoring, n_group, topk_group, group_best, scale)
+        self.routing = dict(scoring=scoring, n_group=n_group, topk_group=topk_group,
+                            group_best=group_best, scale=scale)
+
     def set_shared(self, ws13: Optional[torch.Tensor], ws2: Optional[torch.Tensor]):
         self.ws13, self.ws2 = ws13, ws2
+
+    def set_shared_adapters(self, a13: Optional[torch.Tensor], b13: Optional[torch.Tensor] = None,
+                            a2: Optional[torch.Tensor] = None, b2: Optional[torch.Tensor] = None,
+                            scale: Optional[torch.Tensor] = None):
+        """Low-rank adapters of the shared experts, used where forward() is given an adapter_plan
+        (moe_adapter_plan of the batch): a13 [L, 1 or 2, r, H], b13 [L, 2S, r] beside gate/up, a2
+        [L, 1, r, S], b2 [L, H, r] beside down, scale [L] fp32.  a13=None: no adapters."""
+        self.adapters = None if a13 is None else (a13, b13, a2, b2, scale)
 
     # ---------------------------------------------------------------- buffers
     def buffers(self, T: int) -> dict:
@@ -119,16 +145,69 @@ class MoELayer:
             self._bufs[T] = b
         return b
 
+    def _lora_ws(self, T: int) -> torch.Tensor:
+        """The workspace of the shared experts' two products with adapters, one per batch size and
+        set of shapes (earlier ones stay, since a captured graph may hold them)."""
+        a13, b13, a2, b2, _ = self.adapters
+        key = (T, self.ws13.shape, self.ws2.shape, a13.shape, a2.shape)
+        ws = self._adapter_ws.get(key)
+        if ws is None:
+            n = max(moe_shared_gemm_lora_ws_size(T, *w.shape, *a.shape[:3])
+                    for w, a in ((self.ws13, a13), (self.ws2, a2)))
+            ws = self._adapter_ws[key] = torch.empty(n, dtype=torch.uint8, device=self.device)
+        return ws
+
+    def _shared(self, x, b, step, adapter_plan):
+        """The shared experts' output, with the batch's adapters if there is a plan, or None."""
+        if adapter_plan is not None and (self.adapters is None or self.ws13 is None):
+            raise ValueError("adapter_plan needs shared experts (set_shared) with adapters "
+                             "(set_shared_adapters)")
+        if self.ws13 is None:
+            return None
+        # the shared experts are bf16 MLPs of the bf16 model: their input is x itself
+        if x.dtype != torch.bfloat16:
+            raise TypeError("shared experts take bfloat16 x")
+        if adapter_plan is None:
+            step("shared_gate_up", moe_shared_gemm_bf16, x, self.ws13, EPI_SILU_MUL, out=b["sh_h"])
+            return step("shared_down", moe_shared_gemm_bf16, b["sh_h"], self.ws2, EPI_NONE,
+                        out=b["shared"])
+        a13, b13, a2, b2, scale = self.adapters
+        ws = self._lora_ws(x.shape[0])
+        step("shared_gate_up", moe_shared_gemm_lora_bf16, x, self.ws13, a13, b13, scale,
+             adapter_plan, EPI_SILU_MUL, out=b["sh_h"], ws=ws)
+        return step("shared_down", moe_shared_gemm_lora_bf16, b["sh_h"], self.ws2, a2, b2, scale,
+                    adapter_plan, EPI_NONE, out=b["shared"], ws=ws)
+
+    def _route(self, logits, bias, b, step):
+        """ids and weights of set_routing, or of the plain softmax routing"""
+        if self.routing is None:
+            step("route", moe_route_topk, logits, self.k, bias, self.renormalize, ids=b["ids"],
+                 weights=b["w"])
+        else:
+            step("route", moe_route_experts, logits, self.k, bias=bias,
+                 renormalize=self.renormalize, ids=b["ids"], weights=b["w"], **self.routing)
+
+    def _route_quant_permute(self, logits, x, bias, b, step):
+        if self.routing is None:
+            step("route_quant_permute", moe_route_quant_permute, logits, x, self.k, bias,
+                 self.renormalize, out=b)
+            return
+        self._route(logits, bias, b, step)
+        step("quant_x", quant_fp8_per_token, x, q=b["x_q"], scale=b["x_s"])
+        step("permute", moe_permute, b["ids"], self.E, b["x_q"], b["x_s"], plan=b["plan"],
+             xp_q=b["xp_q"], xp_s=b["xp_s"])
+
     # ---------------------------------------------------------------- forward
     @_on_x_device
     def forward(self, x: torch.Tensor, logits: Optional[torch.Tensor] = None,
                 bias: Optional[torch.Tensor] = None,
                 return_all: bool = False, events: Optional[list] = None,
-                split_mlp: bool = False):
+                split_mlp: bool = False, adapter_plan: Optional[torch.Tensor] = None):
         """y = layer(x).  logits=None: the router's logits are computed from x and the
         weights given to set_router.  With `events` (a list), each call is bracketed by a pair of
         timing events on the current stream, appended as (name, start, end).
-        split_mlp runs the expert MLP as its three separate calls (same results)."""
+        split_mlp runs the expert MLP as its three separate calls (same results).
+        adapter_plan: the batch's moe_adapter_plan, for the shared experts' adapters."""
         T = x.shape[0]
         b = self.buffers(T)
         w4 = self.weight_format != "fp8row"      # INT4 (scale dtype picks the entry point)
@@ -149,8 +228,7 @@ class MoELayer:
             if self.w_router is None:
                 raise ValueError("logits=None needs router weights (set_router)")
             logits = step("router", moe_router_logits, x, self.w_router, out=b["logits"])
-        step("route_quant_permute", moe_route_quant_permute, logits, x, self.k, bias,
-             self.renormalize, out=b)
+        self._route_quant_permute(logits, x, bias, b, step)
         if split_mlp:
             step("gemm_gate_up", gemm, b["xp_q"], b["xp_s"], b["plan"], self.w13, self.s13,
                  epilogue=EPI_SILU_MUL, out=b["h"])
@@ -160,14 +238,7 @@ class MoELayer:
         else:
             step("expert_mlp", mlp, b["xp_q"], b["xp_s"], b["plan"], self.w13, self.s13, self.w2,
                  self.s2, out=b)
-        shared = None
-        if self.ws13 is not None:
-            # the shared experts are bf16 MLPs of the bf16 model: their input is x itself
-            if x.dtype != torch.bfloat16:
-                raise TypeError("shared experts take bfloat16 x")
-            step("shared_gate_up", moe_shared_gemm_bf16, x, self.ws13, EPI_SILU_MUL, out=b["sh_h"])
-            shared = step("shared_down", moe_shared_gemm_bf16, b["sh_h"], self.ws2, EPI_NONE,
-                          out=b["shared"])
+        shared = self._shared(x, b, step, adapter_plan)
         step("combine", moe_combine, b["o"], b["plan"], b["w"], shared, y=b["y"], E=self.E)
         return b if return_all else b["y"]
 
@@ -239,8 +310,7 @@ class HybridMoELayer(MoELayer):
             if self.w_router is None:
                 raise ValueError("logits=None needs router weights (set_router)")
             logits = step("router", moe_router_logits, x, self.w_router, out=b["logits"])
-        step("route_quant_permute", moe_route_quant_permute, logits, x, self.k, bias,
-             self.renormalize, out=b)
+        self._route_quant_permute(logits, x, bias, b, step)
         step("gemm_gate_up", self._gemm_both, b["xp_q"], b["xp_s"], b["plan"], "w13",
              EPI_SILU_MUL, b["h"])
         step("quant_h", quant_fp8_per_token, b["h"], q=b["h_q"], scale=b["h_s"])
@@ -306,19 +376,13 @@ class MxMoELayer(MoELayer):
             self._bufs[T, S] = b
         return b
 
-    def _front(self, x, logits, b, step):
+    def _front(self, x, logits, b, step, adapter_plan=None):
         """(logits, the shared experts' output or None)"""
         if logits is None:
             if self.w_router is None:
                 raise ValueError("logits=None needs router weights (set_router)")
             logits = step("router", moe_router_logits, x, self.w_router, out=b["logits"])
-        if self.ws13 is None:
-            return logits, None
-        if x.dtype != torch.bfloat16:
-            raise TypeError("shared experts take bfloat16 x")
-        step("shared_gate_up", moe_shared_gemm_bf16, x, self.ws13, EPI_SILU_MUL, out=b["sh_h"])
-        return logits, step("shared_down", moe_shared_gemm_bf16, b["sh_h"], self.ws2, EPI_NONE,
-                            out=b["shared"])
+        return logits, self._shared(x, b, step, adapter_plan)
 
     @staticmethod
     def _steps(events):
@@ -336,11 +400,10 @@ class MxMoELayer(MoELayer):
     @_on_x_device
     def forward(self, x: torch.Tensor, logits: Optional[torch.Tensor] = None,
                 bias: Optional[torch.Tensor] = None, return_all: bool = False,
-                events: Optional[list] = None):
+                events: Optional[list] = None, adapter_plan: Optional[torch.Tensor] = None):
         b, step = self.buffers(x.shape[0]), self._steps(events)
-        logits, shared = self._front(x, logits, b, step)
-        step("route", moe_route_topk, logits, self.k, bias, self.renormalize, ids=b["ids"],
-             weights=b["w"])
+        logits, shared = self._front(x, logits, b, step, adapter_plan)
+        self._route(logits, bias, b, step)
         step("quant_x", quant_mxfp4, x, q=b["x_q"], scale=b["x_s"])
         step("plan", moe_permute, b["ids"], self.E, plan=b["plan"])
         step("gemm_gate_up", moe_grouped_gemm_mxfp4, b["x_q"], b["x_s"], b["plan"], self.w13,
@@ -354,12 +417,16 @@ class MxMoELayer(MoELayer):
     @_on_x_device
     def forward_few(self, x: torch.Tensor, logits: Optional[torch.Tensor] = None,
                     bias: Optional[torch.Tensor] = None, return_all: bool = False,
-                    events: Optional[list] = None):
+                    events: Optional[list] = None, adapter_plan: Optional[torch.Tensor] = None):
         """forward() for at most 16 tokens of bf16 x in two kernels, activations in bf16."""
+        if self.routing is not None:
+            raise ValueError("forward_few finds the experts itself, by the plain softmax routing: a "
+                             "layer with set_routing takes forward()")
         T = x.shape[0]
         step = self._steps(events)
         needs = logits is None or self.ws13 is not None
-        logits, shared = self._front(x, logits, self.buffers(T) if needs else None, step)
+        logits, shared = self._front(x, logits, self.buffers(T) if needs else None, step,
+                                     adapter_plan)
         # (buffers of its own: the workspace belongs to this layer's calls)
         self._few[T] = o = step("few", moe_layer_mxfp4_few, logits, x, self.w13, self.s13, self.w2,
                                 self.s2, self.k, bias=bias, renormalize=self.renormalize,

@@ -243,27 +243,18 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, const uint16_t* __restrict__ u) {
 
 // ------------------------------------------------------------------ few rows
 // Up to 64 rows: bound by the stream of W.  One launch multiplies (64 w rows x all rows x a
-// range of K per workgroup, fp32 parts to the workspace) and, in its first workgroups, forms u,
-// which does not depend on the product; a second one adds the parts and the adapters, and
-// applies the epilogue.
-//
-// The product's workgroup takes K in pieces of 512: each wave holds its 16 w rows' piece in
-// registers, 16 loads of 16 bytes per lane that go out at once (two consecutive ones fill whole
-// 128-byte lines), while the x rows' piece is staged in LDS, which the four waves share.  16-byte
-// piece c of LDS row r sits at c ^ 2 (r % 16): the 16 rows x 2 pieces that 32 lanes of an operand
-// read take are then 32 different 16-byte slots of 512 bytes.
+// range of K per workgroup, fp32 parts to the workspace) and, in its first workgroups, forms
+// u's parts, which do not depend on the product; a second one adds the parts and the adapters,
+// and applies the epilogue.
 //
 // Parts are stored as the matrix instruction leaves them: 16 bytes per lane, 1 KB per block.
-constexpr int kFewRows = 64, kFewPiece = 512, kFewCols = 64;
-constexpr int kFewSteps = kFewPiece / 32;
+constexpr int kFewRows = 64, kFewCols = 64;
+constexpr int kFewSlotK = 64, kFewRowB = 2 * kFewSlotK;  // K and bytes of a slot's row: one line
 
-__device__ __forceinline__ uint4 load_stream(const uint16_t* p) {
-  typedef uint32_t v4u __attribute__((ext_vector_type(4)));
-  const v4u v = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(p));
-  return make_uint4(v.x, v.y, v.z, v.w);
-}
+// u parts: a wave takes 16 rows of one adapter x 16 columns x pieces of 512 K
+constexpr int kUPiece = 512, kUSteps = kUPiece / 32, kUSplits = 16;
 
-// the plan's tiles by lane (at most 64 of up to 64 rows), and the adapter of a sorted row
+// the plan's tiles by lane (at most 64 of up to 64 rows), and the tile of a sorted row
 struct FewPlan {
   int n, row0, expert;
   __device__ __forceinline__ FewPlan(const PlanView& pv, int lane) {
@@ -271,17 +262,17 @@ struct FewPlan {
     row0 = pv.tile_row0[min(lane, pv.max_tiles - 1)];
     expert = pv.tile_expert[min(lane, pv.max_tiles - 1)];
   }
-  // the plan tile of sorted row p (-1: none)
+  // -1: none
   __device__ __forceinline__ int tile(int p, int lane) const {
     return __popcll(__ballot(lane < n && row0 <= p)) - 1;
   }
 };
 
-// u (fp32) of up to 16 rows of one adapter x 32 columns: block `b` of the list of 16-row pieces
+// One wave: scale * x A_l^T over pieces c0 .. c1 - 1 of K, for 16-row piece `b` of the adapters'
+// rows and columns 16 cb .. + 15, into u [M][columns].  All loads of a piece go out at once: this
+// is a chain of memory latencies next to the stream of W, so it has to be short.
 __device__ __forceinline__ void few_shrink(const LoraArgs& args, const LoraShape& s, float* u, int b,
-                                           int c0, v4f* red) {
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+                                           int cb, int c0, int c1, int lane) {
   const int ln = lane & 15, kq = lane >> 4;
   const PlanView pv = plan_view(args.plan, s.L + 1, s.M);
   const FewPlan fp(pv, lane);
@@ -299,123 +290,202 @@ __device__ __forceinline__ void few_shrink(const LoraArgs& args, const LoraShape
   const int p0 = readlane(fp.row0, t) + 16 * (b - readlane(before, t));
   const int p1 = min(p0 + 16, readlane(fp.row0, t) + readlane(rows, t));
   const int cols = s.slices * s.r;
+  const uint16_t* arow = args.lora_a + (int64_t(l) * cols + min(16 * cb + ln, cols - 1)) * s.K;
   const uint16_t* x = args.a + int64_t(plan_row(pv, min(p0 + ln, p1 - 1), s.M)) * s.ld_a;
-  const uint16_t* arow[2];
-#pragma unroll
-  for (int q = 0; q < 2; ++q)
-    arow[q] = args.lora_a + (int64_t(l) * cols + min(c0 + 16 * q + ln, cols - 1)) * s.K;
-  v4f acc[2] = {v4f{0.f, 0.f, 0.f, 0.f}, v4f{0.f, 0.f, 0.f, 0.f}};
-  constexpr int kU = 4;
-  for (int k0 = 32 * kU * wave; k0 < s.K; k0 += 32 * kU * 4) {
-    uint4 xv[kU], av[2][kU];
-#pragma unroll
-    for (int j = 0; j < kU; ++j) {
-      const int k = k0 + 32 * j + 8 * kq;
-      xv[j] = load_k(x, k, s.K);
-      av[0][j] = load_k(arow[0], k, s.K);
-      av[1][j] = load_k(arow[1], k, s.K);
-    }
-#pragma unroll
-    for (int j = 0; j < kU; ++j) {
-      acc[0] = mfma(xv[j], av[0][j], acc[0]);
-      acc[1] = mfma(xv[j], av[1][j], acc[1]);
-    }
-  }
-  if (wave > 0) {
-    red[((wave - 1) * 2) * kWave + lane] = acc[0];
-    red[((wave - 1) * 2 + 1) * kWave + lane] = acc[1];
-  }
-  __syncthreads();
-  if (wave > 0) return;
   const float scale = args.scale[l];
+  v4f acc = {0.f, 0.f, 0.f, 0.f};
+  for (int c = c0; c < c1; ++c) {
+    uint4 av[kUSteps], xv[kUSteps];
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const v4f sum = acc[q] + (red[q * kWave + lane] + (red[(2 + q) * kWave + lane] + red[(4 + q) * kWave + lane]));
-    const int c = c0 + 16 * q + ln;
+    for (int j = 0; j < kUSteps; ++j) av[j] = load_k(arow, c * kUPiece + 32 * j + 8 * kq, s.K);
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int p = p0 + 4 * kq + v;
-      if (c < cols && p < p1) u[int64_t(p) * cols + c] = sum[v] * scale;
-    }
+    for (int j = 0; j < kUSteps; ++j) xv[j] = load_k(x, c * kUPiece + 32 * j + 8 * kq, s.K);
+#pragma unroll
+    for (int j = 0; j < kUSteps; ++j) acc = mfma(xv[j], av[j], acc);
+  }
+  const int col = 16 * cb + ln;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const int p = p0 + 4 * kq + v;
+    if (col < cols && p < p1) u[int64_t(p) * cols + col] = acc[v] * scale;
   }
 }
 
+// Position of 16-byte chunk c of a 128-byte LDS row r: c ^ swz(r).  The 16 rows x 2 chunks that
+// 32 lanes of an operand read take are then 32 different 16-byte slots modulo 512 bytes.
+__device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
+
+// s_waitcnt vmcnt(n), the other counters unconstrained
+template <int n>
+__device__ __forceinline__ void wait_vmem() {
+  static_assert(n >= 0 && n < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+// every wave's LDS reads so far are done, without a wait for loads still in flight
+__device__ __forceinline__ void ring_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// 16 bytes per lane straight into LDS, lane l's at dst + 16 l (dst a wave-uniform LDS offset).
+// Written in assembly: the compiler, which counts such a load as a write of all of LDS, would wait
+// for every one in flight ahead of the next LDS read; here the ring's own waits order them.  (No
+// register receives the data, so nothing the compiler allocates is written behind its back; m0,
+// which names the LDS address, is used by nothing else in these kernels.)
+template <bool kOnce>                                    // read once: non-temporal
+__device__ __forceinline__ void load_lds(const uint16_t* src, uint32_t dst) {
+  if constexpr (kOnce)
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt"
+                 :: "v"(src), "s"(dst) : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+                 :: "v"(src), "s"(dst) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_offset(const uint8_t* p) {
+  return uint32_t(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) uint8_t*)p));
+}
+
+template <int MB>
+constexpr int few_slot_bytes() { return (kFewCols + 16 * MB) * kFewRowB; }
+// slots of the ring: what two workgroups of a CU can have in its 160 KB
+template <int MB>
+constexpr int few_ring() { return 80 * 1024 / few_slot_bytes<MB>(); }
+
+// The product.  Both operands reach LDS by loads that write LDS directly, whole 128-byte lines, no
+// staging registers, a ring of slots of 64 K deep in flight.  A wave loads the 16 w rows whose
+// columns it computes and its share of the x rows.
 template <int MB>
 __global__ void __launch_bounds__(256, 2)
 lora_few_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restrict__ parts,
-                int shrink_blocks, int shrink_cols, int pieces_per_split) {
+                int shrink_items, int u_cols, int u_splits, int u_per_split, int slots_per_split) {
   extern __shared__ __align__(16) uint8_t lds[];
-  if (int(blockIdx.x) < shrink_blocks) {
-    few_shrink(args, s, u, blockIdx.x / shrink_cols, (blockIdx.x % shrink_cols) * 32,
-               reinterpret_cast<v4f*>(lds));
-    return;
-  }
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int shrink_blocks = (shrink_items + 3) / 4;
+  if (int(blockIdx.x) < shrink_blocks) {
+    const int item = blockIdx.x * 4 + wave;              // (row piece, K split, 16 columns)
+    if (item >= shrink_items) return;
+    const int cb = item % u_cols, rest = item / u_cols;
+    const int sp = rest % u_splits, pieces = (s.K + kUPiece - 1) / kUPiece;
+    few_shrink(args, s, u + int64_t(sp) * s.M * s.slices * s.r, rest / u_splits, cb, sp * u_per_split,
+               min((sp + 1) * u_per_split, pieces), lane);
+    return;
+  }
+  constexpr int kSlots = few_ring<MB>(), kSlotB = few_slot_bytes<MB>();
+  constexpr int kXLoads = MB == 4 ? 2 : 1;               // x: 16 MB rows over four waves
+  constexpr int kXRows = 4 * MB;                         // x rows per wave
+  constexpr int kLoads = 2 + kXLoads;
   const int ln = lane & 15, kq = lane >> 4;
   const PlanView pv = plan_view(args.plan, s.L + 1, s.M);
-  const int ntiles = (s.N + kFewCols - 1) / kFewCols;
-  const int b = blockIdx.x - shrink_blocks;
-  const int split = b / ntiles, nt = b - split * ntiles;
+  const int ntiles = (s.N + kFewCols - 1) / kFewCols, all_slots = s.K / kFewSlotK;
+  const int b = blockIdx.x - shrink_blocks, splits = (gridDim.x - shrink_blocks) / ntiles;
+  // (neighbouring workgroups take neighbouring ranges of the same rows)
+  const int nt = b / splits, split = b - nt * splits;
   const int n0 = nt * kFewCols + 16 * wave;
-  const uint16_t* wsrc = args.w + int64_t(min(n0 + ln, s.N - 1)) * s.K;
-  const int pieces = (s.K + kFewPiece - 1) / kFewPiece;
-  const int c0 = split * pieces_per_split, c1 = min(c0 + pieces_per_split, pieces);
+  const int s0 = split * slots_per_split, n_slots = min(slots_per_split, all_slots - s0);
 
-  uint4 wv[kFewSteps];
-  auto load_w = [&](int c) {
+  const int lr = lane >> 3;
+  const uint16_t* wsrc[2];
 #pragma unroll
-    for (int j = 0; j < kFewSteps; ++j) {
-      const int k = c * kFewPiece + 32 * j + 8 * kq;
-      const uint4 v = load_stream(wsrc + min(k, s.K - 8));
-      wv[j] = k < s.K ? v : make_uint4(0u, 0u, 0u, 0u);
+  for (int g = 0; g < 2; ++g)
+    wsrc[g] = args.w + int64_t(min(n0 + 8 * g + lr, s.N - 1)) * s.K + s0 * kFewSlotK +
+              (((lane & 7) ^ swz(8 * g + lr)) * 8);
+  const uint16_t* xsrc[kXLoads];
+#pragma unroll
+  for (int g = 0; g < kXLoads; ++g) {
+    // (the rows are read at wave-uniform addresses, through the scalar cache: a vector load's result
+    // could only be waited for together with the w loads issued before it is needed)
+    const int first = kXRows * wave + 8 * g;
+    int row = 0;
+#pragma unroll
+    for (int i = 0; i < (MB == 1 ? 4 : 8); ++i) {
+      const int at = plan_row(pv, first + i, s.M);
+      row = lr == i ? at : row;
     }
-  };
-  // x: thread -> piece tid % 64 of rows tid / 64, + 4, ...
-  const uint16_t* xsrc[4 * MB];
+    xsrc[g] = args.a + int64_t(row) * s.ld_a + s0 * kFewSlotK + (((lane & 7) ^ swz((first + lr) & 15)) * 8);
+  }
+  // slot st of this range; past the last one, the last again (into a buffer that is not read)
+  const uint32_t lds0 = lds_offset(lds);
+  auto issue = [&](int st) {
+    const uint32_t buf = lds0 + (st % kSlots) * kSlotB;
+    const int k = min(st, n_slots - 1) * kFewSlotK;
 #pragma unroll
-  for (int i = 0; i < 4 * MB; ++i)
-    xsrc[i] = args.a + int64_t(plan_row(pv, wave + 4 * i, s.M)) * s.ld_a;
-  load_w(c0);
+    for (int g = 0; g < 2; ++g) load_lds<true>(wsrc[g] + k, buf + (16 * wave + 8 * g) * kFewRowB);
+#pragma unroll
+    for (int g = 0; g < kXLoads; ++g)
+      if (MB > 1 || lane < 32)
+        load_lds<false>(xsrc[g] + k, buf + (kFewCols + kXRows * wave + 8 * g) * kFewRowB);
+  };
   v4f acc[MB];
 #pragma unroll
   for (int i = 0; i < MB; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
-  for (int c = c0; c < c1; ++c) {
-    uint4 xv[4 * MB];
+  const int rd[2] = {ln * kFewRowB + ((kq ^ swz(ln)) * 16), ln * kFewRowB + (((4 + kq) ^ swz(ln)) * 16)};
+  auto multiply = [&](const uint8_t* buf) {
 #pragma unroll
-    for (int i = 0; i < 4 * MB; ++i) xv[i] = load_k(xsrc[i], c * kFewPiece + 8 * lane, s.K);
-    if (c > c0) __syncthreads();
+    for (int h = 0; h < 2; ++h) {
+      const uint4 wv = *reinterpret_cast<const uint4*>(buf + 16 * wave * kFewRowB + rd[h]);
 #pragma unroll
-    for (int i = 0; i < 4 * MB; ++i) {
-      const int row = wave + 4 * i;
-      *reinterpret_cast<uint4*>(lds + row * (2 * kFewPiece) + ((lane ^ (2 * (row & 15))) * 16)) = xv[i];
+      for (int i = 0; i < MB; ++i)
+        acc[i] = mfma(*reinterpret_cast<const uint4*>(buf + (kFewCols + 16 * i) * kFewRowB + rd[h]), wv, acc[i]);
+    }
+  };
+  if (n_slots > 0) {
+#pragma unroll
+    for (int st = 0; st < kSlots; ++st) issue(st);
+    wait_vmem<(kSlots - 1) * kLoads>();
+    ring_barrier();
+    for (int st = 0; st < n_slots; ++st) {
+      multiply(lds + (st % kSlots) * kSlotB);
+      if (st + 1 == n_slots) break;
+      wait_vmem<(kSlots - 2) * kLoads>();                // this wave's loads of slot st + 1 have landed
+      ring_barrier();                                    // ... every wave's, and slot st is read
+      issue(st + kSlots);
+    }
+    wait_vmem<0>();
+  }
+  const int tail = s.K - all_slots * kFewSlotK;          // K past whole slots, zeros after it
+  if (tail > 0 && split == splits - 1) {
+    ring_barrier();
+    const int k0 = all_slots * kFewSlotK;
+    for (int i = tid; i < (kFewCols + 16 * MB) * 8; i += 256) {
+      const int row = i >> 3, c = i & 7;
+      const uint16_t* src = row < kFewCols
+          ? args.w + int64_t(min(nt * kFewCols + row, s.N - 1)) * s.K
+          : args.a + int64_t(plan_row(pv, row - kFewCols, s.M)) * s.ld_a;
+      *reinterpret_cast<uint4*>(lds + row * kFewRowB + ((c ^ swz(row & 15)) * 16)) = load_k(src, k0 + 8 * c, s.K);
     }
     __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kFewSteps; ++j)
-#pragma unroll
-      for (int i = 0; i < MB; ++i) {
-        const uint4 a = *reinterpret_cast<const uint4*>(
-            lds + (16 * i + ln) * (2 * kFewPiece) + (((4 * j + kq) ^ (2 * ln)) * 16));
-        acc[i] = mfma(a, wv[j], acc[i]);
-      }
-    if (c + 1 < c1) load_w(c + 1);
+    multiply(lds);
   }
   if (n0 >= s.N) return;
-  const int nb = s.N / 16;
+  const int nb = s.N / 16, mblocks = (s.M + 15) / 16;
 #pragma unroll
   for (int i = 0; i < MB; ++i)
-    if (16 * i < s.M) parts[((int64_t(split) * ((s.M + 15) / 16) + i) * nb + n0 / 16) * kWave + lane] = acc[i];
+    if (i < mblocks) parts[((int64_t(split) * mblocks + i) * nb + n0 / 16) * kWave + lane] = acc[i];
+}
+
+// at[0] + at[stride] + ... (n of them, in this order), loaded eight at a time
+__device__ __forceinline__ v4f add_parts(const v4f* at, int64_t stride, int n) {
+  v4f sum = {0.f, 0.f, 0.f, 0.f};
+  for (int i0 = 0; i0 < n; i0 += 8) {
+    v4f v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = at[min(i0 + i, n - 1) * stride];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i0 + i < n) sum = sum + v[i];
+  }
+  return sum;
 }
 
 // parts and adapters joined: a wave forms 16 rows x 16 output columns (of the gate and the up
 // half with SILU_MUL).  Lane l has column l % 16 of rows 4 (l / 16) .. + 3, whose adapters may all
-// differ: it reads their B rows for its column (r consecutive values) and u, and sums r products in
-// fp32 for each.  All of these loads are independent.
+// differ: it reads their B rows for its column (r consecutive values) and sums r products with u
+// in fp32 for each.  Everything but B is loaded at once, B as soon as the rows' adapters are known.
 template <int EPI>
 __global__ void __launch_bounds__(256)
 lora_join_kernel(LoraArgs args, LoraShape s, const float* __restrict__ u,
-                 const v4f* __restrict__ parts, int splits) {
+                 const v4f* __restrict__ parts, int splits, int u_splits) {
+  extern __shared__ __align__(16) float us[];            // u of the 16 rows [16][columns]
   constexpr bool kSilu = EPI == MOEQ_EPI_SILU_MUL;
   constexpr int kHalves = kSilu ? 2 : 1;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -423,75 +493,113 @@ lora_join_kernel(LoraArgs args, LoraShape s, const float* __restrict__ u,
   const int ln = lane & 15, kq = lane >> 4;
   const int cols = kSilu ? s.N / 2 : s.N;
   const int cblocks = cols / 16, mblocks = (s.M + 15) / 16, nb = s.N / 16;
-  const int item = blockIdx.x * 4 + wave;
-  if (item >= cblocks * mblocks) return;
-  const int mb = item / cblocks, cb = item - mb * cblocks;
+  const int mb = blockIdx.y, cb = min(int(blockIdx.x) * 4 + wave, cblocks - 1);
+  const bool mine = int(blockIdx.x) * 4 + wave < cblocks;
   const PlanView pv = plan_view(args.plan, s.L + 1, s.M);
   const FewPlan fp(pv, lane);
+  const int rows = min(16, s.M - 16 * mb);
+  int orow[4];
+#pragma unroll
+  for (int v = 0; v < 4; ++v) orow[v] = plan_row(pv, 16 * mb + 4 * kq + v, s.M);
   v4f acc[kHalves];
 #pragma unroll
   for (int h = 0; h < kHalves; ++h) {
     const v4f* at = parts + (int64_t(mb) * nb + cb + h * cblocks) * kWave + lane;
-    acc[h] = at[0];
-    for (int i = 1; i < splits; ++i) acc[h] = acc[h] + at[int64_t(i) * mblocks * nb * kWave];
+    acc[h] = add_parts(at, int64_t(mblocks) * nb * kWave, splits);
+  }
+  const int ucols = s.slices * s.r;
+  for (int i = 4 * tid; i < rows * ucols; i += 1024) {
+    const v4f* at = reinterpret_cast<const v4f*>(u + int64_t(16 * mb) * ucols + i);
+    *reinterpret_cast<v4f*>(us + i) = add_parts(at, int64_t(s.M) * ucols / 4, u_splits);
   }
   // lane i < 16: the adapter of row 16 mb + i (-1: none)
   int adapter = -1;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const int p = 16 * mb + i;
-    const int t = fp.tile(p, lane);
+    const int t = fp.tile(16 * mb + i, lane);
     const int e = readlane(fp.expert, max(t, 0));
-    if (lane == i && t >= 0 && p < s.M && e >= 0 && e < s.L) adapter = e;
+    if (lane == i && t >= 0 && i < rows && e >= 0 && e < s.L) adapter = e;
   }
-  const int ucols = s.slices * s.r;
+  bool has[4];
+  const uint16_t* br[4][kHalves];                        // (rows without an adapter read one address)
+  const float* ur[4][kHalves];
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
     const int l = __shfl(adapter, 4 * kq + v);
-    if (l < 0) continue;
-    const float* ur = u + int64_t(16 * mb + 4 * kq + v) * ucols;
+    has[v] = l >= 0;
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) {
       const int n = (cb + h * cblocks) * 16 + ln;
-      const uint16_t* br = args.lora_b + (int64_t(l) * s.N + n) * s.r;
-      const float* us = ur + (s.slices == 2 && n >= s.N / 2 ? s.r : 0);
-      float d = 0.0f;
-      for (int j = 0; j < s.r; j += 8) {
-        float bv[8];
-        bf16x8_to_f32(load16(br + j), bv);
-        const float4 u0 = *reinterpret_cast<const float4*>(us + j);
-        const float4 u1 = *reinterpret_cast<const float4*>(us + j + 4);
-        d = fmaf(u0.x, bv[0], d); d = fmaf(u0.y, bv[1], d);
-        d = fmaf(u0.z, bv[2], d); d = fmaf(u0.w, bv[3], d);
-        d = fmaf(u1.x, bv[4], d); d = fmaf(u1.y, bv[5], d);
-        d = fmaf(u1.z, bv[6], d); d = fmaf(u1.w, bv[7], d);
-      }
-      acc[h][v] += d;
+      br[v][h] = args.lora_b + (has[v] ? (int64_t(l) * s.N + n) * s.r : 0);
+      ur[v][h] = us + (has[v] ? (4 * kq + v) * ucols + (s.slices == 2 && n >= s.N / 2 ? s.r : 0) : 0);
     }
   }
+  uint4 bv[4][kHalves];
+  auto load_b = [&](int j) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) bv[v][h] = load16(br[v][h] + j);
+  };
+  load_b(0);
+  __syncthreads();                                       // u is in LDS
+  float d[4][kHalves] = {};
+  for (int j = 0; j < s.r; j += 8) {
+    uint4 cur[4][kHalves];
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) cur[v][h] = bv[v][h];
+    load_b(min(j + 8, s.r - 8));
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) {
+        float f[8];
+        bf16x8_to_f32(cur[v][h], f);
+        const float4 u0 = *reinterpret_cast<const float4*>(ur[v][h] + j);
+        const float4 u1 = *reinterpret_cast<const float4*>(ur[v][h] + j + 4);
+        float& sum = d[v][h];
+        sum = fmaf(u0.x, f[0], sum); sum = fmaf(u0.y, f[1], sum);
+        sum = fmaf(u0.z, f[2], sum); sum = fmaf(u0.w, f[3], sum);
+        sum = fmaf(u1.x, f[4], sum); sum = fmaf(u1.y, f[5], sum);
+        sum = fmaf(u1.z, f[6], sum); sum = fmaf(u1.w, f[7], sum);
+      }
+  }
+  if (!mine) return;
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
-    const int p = 16 * mb + 4 * kq + v;
-    if (p >= s.M) continue;
+    if (4 * kq + v >= rows) continue;
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) acc[h][v] += has[v] ? d[v][h] : 0.0f;
     const float f = kSilu ? silu_f32(acc[0][v]) * acc[kHalves - 1][v] : acc[0][v];
-    args.out[int64_t(plan_row(pv, p, s.M)) * cols + cb * 16 + ln] = to_bf16(f);
+    args.out[int64_t(orow[v]) * cols + cb * 16 + ln] = to_bf16(f);
   }
 }
 
 size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
-// splits of K of the few-row product: about 512 workgroups, whole pieces of K each
+// Splits of K of the few-row product: about 512 workgroups, two per CU; and of u.
 struct FewSplit {
-  int splits, per_split;
+  int splits, slots;                                     // slots of 64 K per split
+  int u_splits, u_pieces;                                // pieces of 512 K per split of u
 };
 FewSplit few_split(const LoraShape& s) {
-  const int ntiles = (s.N + kFewCols - 1) / kFewCols, pieces = (s.K + kFewPiece - 1) / kFewPiece;
+  const int ntiles = (s.N + kFewCols - 1) / kFewCols;
+  const int slots = s.K / kFewSlotK > 0 ? s.K / kFewSlotK : 1;
   int want = (512 + ntiles - 1) / ntiles;
-  if (want > pieces) want = pieces;
-  const int per = (pieces + want - 1) / want;
-  return {(pieces + per - 1) / per, per};
+  if (want > slots) want = slots;
+  const int per = (slots + want - 1) / want;
+  const int pieces = (s.K + kUPiece - 1) / kUPiece;
+  const int u_per = (pieces + kUSplits - 1) / kUSplits;
+  return {(slots + per - 1) / per, per, (pieces + u_per - 1) / u_per, u_per};
 }
-size_t few_u_bytes(const LoraShape& s) { return align256(size_t(s.M) * s.slices * s.r * sizeof(float)); }
+size_t few_u_bytes(const LoraShape& s) {
+  return align256(size_t(few_split(s).u_splits) * s.M * s.slices * s.r * sizeof(float));
+}
+size_t few_part_bytes(const LoraShape& s) {
+  return size_t(few_split(s).splits) * ((s.M + 15) / 16 * 16) * s.N * sizeof(float);
+}
 
 template <int MB>
 hipError_t launch_few(const LoraArgs& args, const LoraShape& s, hipStream_t stream) {
@@ -500,26 +608,28 @@ hipError_t launch_few(const LoraArgs& args, const LoraShape& s, hipStream_t stre
   v4f* parts = reinterpret_cast<v4f*>(static_cast<uint8_t*>(args.ws) + few_u_bytes(s));
   const int reached = s.L < s.M ? s.L : s.M;             // adapters that have rows, at most
   const int row_pieces = reached + s.M / 16 < s.M ? reached + s.M / 16 : s.M;
-  const int shrink_cols = (s.slices * s.r + 31) / 32, shrink = row_pieces * shrink_cols;
+  const int u_cols = (s.slices * s.r + 15) / 16, items = row_pieces * u_cols * fs.u_splits;
   const int ntiles = (s.N + kFewCols - 1) / kFewCols;
-  const unsigned lds = 16 * MB * 2 * kFewPiece;          // at least the 6 KB of few_shrink
-  hipLaunchKernelGGL(lora_few_kernel<MB>, dim3(unsigned(shrink + ntiles * fs.splits)), dim3(256), lds,
-                     stream, args, s, u, parts, shrink, shrink_cols, fs.per_split);
-  hipError_t err = hipGetLastError();
+  const unsigned lds = few_ring<MB>() * few_slot_bytes<MB>();
+  hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void*>(&lora_few_kernel<MB>),
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, int(lds));
   if (err != hipSuccess) return err;
+  hipLaunchKernelGGL(lora_few_kernel<MB>, dim3(unsigned((items + 3) / 4 + ntiles * fs.splits)), dim3(256),
+                     lds, stream, args, s, u, parts, items, u_cols, fs.u_splits, fs.u_pieces, fs.slots);
+  if ((err = hipGetLastError()) != hipSuccess) return err;
   const bool silu = s.epilogue == MOEQ_EPI_SILU_MUL;
-  const int items = (silu ? s.N / 2 : s.N) / 16 * ((s.M + 15) / 16);
+  const int cblocks = (silu ? s.N / 2 : s.N) / 16;
   const auto join = silu ? lora_join_kernel<MOEQ_EPI_SILU_MUL> : lora_join_kernel<MOEQ_EPI_NONE>;
-  hipLaunchKernelGGL(join, dim3(unsigned((items + 3) / 4)), dim3(256), 0, stream, args, s, u, parts,
-                     fs.splits);
+  hipLaunchKernelGGL(join, dim3(unsigned((cblocks + 3) / 4), unsigned((s.M + 15) / 16)), dim3(256),
+                     unsigned(16 * s.slices * s.r * sizeof(float)), stream, args, s, u, parts, fs.splits,
+                     fs.u_splits);
   return hipGetLastError();
 }
 
 }  // namespace
 
 size_t lora_ws_bytes(const LoraShape& s) {
-  if (s.M <= kFewRows)
-    return few_u_bytes(s) + align256(size_t(few_split(s).splits) * ((s.M + 15) / 16) * s.N * 16 * sizeof(float)) + 256;
+  if (s.M <= kFewRows) return few_u_bytes(s) + align256(few_part_bytes(s)) + 256;
   return align256(size_t(s.M) * s.slices * 2 * s.r * sizeof(uint16_t));
 }
 

@@ -463,29 +463,48 @@ lora_few_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restri
     if (i < mblocks) parts[((int64_t(split) * mblocks + i) * nb + n0 / 16) * kWave + lane] = acc[i];
 }
 
-// at[0] + at[stride] + ... (n of them, in this order), loaded eight at a time
-__device__ __forceinline__ v4f add_parts(const v4f* at, int64_t stride, int n) {
-  v4f sum = {0.f, 0.f, 0.f, 0.f};
-  for (int i0 = 0; i0 < n; i0 += 8) {
-    v4f v[8];
+// at[0] + at[stride] + ... (n of them, in this order), eight loads at a time; the first eight go out
+// in load(), well ahead of sum()
+struct PartSum {
+  static constexpr int kAhead = 8;
+  v4f v[kAhead];
+  __device__ __forceinline__ void load(const v4f* at, int64_t stride, int i0, int n) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = at[min(i0 + i, n - 1) * stride];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i0 + i < n) sum = sum + v[i];
+    for (int i = 0; i < kAhead; ++i) v[i] = at[min(i0 + i, n - 1) * stride];
   }
-  return sum;
-}
+  __device__ __forceinline__ v4f sum(const v4f* at, int64_t stride, int n) {
+    v4f acc = v[0];
+#pragma unroll
+    for (int i = 1; i < kAhead; ++i)
+      if (i < n) acc = acc + v[i];
+    for (int i0 = kAhead; i0 < n; i0 += kAhead) {
+      load(at, stride, i0, n);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (i0 + i < n) acc = acc + v[i];
+    }
+    return acc;
+  }
+};
 
-// parts and adapters joined: a wave forms 16 rows x 16 output columns (of the gate and the up
-// half with SILU_MUL).  Lane l has column l % 16 of rows 4 (l / 16) .. + 3, whose adapters may all
-// differ: it reads their B rows for its column (r consecutive values) and sums r products with u
-// in fp32 for each.  Everything but B is loaded at once, B as soon as the rows' adapters are known.
+// bytes of LDS for u of 16 rows in two bf16 parts, each slice padded to whole steps of 32
+__host__ __device__ inline int join_u_row(int slices, int r) { return slices * ((r + 31) / 32 * 32) * 4 + 16; }
+
+// parts and adapters joined: a workgroup forms 16 rows x 16 output columns (of the gate and the up
+// half with SILU_MUL).  For each adapter among the 16 rows, its B rows of these columns times all
+// 16 rows' u, kept for the adapter's own rows: each B value is read once, in half lines that the
+// two steps of a pair complete.  (A lane that read the B rows of its own column for its four rows,
+// and summed without the matrix instruction, used 16 bytes of each line at a time and read lines
+// over: 11.7 us for 64 rows of rank 64 x 4096 columns.)  This launch is latency: everything but B
+// is loaded at once, B as soon as the rows' adapters are known, and the adapters, up to 16, are
+// dealt over the four waves, so that none loads twice (four columns' worth per workgroup and all
+// adapters in each wave: 9.3 us instead of JOIN16 for 16 rows x 8192).
 template <int EPI>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 2)
 lora_join_kernel(LoraArgs args, LoraShape s, const float* __restrict__ u,
                  const v4f* __restrict__ parts, int splits, int u_splits) {
-  extern __shared__ __align__(16) float us[];            // u of the 16 rows [16][columns]
+  extern __shared__ __align__(16) uint8_t us[];          // u: [16 rows][slice][hi, lo][r to 32]
+  __shared__ v4f red[3][2][kWave];
   constexpr bool kSilu = EPI == MOEQ_EPI_SILU_MUL;
   constexpr int kHalves = kSilu ? 2 : 1;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -493,85 +512,144 @@ lora_join_kernel(LoraArgs args, LoraShape s, const float* __restrict__ u,
   const int ln = lane & 15, kq = lane >> 4;
   const int cols = kSilu ? s.N / 2 : s.N;
   const int cblocks = cols / 16, mblocks = (s.M + 15) / 16, nb = s.N / 16;
-  const int mb = blockIdx.y, cb = min(int(blockIdx.x) * 4 + wave, cblocks - 1);
-  const bool mine = int(blockIdx.x) * 4 + wave < cblocks;
+  const int mb = blockIdx.y, cb = blockIdx.x;
   const PlanView pv = plan_view(args.plan, s.L + 1, s.M);
   const FewPlan fp(pv, lane);
   const int rows = min(16, s.M - 16 * mb);
+  const int64_t part_stride = int64_t(mblocks) * nb * kWave, u_stride = int64_t(s.M) * s.slices * s.r / 4;
+  const v4f* pat[kHalves];
+  PartSum ps[kHalves], pu;
+#pragma unroll
+  for (int h = 0; h < kHalves; ++h) {
+    pat[h] = parts + (int64_t(mb) * nb + cb + h * cblocks) * kWave + lane;
+    if (wave == 0) ps[h].load(pat[h], part_stride, 0, splits);
+  }
+  // u's elements, four at a time: thread i takes quads i, i + 256, ... of [row][slice][r to 32]
+  const int r32 = (s.r + 31) / 32 * 32, quads = s.slices * (r32 / 4), row_bytes = join_u_row(s.slices, s.r);
+  const auto u_quad = [&](int i, int& row, int& slice, int& k) {
+    row = i / quads;
+    const int c = i - row * quads;
+    slice = c / (r32 / 4);
+    k = 4 * (c - slice * (r32 / 4));
+    return reinterpret_cast<const v4f*>(
+        u + (int64_t(16 * mb + min(row, rows - 1)) * s.slices + slice) * s.r + min(k, s.r - 4));
+  };
+  int urow, uslice, uk;
+  const v4f* uat = u_quad(min(tid, 16 * quads - 1), urow, uslice, uk);
+  pu.load(uat, u_stride, 0, u_splits);
   int orow[4];
 #pragma unroll
   for (int v = 0; v < 4; ++v) orow[v] = plan_row(pv, 16 * mb + 4 * kq + v, s.M);
-  v4f acc[kHalves];
-#pragma unroll
-  for (int h = 0; h < kHalves; ++h) {
-    const v4f* at = parts + (int64_t(mb) * nb + cb + h * cblocks) * kWave + lane;
-    acc[h] = add_parts(at, int64_t(mblocks) * nb * kWave, splits);
-  }
-  const int ucols = s.slices * s.r;
-  for (int i = 4 * tid; i < rows * ucols; i += 1024) {
-    const v4f* at = reinterpret_cast<const v4f*>(u + int64_t(16 * mb) * ucols + i);
-    *reinterpret_cast<v4f*>(us + i) = add_parts(at, int64_t(s.M) * ucols / 4, u_splits);
-  }
-  // lane i < 16: the adapter of row 16 mb + i (-1: none)
+
+  // lane i < 16: the adapter of row 16 mb + i (-1: none).  Rows are sorted by adapter, so each
+  // adapter's rows follow its first one.
   int adapter = -1;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const int t = fp.tile(16 * mb + i, lane);
     const int e = readlane(fp.expert, max(t, 0));
-    if (lane == i && t >= 0 && i < rows && e >= 0 && e < s.L) adapter = e;
+    const int found = t >= 0 && i < rows && uint32_t(e) < uint32_t(s.L) ? e : -1;
+    adapter = lane == i ? found : adapter;
   }
-  bool has[4];
-  const uint16_t* br[4][kHalves];                        // (rows without an adapter read one address)
-  const float* ur[4][kHalves];
+  const uint32_t with = uint32_t(__ballot(adapter >= 0));
+  const int before = __shfl_up(adapter, 1);
+  uint32_t firsts = uint32_t(__ballot(adapter >= 0 && (lane == 0 || before != adapter)));
+  // first w row of the block's halves, and their slice of u
+  int wrow[kHalves], slice[kHalves];
 #pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    const int l = __shfl(adapter, 4 * kq + v);
-    has[v] = l >= 0;
-#pragma unroll
-    for (int h = 0; h < kHalves; ++h) {
-      const int n = (cb + h * cblocks) * 16 + ln;
-      br[v][h] = args.lora_b + (has[v] ? (int64_t(l) * s.N + n) * s.r : 0);
-      ur[v][h] = us + (has[v] ? (4 * kq + v) * ucols + (s.slices == 2 && n >= s.N / 2 ? s.r : 0) : 0);
-    }
+  for (int h = 0; h < kHalves; ++h) {
+    wrow[h] = (cb + h * cblocks) * 16;
+    slice[h] = s.slices == 2 && wrow[h] >= s.N / 2;
   }
-  uint4 bv[4][kHalves];
-  auto load_b = [&](int j) {
+  constexpr int kMine = 4;                               // adapters of a wave
+  uint32_t of[kMine];                                    // their rows, one bit each
+  int id[kMine], n_mine = 0;
+  for (int i = 0; i < wave; ++i) firsts &= firsts - 1;
 #pragma unroll
-    for (int v = 0; v < 4; ++v)
+  for (int a = 0; a < kMine; ++a) {                      // every fourth of the list
+    const int i = firsts ? __ffs(firsts) - 1 : 0;
+    const uint32_t rest = firsts & (firsts - 1);
+    // the bits from this first row up to the next one
+    of[a] = firsts ? with & (~0u << i) & (rest ? (rest & -rest) - 1 : ~0u) : 0u;
+    id[a] = max(readlane(adapter, i), 0);
+    n_mine += firsts != 0;
+    firsts = rest;
+    for (int j = 0; j < 3; ++j) firsts &= firsts - 1;
+  }
+  uint4 b[kMine][2][kHalves];
+  auto load_b = [&](int k0) {
 #pragma unroll
-      for (int h = 0; h < kHalves; ++h) bv[v][h] = load16(br[v][h] + j);
-  };
-  load_b(0);
-  __syncthreads();                                       // u is in LDS
-  float d[4][kHalves] = {};
-  for (int j = 0; j < s.r; j += 8) {
-    uint4 cur[4][kHalves];
-#pragma unroll
-    for (int v = 0; v < 4; ++v)
-#pragma unroll
-      for (int h = 0; h < kHalves; ++h) cur[v][h] = bv[v][h];
-    load_b(min(j + 8, s.r - 8));
-#pragma unroll
-    for (int v = 0; v < 4; ++v)
+    for (int a = 0; a < kMine; ++a)
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) {
-        float f[8];
-        bf16x8_to_f32(cur[v][h], f);
-        const float4 u0 = *reinterpret_cast<const float4*>(ur[v][h] + j);
-        const float4 u1 = *reinterpret_cast<const float4*>(ur[v][h] + j + 4);
-        float& sum = d[v][h];
-        sum = fmaf(u0.x, f[0], sum); sum = fmaf(u0.y, f[1], sum);
-        sum = fmaf(u0.z, f[2], sum); sum = fmaf(u0.w, f[3], sum);
-        sum = fmaf(u1.x, f[4], sum); sum = fmaf(u1.y, f[5], sum);
-        sum = fmaf(u1.z, f[6], sum); sum = fmaf(u1.w, f[7], sum);
+        const uint16_t* at = args.lora_b + (int64_t(id[a]) * s.N + wrow[h] + ln) * s.r;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) b[a][j][h] = load16(at + min(k0 + 32 * j + 8 * kq, s.r - 8));
+      }
+  };
+  if (n_mine > 0) load_b(0);
+  v4f acc[kHalves];
+#pragma unroll
+  for (int h = 0; h < kHalves; ++h)
+    acc[h] = wave == 0 ? ps[h].sum(pat[h], part_stride, splits) : v4f{0.f, 0.f, 0.f, 0.f};
+  for (int i = tid; i < 16 * quads; i += 256) {
+    if (i >= 256) {
+      uat = u_quad(i, urow, uslice, uk);
+      pu.load(uat, u_stride, 0, u_splits);
+    }
+    const v4f f = pu.sum(uat, u_stride, u_splits);
+    uint16_t hi[4], lo[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) split2(uk < s.r ? f[j] : 0.0f, hi[j], lo[j]);
+    uint8_t* to = us + urow * row_bytes + (uslice * 2 * r32 + uk) * 2;
+    *reinterpret_cast<uint2*>(to) = make_uint2(hi[0] | uint32_t(hi[1]) << 16, hi[2] | uint32_t(hi[3]) << 16);
+    *reinterpret_cast<uint2*>(to + 2 * r32) =
+        make_uint2(lo[0] | uint32_t(lo[1]) << 16, lo[2] | uint32_t(lo[3]) << 16);
+  }
+  __syncthreads();                                       // u is in LDS
+  for (int k0 = 0; n_mine > 0 && k0 < s.r; k0 += 64) {
+    uint4 hi[2][kHalves], lo[2][kHalves];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) {
+        const int k = min(k0 + 32 * j, r32 - 32) + 8 * kq;   // (a step past r is not used)
+        const uint8_t* at = us + ln * row_bytes + (slice[h] * 2 * r32 + k) * 2;
+        hi[j][h] = *reinterpret_cast<const uint4*>(at);
+        lo[j][h] = *reinterpret_cast<const uint4*>(at + 2 * r32);
+      }
+    if (k0 > 0) load_b(k0);
+#pragma unroll
+    for (int a = 0; a < kMine; ++a)
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) {
+        v4f d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const bool in = k0 + 32 * j + 8 * kq < s.r;
+          const uint4 w = b[a][j][h];
+          const uint4 bv = make_uint4(in ? w.x : 0u, in ? w.y : 0u, in ? w.z : 0u, in ? w.w : 0u);
+          if (j == 0 || k0 + 32 < s.r) {
+            d = mfma(hi[j][h], bv, d);
+            d = mfma(lo[j][h], bv, d);
+          }
+        }
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[h][v] += of[a] >> (4 * kq + v) & 1 ? d[v] : 0.0f;
       }
   }
-  if (!mine) return;
+  if (wave > 0) {
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) red[wave - 1][h][lane] = acc[h];
+  }
+  __syncthreads();
+  if (wave > 0) return;
+#pragma unroll
+  for (int h = 0; h < kHalves; ++h)
+    acc[h] = acc[h] + (red[0][h][lane] + (red[1][h][lane] + red[2][h][lane]));
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
     if (4 * kq + v >= rows) continue;
-#pragma unroll
-    for (int h = 0; h < kHalves; ++h) acc[h][v] += has[v] ? d[v][h] : 0.0f;
     const float f = kSilu ? silu_f32(acc[0][v]) * acc[kHalves - 1][v] : acc[0][v];
     args.out[int64_t(orow[v]) * cols + cb * 16 + ln] = to_bf16(f);
   }
@@ -620,8 +698,8 @@ hipError_t launch_few(const LoraArgs& args, const LoraShape& s, hipStream_t stre
   const bool silu = s.epilogue == MOEQ_EPI_SILU_MUL;
   const int cblocks = (silu ? s.N / 2 : s.N) / 16;
   const auto join = silu ? lora_join_kernel<MOEQ_EPI_SILU_MUL> : lora_join_kernel<MOEQ_EPI_NONE>;
-  hipLaunchKernelGGL(join, dim3(unsigned((cblocks + 3) / 4), unsigned((s.M + 15) / 16)), dim3(256),
-                     unsigned(16 * s.slices * s.r * sizeof(float)), stream, args, s, u, parts, fs.splits,
+  hipLaunchKernelGGL(join, dim3(unsigned(cblocks), unsigned((s.M + 15) / 16)), dim3(256),
+                     unsigned(16 * join_u_row(s.slices, s.r)), stream, args, s, u, parts, fs.splits,
                      fs.u_splits);
   return hipGetLastError();
 }

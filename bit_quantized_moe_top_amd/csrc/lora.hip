@@ -252,7 +252,7 @@ constexpr int kFewRows = 64, kFewCols = 64;
 constexpr int kFewSlotK = 64, kFewRowB = 2 * kFewSlotK;  // K and bytes of a slot's row: one line
 
 // u parts: a wave takes 16 rows of one adapter x 16 columns x pieces of 512 K
-constexpr int kUPiece = 512, kUSteps = kUPiece / 32, kUSplits = 16;
+constexpr int kUPiece = 512, kUSteps = kUPiece / 32, kUSplits = 4;
 
 // the plan's tiles by lane (at most 64 of up to 64 rows), and the tile of a sorted row
 struct FewPlan {
@@ -262,9 +262,15 @@ struct FewPlan {
     row0 = pv.tile_row0[min(lane, pv.max_tiles - 1)];
     expert = pv.tile_expert[min(lane, pv.max_tiles - 1)];
   }
-  // -1: none
-  __device__ __forceinline__ int tile(int p, int lane) const {
-    return __popcll(__ballot(lane < n && row0 <= p)) - 1;
+  // adapter of sorted row p0 + lane, lane < 16 (the tile that holds it; -1: none)
+  __device__ __forceinline__ int adapter16(int p0, int lane) const {
+    const int base = __popcll(__ballot(lane < n && row0 <= p0)) - 1;
+    const int at = row0 - p0;
+    const uint32_t bit = lane < n && at > 0 && at < 16 ? 1u << at : 0u;
+    const uint32_t starts = uint32_t(wave_reduce(int(bit), [](int a, int b) { return a | b; }, 0));
+    const int t = base + __popc(starts & ((2u << (lane & 15)) - 1u));
+    const int e = __shfl(expert, max(t, 0));
+    return t >= 0 ? e : -1;
   }
 };
 
@@ -346,15 +352,15 @@ __device__ __forceinline__ uint32_t lds_offset(const uint8_t* p) {
 
 template <int MB>
 constexpr int few_slot_bytes() { return (kFewCols + 16 * MB) * kFewRowB; }
-// slots of the ring: what two workgroups of a CU can have in its 160 KB
+// slots of the ring: what three workgroups of a CU can have in its 160 KB
 template <int MB>
-constexpr int few_ring() { return 80 * 1024 / few_slot_bytes<MB>(); }
+constexpr int few_ring() { return 160 * 1024 / 3 / few_slot_bytes<MB>(); }
 
 // The product.  Both operands reach LDS by loads that write LDS directly, whole 128-byte lines, no
 // staging registers, a ring of slots of 64 K deep in flight.  A wave loads the 16 w rows whose
 // columns it computes and its share of the x rows.
 template <int MB>
-__global__ void __launch_bounds__(256, 2)
+__global__ void __launch_bounds__(256, 3)
 lora_few_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restrict__ parts,
                 int shrink_items, int u_cols, int u_splits, int u_per_split, int slots_per_split) {
   extern __shared__ __align__(16) uint8_t lds[];
@@ -543,14 +549,8 @@ lora_join_kernel(LoraArgs args, LoraShape s, const float* __restrict__ u,
 
   // lane i < 16: the adapter of row 16 mb + i (-1: none).  Rows are sorted by adapter, so each
   // adapter's rows follow its first one.
-  int adapter = -1;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int t = fp.tile(16 * mb + i, lane);
-    const int e = readlane(fp.expert, max(t, 0));
-    const int found = t >= 0 && i < rows && uint32_t(e) < uint32_t(s.L) ? e : -1;
-    adapter = lane == i ? found : adapter;
-  }
+  int adapter = fp.adapter16(16 * mb, lane);
+  if (lane >= rows || adapter >= s.L || adapter < 0) adapter = -1;
   const uint32_t with = uint32_t(__ballot(adapter >= 0));
   const int before = __shfl_up(adapter, 1);
   uint32_t firsts = uint32_t(__ballot(adapter >= 0 && (lane == 0 || before != adapter)));

@@ -252,7 +252,7 @@ constexpr int kFewRows = 64, kFewCols = 64;
 constexpr int kFewSlotK = 64, kFewRowB = 2 * kFewSlotK;  // K and bytes of a slot's row: one line
 
 // u parts: a wave takes 16 rows of one adapter x 16 columns x pieces of 512 K
-constexpr int kUPiece = 512, kUSteps = kUPiece / 32, kUSplits = 4;
+constexpr int kUPiece = 512, kUSteps = kUPiece / 32, kUSplits = 16;
 
 // the plan's tiles by lane (at most 64 of up to 64 rows), and the tile of a sorted row
 struct FewPlan {

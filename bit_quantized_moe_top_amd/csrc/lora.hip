@@ -31,10 +31,13 @@ __device__ __forceinline__ v4f mfma(const uint4& a, const uint4& b, const v4f& c
 }
 
 __device__ __forceinline__ uint4 load16(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
-// 8 elements at k of a row of n (a multiple of 8), 0 past its end
-__device__ __forceinline__ uint4 load_k(const uint16_t* row, int k, int n) {
-  return k < n ? load16(row + k) : make_uint4(0u, 0u, 0u, 0u);
+// 8 elements at k of a row of n (a multiple of 8), 0 past its end: read inside the row by load_in,
+// and dropped by keep.  (A branch would keep the loads around it from being in flight together.)
+__device__ __forceinline__ uint4 load_in(const uint16_t* row, int k, int n) { return load16(row + min(k, n - 8)); }
+__device__ __forceinline__ uint4 keep(const uint4& v, bool in) {
+  return make_uint4(in ? v.x : 0u, in ? v.y : 0u, in ? v.z : 0u, in ? v.w : 0u);
 }
+__device__ __forceinline__ uint4 load_k(const uint16_t* row, int k, int n) { return keep(load_in(row, k, n), k < n); }
 
 // u of sorted row p, slice s: r hi values, then r lo values
 __device__ __forceinline__ int64_t u_at(int64_t p, int s, int slices, int r) {
@@ -58,11 +61,14 @@ __device__ __forceinline__ int plan_row(const PlanView& pv, int p, int M) {
 }
 
 // ------------------------------------------------------------------ shrink
-constexpr int kShrinkRows = 16, kShrinkCols = 32;
+// u of 16 rows of one adapter x 32 columns per workgroup.  Eight waves share K in pieces of 512,
+// all of a piece's loads in flight at once: the launch is a chain of memory latencies, not of work.
+constexpr int kShrinkRows = 16, kShrinkCols = 32, kShrinkWaves = 8;
+constexpr int kUPiece = 512, kUSteps = kUPiece / 32;     // K of a piece, and its steps
 
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(64 * kShrinkWaves)
 lora_shrink_kernel(LoraArgs args, LoraShape s, uint16_t* __restrict__ u) {
-  __shared__ v4f red[3][2][kWave];
+  __shared__ v4f red[kShrinkWaves][2][kWave];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int ln = lane & 15, kq = lane >> 4;
@@ -83,32 +89,41 @@ lora_shrink_kernel(LoraArgs args, LoraShape s, uint16_t* __restrict__ u) {
   for (int q = 0; q < 2; ++q)
     arow[q] = args.lora_a + (int64_t(l) * cols + min(c0 + 16 * q + ln, cols - 1)) * s.K;
   v4f acc[2] = {v4f{0.f, 0.f, 0.f, 0.f}, v4f{0.f, 0.f, 0.f, 0.f}};
-  for (int k0 = 32 * wave; k0 < s.K; k0 += 128) {
-    const int k = k0 + 8 * kq;
-    const uint4 xv = load_k(x, k, s.K);
+  for (int c = wave * kUPiece; c < s.K; c += kShrinkWaves * kUPiece) {
+    uint4 xv[kUSteps], av[2][kUSteps];
 #pragma unroll
-    for (int q = 0; q < 2; ++q) acc[q] = mfma(xv, load_k(arow[q], k, s.K), acc[q]);
+    for (int j = 0; j < kUSteps; ++j) {
+      const int k = c + 32 * j + 8 * kq;
+      xv[j] = load_in(x, k, s.K);
+      av[0][j] = load_in(arow[0], k, s.K);
+      av[1][j] = load_in(arow[1], k, s.K);
+    }
+    __builtin_amdgcn_sched_barrier(0);                   // all of them in flight
+#pragma unroll
+    for (int j = 0; j < kUSteps; ++j) {
+      const bool in = c + 32 * j + 8 * kq < s.K;
+      const uint4 v = keep(xv[j], in);
+      acc[0] = mfma(v, keep(av[0][j], in), acc[0]);
+      acc[1] = mfma(v, keep(av[1][j], in), acc[1]);
+    }
   }
-  if (wave > 0) {
-    red[wave - 1][0][lane] = acc[0];
-    red[wave - 1][1][lane] = acc[1];
-  }
+  red[wave][0][lane] = acc[0];
+  red[wave][1][lane] = acc[1];
   __syncthreads();
-  if (wave > 0) return;
+  if (wave > 1) return;
+  const int q = wave;                                    // wave q adds and stores columns 16 q ..
+  v4f sum = red[0][q][lane];
+#pragma unroll
+  for (int w = 1; w < kShrinkWaves; ++w) sum = sum + red[w][q][lane];
+  const int c = c0 + 16 * q + ln;
+  if (c >= cols) return;
   const float scale = args.scale[l];
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const v4f sum = acc[q] + (red[0][q][lane] + (red[1][q][lane] + red[2][q][lane]));
-    const int c = c0 + 16 * q + ln;
-    if (c >= cols) continue;
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int p = p0 + 4 * kq + v;
-      if (p >= p1) continue;
-      const float f = sum[v] * scale;
-      uint16_t* at = u + u_at(p, c / s.r, s.slices, s.r) + c % s.r;
-      split2(f, at[0], at[s.r]);
-    }
+  for (int v = 0; v < 4; ++v) {
+    const int p = p0 + 4 * kq + v;
+    if (p >= p1) continue;
+    uint16_t* at = u + u_at(p, c / s.r, s.slices, s.r) + c % s.r;
+    split2(sum[v] * scale, at[0], at[s.r]);
   }
 }
 
@@ -123,7 +138,8 @@ __device__ __forceinline__ int adapter_at(const PlanView& pv, int L, int p, int 
 
 // acc[i][q] += u B_l^T for the wave's rows p0 + 16 i .. and w rows wrow[q] .. + 15.  The
 // product of one adapter is formed by itself and added to its own rows only: what another
-// adapter holds, infinities and NaN too, does not reach them.
+// adapter holds, infinities and NaN too, does not reach them.  All operands of 32 ranks are loaded
+// at once; row blocks without a row of the adapter are left out.
 template <int MB, int NQ>
 __device__ __forceinline__ void add_adapters(v4f (&acc)[MB][NQ], const PlanView& pv,
                                              const LoraArgs& args, const LoraShape& s,
@@ -135,108 +151,262 @@ __device__ __forceinline__ void add_adapters(v4f (&acc)[MB][NQ], const PlanView&
     const int lo = max(pv.offsets[l], p0), hi = min(pv.offsets[l + 1], pend);
     if (lo >= pend) break;
     if (lo >= hi) continue;
+    for (int k0 = 0; k0 < s.r; k0 += 32) {
+      const int k = k0 + 8 * kq;
+      uint4 b[NQ];
 #pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-      const int slice = s.slices == 2 && wrow[q] >= s.N / 2;
-      const uint16_t* b = args.lora_b + (int64_t(l) * s.N + wrow[q] + ln) * s.r;
+      for (int q = 0; q < NQ; ++q) b[q] = load_k(args.lora_b + (int64_t(l) * s.N + wrow[q] + ln) * s.r, k, s.r);
+      for (int slice = 0; slice < s.slices; ++slice) {
+        uint4 uh[MB], ul[MB];
 #pragma unroll
-      for (int i = 0; i < MB; ++i) {
-        if (p0 + 16 * i >= hi || p0 + 16 * i + 16 <= lo) continue;
-        const uint16_t* up = u + u_at(min(p0 + 16 * i + ln, s.M - 1), slice, s.slices, s.r);
-        v4f d = v4f{0.f, 0.f, 0.f, 0.f};
-        for (int k0 = 0; k0 < s.r; k0 += 32) {
-          const int k = k0 + 8 * kq;
-          const uint4 bv = load_k(b, k, s.r);
-          d = mfma(load_k(up, k, s.r), bv, d);
-          d = mfma(load_k(up + s.r, k, s.r), bv, d);
+        for (int i = 0; i < MB; ++i) {
+          const uint16_t* up = u + u_at(min(p0 + 16 * i + ln, s.M - 1), slice, s.slices, s.r);
+          uh[i] = load_k(up, k, s.r);
+          ul[i] = load_k(up + s.r, k, s.r);
         }
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int p = p0 + 16 * i + 4 * kq + v;
-          acc[i][q][v] += p >= lo && p < hi ? d[v] : 0.0f;
+        for (int i = 0; i < MB; ++i) {
+          if (p0 + 16 * i >= hi || p0 + 16 * i + 16 <= lo) continue;
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) {
+            if (s.slices == 2 && (wrow[q] >= s.N / 2) != (slice == 1)) continue;
+            v4f d = v4f{0.f, 0.f, 0.f, 0.f};
+            d = mfma(uh[i], b[q], d);
+            d = mfma(ul[i], b[q], d);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const int p = p0 + 16 * i + 4 * kq + v;
+              acc[i][q][v] += p >= lo && p < hi ? d[v] : 0.0f;
+            }
+          }
         }
       }
     }
   }
 }
 
-// ------------------------------------------------------------- shared product
-constexpr int kTile = 64, kStep = 32, kPadRow = kStep + 8;
+// ------------------------------------------------------- operands through LDS
+// Rows of 64 K, one 128-byte line each, loaded straight into LDS.
+constexpr int kSlotK = 64, kRowB = 2 * kSlotK;
 
-template <int EPI>
-__global__ void __launch_bounds__(256)
+// Position of 16-byte chunk c of a 128-byte LDS row r: c ^ swz(r).  The 16 rows x 2 chunks that
+// 32 lanes of an operand read take are then 32 different 16-byte slots modulo 512 bytes.
+__device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
+
+// s_waitcnt vmcnt(n), the other counters unconstrained
+template <int n>
+__device__ __forceinline__ void wait_vmem() {
+  static_assert(n >= 0 && n < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+// every wave's LDS reads so far are done, without a wait for loads still in flight
+__device__ __forceinline__ void ring_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// 16 bytes per lane straight into LDS, lane l's at dst + 16 l (dst a wave-uniform LDS offset).
+// Written in assembly: the compiler, which counts such a load as a write of all of LDS, would wait
+// for every one in flight ahead of the next LDS read; here the ring's own waits order them.  (No
+// register receives the data, so nothing the compiler allocates is written behind its back; m0,
+// which names the LDS address, is used by nothing else in these kernels.)
+template <bool kOnce>                                    // read once: non-temporal
+__device__ __forceinline__ void load_lds(const uint16_t* src, uint32_t dst) {
+  if constexpr (kOnce)
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt"
+                 :: "v"(src), "s"(dst) : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+                 :: "v"(src), "s"(dst) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_offset(const uint8_t* p) {
+  return uint32_t(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) uint8_t*)p));
+}
+
+// ------------------------------------------------------------- shared product
+// B x B tiles; kWM x kWN waves of B / kWM rows x B / kWN columns.  The ring holds units: the 128-byte
+// pieces (64 K) of the tile's x rows or of its w rows, in turn.  The kUnits first go out up front.
+// A slot (an x unit and the w unit after it) is multiplied in two halves of 32 K, row block by row
+// block.  A row block's x operand is read anew, for the next half, as soon as its products are
+// issued, so it has a half's time to arrive and needs no second register; the w operands, used by
+// all row blocks, have two sets.  The ring moves on after kOpen row blocks of the second half of
+// slot st: by then its operands are in registers (lgkmcnt(0), which waits for nothing), and this
+// wave's loads of slot st + 1 have landed (all but the kUnits - 4 units issued after them); after
+// the barrier the same holds for every wave, so slot st + 1 can be read, and the next two units
+// take slot st's places.
+template <int B>
+struct Tile {
+  static constexpr int kWM = 2, kWN = B == 256 ? 4 : 2, kWaves = kWM * kWN;
+  static constexpr int kRows = B / kWM, kCols = B / kWN, kM = kRows / 16, kN = kCols / 16;
+  static constexpr int kUnitB = B * kRowB, kLoads = B / 8 / kWaves;    // loads of a unit per wave
+  // a CU's 160 KB for one workgroup of 256 x 256, half of them for smaller tiles
+  static constexpr int kUnits = B == 256 ? 5 : 80 * 1024 / kUnitB;
+  static constexpr int kLds = kUnits * kUnitB, kThreads = 64 * kWaves;
+  static_assert(kUnits >= 4, "two slots");
+};
+
+template <int EPI, int B>
+__global__ void __launch_bounds__(Tile<B>::kThreads, 2)
 lora_gemm_kernel(LoraArgs args, LoraShape s, const uint16_t* __restrict__ u) {
-  __shared__ __align__(16) uint16_t As[kTile * kPadRow], Bs[kTile * kPadRow];
+  using T = Tile<B>;
+  constexpr int kM = T::kM, kN = T::kN, kL = T::kLoads;  // kM x kN blocks of 16 x 16 per wave
+  constexpr bool kSilu = EPI == MOEQ_EPI_SILU_MUL;
+  extern __shared__ __align__(16) uint8_t lds[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int ln = lane & 15, kq = lane >> 4;
+  const int ln = lane & 15, kq = lane >> 4, lr = lane >> 3;
+  const int wm = wave / T::kWN, wn = wave % T::kWN;
   const PlanView pv = plan_view(args.plan, s.L + 1, s.M);
-  constexpr bool kSilu = EPI == MOEQ_EPI_SILU_MUL;
   const int cols = kSilu ? s.N / 2 : s.N;                // output columns, a multiple of 16
-  constexpr int kOutTile = kSilu ? kTile / 2 : kTile;    // output columns per workgroup
-  const int ntiles = (cols + kOutTile - 1) / kOutTile;
-  const int mt = blockIdx.x / ntiles, nt = blockIdx.x - mt * ntiles;
-  const int m0 = mt * kTile, n0 = nt * kOutTile;
-  const int wm = wave >> 1, wn = wave & 1;
+  constexpr int kOut = kSilu ? B / 2 : B;                // output columns per workgroup
+  // Workgroups go round the XCDs: each takes a run of tiles, all row tiles of a column tile before
+  // the next one, so that an XCD's tiles share their w rows in its L2.
+  const int mtiles = (s.M + B - 1) / B, tiles = gridDim.x;
+  const int xcd = blockIdx.x & 7;
+  const int tile = xcd * (tiles >> 3) + min(xcd, tiles & 7) + int(blockIdx.x >> 3);
+  const int nt = tile / mtiles, mt = tile - nt * mtiles;
+  const int m0 = mt * B, n0 = nt * kOut;
 
-  // w row of tile row i: 64 columns, or 32 gate and their 32 up rows; past the end the last one
+  // w row of tile row i: B columns, or B/2 gate and their B/2 up rows; past the end the last one
   // again (its results are not stored)
   const auto w_row = [&](int i) {
-    if (kSilu) return i < kTile / 2 ? min(n0 + i, cols - 1) : cols + min(n0 + i - kTile / 2, cols - 1);
+    if (kSilu) return i < B / 2 ? min(n0 + i, cols - 1) : cols + min(n0 + i - B / 2, cols - 1);
     return min(n0 + i, cols - 1);
   };
-  // the wave's 16-column blocks: two of its half, or one gate block and the matching up block
-  const auto block_row = [&](int q) { return kSilu ? q * (kTile / 2) + 16 * wn : 32 * wn + 16 * q; };
+  // tile row of the wave's 16-column block q: gate blocks, then the matching up blocks
+  const auto block_row = [&](int q) {
+    return kSilu ? (q < kN / 2 ? 0 : B / 2) + (T::kCols / 2) * wn + 16 * (q % (kN / 2))
+                 : T::kCols * wn + 16 * q;
+  };
 
-  const int sr = tid >> 2, sk = (tid & 3) * 8;
-  const uint16_t* xsrc = args.a + int64_t(plan_row(pv, m0 + sr, s.M)) * s.ld_a;
-  const uint16_t* wsrc = args.w + int64_t(w_row(sr)) * s.K;
-  v4f acc[2][2];
+  // loads: wave v moves rows 8 (kL v + g) + lr, lane's chunk (lane % 8) ^ swz(row)
+  const uint16_t *xsrc[kL], *wsrc[kL];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int q = 0; q < 2; ++q) acc[i][q] = v4f{0.f, 0.f, 0.f, 0.f};
-  uint4 xv = load_k(xsrc, sk, s.K), wv = load_k(wsrc, sk, s.K);
-  for (int k0 = 0; k0 < s.K; k0 += kStep) {
-    *reinterpret_cast<uint4*>(&As[sr * kPadRow + sk]) = xv;
-    *reinterpret_cast<uint4*>(&Bs[sr * kPadRow + sk]) = wv;
-    __syncthreads();
-    xv = load_k(xsrc, k0 + kStep + sk, s.K);
-    wv = load_k(wsrc, k0 + kStep + sk, s.K);
-    uint4 a[2], b[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) a[i] = load16(&As[(32 * wm + 16 * i + ln) * kPadRow + 8 * kq]);
-#pragma unroll
-    for (int q = 0; q < 2; ++q) b[q] = load16(&Bs[(block_row(q) + ln) * kPadRow + 8 * kq]);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int q = 0; q < 2; ++q) acc[i][q] = mfma(a[i], b[q], acc[i][q]);
-    __syncthreads();
+  for (int g = 0; g < kL; ++g) {
+    const int row = 8 * (kL * wave + g) + lr, c = ((lane & 7) ^ swz(row & 15)) * 8;
+    xsrc[g] = args.a + int64_t(plan_row(pv, m0 + row, s.M)) * s.ld_a + c;
+    wsrc[g] = args.w + int64_t(w_row(row)) * s.K + c;
   }
+  const uint32_t lds0 = lds_offset(lds) + 8 * kL * wave * kRowB;
+  const int slots = s.K / kSlotK;
+  // load g of unit `unit` (2 st: x, 2 st + 1: w of slot st); past the last slot, the last again
+  const auto issue = [&](bool is_w, int g, int unit) {
+    const int k = min(unit >> 1, slots - 1) * kSlotK;
+    load_lds<false>((is_w ? wsrc[g] : xsrc[g]) + k,
+                    lds0 + uint32_t(unit % T::kUnits) * T::kUnitB + 8 * g * kRowB);
+  };
+
+  v4f acc[kM][kN];
+#pragma unroll
+  for (int i = 0; i < kM; ++i)
+#pragma unroll
+    for (int q = 0; q < kN; ++q) acc[i][q] = v4f{0.f, 0.f, 0.f, 0.f};
+  const int rd[2] = {ln * kRowB + ((kq ^ swz(ln)) * 16), ln * kRowB + (((4 + kq) ^ swz(ln)) * 16)};
+  uint4 xa[kM], wb[2][kN];
+  const auto read_x = [&](int i, const uint8_t* buf, int h) {
+    xa[i] = *reinterpret_cast<const uint4*>(buf + (T::kRows * wm + 16 * i) * kRowB + rd[h]);
+  };
+  const auto read_w = [&](const uint8_t* buf, int h) {
+#pragma unroll
+    for (int q = 0; q < kN; ++q) wb[h][q] = *reinterpret_cast<const uint4*>(buf + block_row(q) * kRowB + rd[h]);
+  };
+  const auto multiply = [&](int i, int h) {
+#pragma unroll
+    for (int q = 0; q < kN; ++q) acc[i][q] = mfma(xa[i], wb[h][q], acc[i][q]);
+  };
+  constexpr int kOpen = kM / 4;
+
+  if (slots > 0) {
+#pragma unroll
+    for (int unit = 0; unit < T::kUnits; ++unit)
+#pragma unroll
+      for (int g = 0; g < kL; ++g) issue(unit & 1, g, unit);
+    wait_vmem<(T::kUnits - 2) * kL>();
+    ring_barrier();
+    int px = 0, pw = 1;                                  // ring places of the slot's units
+    read_w(lds + T::kUnitB, 0);
+#pragma unroll
+    for (int i = 0; i < kM; ++i) read_x(i, lds, 0);
+    const auto first_half = [&] {
+      read_w(lds + pw * T::kUnitB, 1);
+#pragma unroll
+      for (int i = 0; i < kM; ++i) {
+        multiply(i, 0);
+        read_x(i, lds + px * T::kUnitB, 1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    for (int st = 0; st + 1 < slots; ++st) {
+      first_half();
+      px = px + 2 >= T::kUnits ? px + 2 - T::kUnits : px + 2;
+      pw = pw + 2 >= T::kUnits ? pw + 2 - T::kUnits : pw + 2;
+      const int unit = 2 * st + T::kUnits;
+#pragma unroll
+      for (int i = 0; i < kM; ++i) {
+        if (i == kOpen) {
+          wait_vmem<(T::kUnits - 4) * kL>();
+          ring_barrier();
+          read_w(lds + pw * T::kUnitB, 0);
+#pragma unroll
+          for (int j = 0; j < kOpen; ++j) read_x(j, lds + px * T::kUnitB, 0);
+        }
+        multiply(i, 1);
+        if (i >= kOpen) {
+          read_x(i, lds + px * T::kUnitB, 0);
+          constexpr int kPer = (2 * kL + kM - kOpen - 1) / (kM - kOpen);
+#pragma unroll
+          for (int j = kPer * (i - kOpen); j < kPer * (i - kOpen + 1); ++j)
+            if (j < 2 * kL) issue((T::kUnits + j / kL) & 1, j % kL, unit + j / kL);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    first_half();
+#pragma unroll
+    for (int i = 0; i < kM; ++i) multiply(i, 1);
+    wait_vmem<0>();                                      // the loads past the last slot
+  }
+  if (s.K > slots * kSlotK) {                            // K past whole slots, zeros after it
+    ring_barrier();
+    const int k0 = slots * kSlotK;
+    for (int i = tid; i < 2 * B * 8; i += T::kThreads) {
+      const int row = i >> 3, c = i & 7;
+      const uint16_t* src = row < B ? args.a + int64_t(plan_row(pv, m0 + row, s.M)) * s.ld_a
+                                    : args.w + int64_t(w_row(row - B)) * s.K;
+      *reinterpret_cast<uint4*>(lds + row * kRowB + ((c ^ swz(row & 15)) * 16)) = load_k(src, k0 + 8 * c, s.K);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      read_w(lds + B * kRowB, h);
+#pragma unroll
+      for (int i = 0; i < kM; ++i) {
+        read_x(i, lds, h);
+        multiply(i, h);
+      }
+    }
+  }
+
   // first w row of each column block, kept inside W for blocks past the last column
-  int wrow[2], ocol[2];
+  int wrow[kN], ocol[kN];
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    ocol[q] = n0 + (kSilu ? 16 * wn : block_row(q));
-    wrow[q] = min(ocol[q], cols - 16) + (kSilu && q ? cols : 0);
+  for (int q = 0; q < kN; ++q) {
+    const bool up = kSilu && q >= kN / 2;
+    ocol[q] = n0 + block_row(q) - (up ? B / 2 : 0);
+    wrow[q] = min(ocol[q], cols - 16) + (up ? cols : 0);
   }
-  const int p0 = m0 + 32 * wm;
-  add_adapters<2, 2>(acc, pv, args, s, u, p0, wrow, lane);
+  const int p0 = m0 + T::kRows * wm;
+  add_adapters<kM, kN>(acc, pv, args, s, u, p0, wrow, lane);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < kM; ++i) {
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       const int p = p0 + 16 * i + 4 * kq + v;
       if (p >= s.M) continue;
       uint16_t* o = args.out + int64_t(plan_row(pv, p, s.M)) * cols;
-      if (kSilu) {
-        if (ocol[0] < cols) o[ocol[0] + ln] = to_bf16(silu_f32(acc[i][0][v]) * acc[i][1][v]);
-      } else {
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-          if (ocol[q] < cols) o[ocol[q] + ln] = to_bf16(acc[i][q][v]);
-      }
+      for (int q = 0; q < (kSilu ? kN / 2 : kN); ++q)
+        if (ocol[q] < cols)
+          o[ocol[q] + ln] = to_bf16(kSilu ? silu_f32(acc[i][q][v]) * acc[i][q + (kSilu ? kN / 2 : 0)][v] : acc[i][q][v]);
     }
   }
 }
@@ -249,10 +419,10 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, const uint16_t* __restrict__ u) {
 //
 // Parts are stored as the matrix instruction leaves them: 16 bytes per lane, 1 KB per block.
 constexpr int kFewRows = 64, kFewCols = 64;
-constexpr int kFewSlotK = 64, kFewRowB = 2 * kFewSlotK;  // K and bytes of a slot's row: one line
 
-// u parts: a wave takes 16 rows of one adapter x 16 columns x pieces of 512 K
-constexpr int kUPiece = 512, kUSteps = kUPiece / 32, kUSplits = 16;
+// u parts: a wave takes 16 rows of one adapter x 16 columns x a piece of 512 K (several, if there
+// are more than 16)
+constexpr int kUSplits = 16;
 
 // the plan's tiles by lane (at most 64 of up to 64 rows), and the tile of a sorted row
 struct FewPlan {
@@ -303,11 +473,15 @@ __device__ __forceinline__ void few_shrink(const LoraArgs& args, const LoraShape
   for (int c = c0; c < c1; ++c) {
     uint4 av[kUSteps], xv[kUSteps];
 #pragma unroll
-    for (int j = 0; j < kUSteps; ++j) av[j] = load_k(arow, c * kUPiece + 32 * j + 8 * kq, s.K);
+    for (int j = 0; j < kUSteps; ++j) av[j] = load_in(arow, c * kUPiece + 32 * j + 8 * kq, s.K);
 #pragma unroll
-    for (int j = 0; j < kUSteps; ++j) xv[j] = load_k(x, c * kUPiece + 32 * j + 8 * kq, s.K);
+    for (int j = 0; j < kUSteps; ++j) xv[j] = load_in(x, c * kUPiece + 32 * j + 8 * kq, s.K);
+    __builtin_amdgcn_sched_barrier(0);                   // all of them in flight
 #pragma unroll
-    for (int j = 0; j < kUSteps; ++j) acc = mfma(xv[j], av[j], acc);
+    for (int j = 0; j < kUSteps; ++j) {
+      const bool in = c * kUPiece + 32 * j + 8 * kq < s.K;
+      acc = mfma(keep(xv[j], in), keep(av[j], in), acc);
+    }
   }
   const int col = 16 * cb + ln;
 #pragma unroll
@@ -317,41 +491,8 @@ __device__ __forceinline__ void few_shrink(const LoraArgs& args, const LoraShape
   }
 }
 
-// Position of 16-byte chunk c of a 128-byte LDS row r: c ^ swz(r).  The 16 rows x 2 chunks that
-// 32 lanes of an operand read take are then 32 different 16-byte slots modulo 512 bytes.
-__device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
-
-// s_waitcnt vmcnt(n), the other counters unconstrained
-template <int n>
-__device__ __forceinline__ void wait_vmem() {
-  static_assert(n >= 0 && n < 64, "vmcnt range");
-  __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8));
-}
-// every wave's LDS reads so far are done, without a wait for loads still in flight
-__device__ __forceinline__ void ring_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-
-// 16 bytes per lane straight into LDS, lane l's at dst + 16 l (dst a wave-uniform LDS offset).
-// Written in assembly: the compiler, which counts such a load as a write of all of LDS, would wait
-// for every one in flight ahead of the next LDS read; here the ring's own waits order them.  (No
-// register receives the data, so nothing the compiler allocates is written behind its back; m0,
-// which names the LDS address, is used by nothing else in these kernels.)
-template <bool kOnce>                                    // read once: non-temporal
-__device__ __forceinline__ void load_lds(const uint16_t* src, uint32_t dst) {
-  if constexpr (kOnce)
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt"
-                 :: "v"(src), "s"(dst) : "memory");
-  else
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
-                 :: "v"(src), "s"(dst) : "memory");
-}
-__device__ __forceinline__ uint32_t lds_offset(const uint8_t* p) {
-  return uint32_t(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) uint8_t*)p));
-}
-
 template <int MB>
-constexpr int few_slot_bytes() { return (kFewCols + 16 * MB) * kFewRowB; }
+constexpr int few_slot_bytes() { return (kFewCols + 16 * MB) * kRowB; }
 // slots of the ring: what three workgroups of a CU can have in its 160 KB
 template <int MB>
 constexpr int few_ring() { return 160 * 1024 / 3 / few_slot_bytes<MB>(); }
@@ -382,7 +523,7 @@ lora_few_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restri
   constexpr int kLoads = 2 + kXLoads;
   const int ln = lane & 15, kq = lane >> 4;
   const PlanView pv = plan_view(args.plan, s.L + 1, s.M);
-  const int ntiles = (s.N + kFewCols - 1) / kFewCols, all_slots = s.K / kFewSlotK;
+  const int ntiles = (s.N + kFewCols - 1) / kFewCols, all_slots = s.K / kSlotK;
   const int b = blockIdx.x - shrink_blocks, splits = (gridDim.x - shrink_blocks) / ntiles;
   // (neighbouring workgroups take neighbouring ranges of the same rows)
   const int nt = b / splits, split = b - nt * splits;
@@ -393,7 +534,7 @@ lora_few_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restri
   const uint16_t* wsrc[2];
 #pragma unroll
   for (int g = 0; g < 2; ++g)
-    wsrc[g] = args.w + int64_t(min(n0 + 8 * g + lr, s.N - 1)) * s.K + s0 * kFewSlotK +
+    wsrc[g] = args.w + int64_t(min(n0 + 8 * g + lr, s.N - 1)) * s.K + s0 * kSlotK +
               (((lane & 7) ^ swz(8 * g + lr)) * 8);
   const uint16_t* xsrc[kXLoads];
 #pragma unroll
@@ -407,31 +548,31 @@ lora_few_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restri
       const int at = plan_row(pv, first + i, s.M);
       row = lr == i ? at : row;
     }
-    xsrc[g] = args.a + int64_t(row) * s.ld_a + s0 * kFewSlotK + (((lane & 7) ^ swz((first + lr) & 15)) * 8);
+    xsrc[g] = args.a + int64_t(row) * s.ld_a + s0 * kSlotK + (((lane & 7) ^ swz((first + lr) & 15)) * 8);
   }
   // slot st of this range; past the last one, the last again (into a buffer that is not read)
   const uint32_t lds0 = lds_offset(lds);
   auto issue = [&](int st) {
     const uint32_t buf = lds0 + (st % kSlots) * kSlotB;
-    const int k = min(st, n_slots - 1) * kFewSlotK;
+    const int k = min(st, n_slots - 1) * kSlotK;
 #pragma unroll
-    for (int g = 0; g < 2; ++g) load_lds<true>(wsrc[g] + k, buf + (16 * wave + 8 * g) * kFewRowB);
+    for (int g = 0; g < 2; ++g) load_lds<true>(wsrc[g] + k, buf + (16 * wave + 8 * g) * kRowB);
 #pragma unroll
     for (int g = 0; g < kXLoads; ++g)
       if (MB > 1 || lane < 32)
-        load_lds<false>(xsrc[g] + k, buf + (kFewCols + kXRows * wave + 8 * g) * kFewRowB);
+        load_lds<false>(xsrc[g] + k, buf + (kFewCols + kXRows * wave + 8 * g) * kRowB);
   };
   v4f acc[MB];
 #pragma unroll
   for (int i = 0; i < MB; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
-  const int rd[2] = {ln * kFewRowB + ((kq ^ swz(ln)) * 16), ln * kFewRowB + (((4 + kq) ^ swz(ln)) * 16)};
+  const int rd[2] = {ln * kRowB + ((kq ^ swz(ln)) * 16), ln * kRowB + (((4 + kq) ^ swz(ln)) * 16)};
   auto multiply = [&](const uint8_t* buf) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint4 wv = *reinterpret_cast<const uint4*>(buf + 16 * wave * kFewRowB + rd[h]);
+      const uint4 wv = *reinterpret_cast<const uint4*>(buf + 16 * wave * kRowB + rd[h]);
 #pragma unroll
       for (int i = 0; i < MB; ++i)
-        acc[i] = mfma(*reinterpret_cast<const uint4*>(buf + (kFewCols + 16 * i) * kFewRowB + rd[h]), wv, acc[i]);
+        acc[i] = mfma(*reinterpret_cast<const uint4*>(buf + (kFewCols + 16 * i) * kRowB + rd[h]), wv, acc[i]);
     }
   };
   if (n_slots > 0) {
@@ -448,16 +589,16 @@ lora_few_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restri
     }
     wait_vmem<0>();
   }
-  const int tail = s.K - all_slots * kFewSlotK;          // K past whole slots, zeros after it
+  const int tail = s.K - all_slots * kSlotK;          // K past whole slots, zeros after it
   if (tail > 0 && split == splits - 1) {
     ring_barrier();
-    const int k0 = all_slots * kFewSlotK;
+    const int k0 = all_slots * kSlotK;
     for (int i = tid; i < (kFewCols + 16 * MB) * 8; i += 256) {
       const int row = i >> 3, c = i & 7;
       const uint16_t* src = row < kFewCols
           ? args.w + int64_t(min(nt * kFewCols + row, s.N - 1)) * s.K
           : args.a + int64_t(plan_row(pv, row - kFewCols, s.M)) * s.ld_a;
-      *reinterpret_cast<uint4*>(lds + row * kFewRowB + ((c ^ swz(row & 15)) * 16)) = load_k(src, k0 + 8 * c, s.K);
+      *reinterpret_cast<uint4*>(lds + row * kRowB + ((c ^ swz(row & 15)) * 16)) = load_k(src, k0 + 8 * c, s.K);
     }
     __syncthreads();
     multiply(lds);
@@ -664,7 +805,7 @@ struct FewSplit {
 };
 FewSplit few_split(const LoraShape& s) {
   const int ntiles = (s.N + kFewCols - 1) / kFewCols;
-  const int slots = s.K / kFewSlotK > 0 ? s.K / kFewSlotK : 1;
+  const int slots = s.K / kSlotK > 0 ? s.K / kSlotK : 1;
   int want = (512 + ntiles - 1) / ntiles;
   if (want > slots) want = slots;
   const int per = (slots + want - 1) / want;
@@ -704,6 +845,22 @@ hipError_t launch_few(const LoraArgs& args, const LoraShape& s, hipStream_t stre
   return hipGetLastError();
 }
 
+constexpr int64_t kEnoughTiles = 200;
+int64_t tiles_of(const LoraShape& s, int b) {
+  return int64_t((s.M + b - 1) / b) * ((s.N + b - 1) / b);
+}
+
+template <int B>
+hipError_t launch_tiles(const LoraArgs& args, const LoraShape& s, const uint16_t* u, hipStream_t stream) {
+  const bool silu = s.epilogue == MOEQ_EPI_SILU_MUL;
+  const auto fn = silu ? lora_gemm_kernel<MOEQ_EPI_SILU_MUL, B> : lora_gemm_kernel<MOEQ_EPI_NONE, B>;
+  const hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void*>(fn),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, Tile<B>::kLds);
+  if (err != hipSuccess) return err;
+  hipLaunchKernelGGL(fn, dim3(unsigned(tiles_of(s, B))), dim3(Tile<B>::kThreads), Tile<B>::kLds, stream, args, s, u);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 size_t lora_ws_bytes(const LoraShape& s) {
@@ -719,19 +876,12 @@ hipError_t launch_shared_gemm_lora(const LoraArgs& args, const LoraShape& s, hip
   uint16_t* u = static_cast<uint16_t*>(args.ws);
   const dim3 sgrid(unsigned(plan_max_tiles(s.L + 1, s.M)) * (MOEQ_TILE_M / kShrinkRows),
                    unsigned((s.slices * s.r + kShrinkCols - 1) / kShrinkCols));
-  hipLaunchKernelGGL(lora_shrink_kernel, sgrid, dim3(256), 0, stream, args, s, u);
+  hipLaunchKernelGGL(lora_shrink_kernel, sgrid, dim3(64 * kShrinkWaves), 0, stream, args, s, u);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  const bool silu = s.epilogue == MOEQ_EPI_SILU_MUL;
-  const int cols = silu ? s.N / 2 : s.N, out_tile = silu ? kTile / 2 : kTile;
-  const int64_t blocks = int64_t((s.M + kTile - 1) / kTile) * ((cols + out_tile - 1) / out_tile);
-  if (silu)
-    hipLaunchKernelGGL(lora_gemm_kernel<MOEQ_EPI_SILU_MUL>, dim3(unsigned(blocks)), dim3(256), 0, stream,
-                       args, s, u);
-  else
-    hipLaunchKernelGGL(lora_gemm_kernel<MOEQ_EPI_NONE>, dim3(unsigned(blocks)), dim3(256), 0, stream,
-                       args, s, u);
-  return hipGetLastError();
+  if (tiles_of(s, 256) >= kEnoughTiles) return launch_tiles<256>(args, s, u, stream);
+  if (tiles_of(s, 128) >= kEnoughTiles) return launch_tiles<128>(args, s, u, stream);
+  return launch_tiles<64>(args, s, u, stream);
 }
 
 }  // namespace moeq

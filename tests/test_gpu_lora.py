@@ -95,6 +95,9 @@ SHAPES = [
     (40, 32, 4096, 3, 1, 64), (63, 2080, 320, 8, 2, 8), (64, 128, 512, 3, 1, 16),
     (65, 1504, 1448, 9, 1, 24), (128, 512, 2048, 6, 2, 16), (130, 96, 200, 7, 2, 64),
     (257, 544, 1032, 60, 2, 48), (300, 528, 136, 20, 1, 256), (600, 320, 448, 4, 1, 128),
+    # enough tiles for the larger ones, ragged in every direction
+    (260, 8544, 200, 5, 2, 16), (2500, 5408, 136, 4, 2, 24), (1300, 10272, 328, 70, 1, 64),
+    (1500, 8736, 48, 3, 2, 8),
 ]
 
 

@@ -39,11 +39,6 @@ __device__ __forceinline__ uint4 keep(const uint4& v, bool in) {
 }
 __device__ __forceinline__ uint4 load_k(const uint16_t* row, int k, int n) { return keep(load_in(row, k, n), k < n); }
 
-// u of sorted row p, slice s: r hi values, then r lo values
-__device__ __forceinline__ int64_t u_at(int64_t p, int s, int slices, int r) {
-  return (p * slices + s) * 2 * r;
-}
-
 // round to nearest even (NaNs stay NaNs)
 __device__ __forceinline__ uint16_t to_bf16(float f) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f)); }
 
@@ -61,19 +56,20 @@ __device__ __forceinline__ int plan_row(const PlanView& pv, int p, int M) {
 }
 
 // ------------------------------------------------------------------ shrink
-// u of 16 rows of one adapter x 32 columns per workgroup.  Eight waves share K in pieces of 512,
-// all of a piece's loads in flight at once: the launch is a chain of memory latencies, not of work.
-constexpr int kShrinkRows = 16, kShrinkCols = 32, kShrinkWaves = 8;
-constexpr int kUPiece = 512, kUSteps = kUPiece / 32;     // K of a piece, and its steps
+// Parts of u: 32 rows of one adapter x 32 columns x a share of K per workgroup, summed over its
+// four waves, [split][M][columns] in fp32.  A wave takes K in pieces of 256, all of a piece's loads
+// in flight at once: the launch is a chain of memory latencies, not of work.
+constexpr int kShrinkRows = 32, kShrinkCols = 32;
+constexpr int kShrinkPiece = 256, kShrinkSteps = kShrinkPiece / 32;
 
-__global__ void __launch_bounds__(64 * kShrinkWaves)
-lora_shrink_kernel(LoraArgs args, LoraShape s, uint16_t* __restrict__ u) {
-  __shared__ v4f red[kShrinkWaves][2][kWave];
+__global__ void __launch_bounds__(256)
+lora_shrink_kernel(LoraArgs args, LoraShape s, float* __restrict__ u) {
+  __shared__ v4f red[4][4][kWave];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int ln = lane & 15, kq = lane >> 4;
   const PlanView pv = plan_view(args.plan, s.L + 1, s.M);
-  // blockIdx.x: plan tile and its 16-row part; blockIdx.y: 32 columns of u
+  // blockIdx.x: plan tile and its 32-row part; blockIdx.y: 32 columns of u; blockIdx.z: split of K
   constexpr int kParts = MOEQ_TILE_M / kShrinkRows;
   const int tile = blockIdx.x / kParts, part = blockIdx.x % kParts;
   if (tile >= min(pv.base[kPlanTiles], pv.max_tiles)) return;
@@ -83,47 +79,45 @@ lora_shrink_kernel(LoraArgs args, LoraShape s, uint16_t* __restrict__ u) {
   const int p1 = min(min(pv.offsets[l + 1], s.M), pv.tile_row0[tile] + MOEQ_TILE_M);
   if (p0 < 0 || p0 >= p1) return;
   const int cols = s.slices * s.r, c0 = blockIdx.y * kShrinkCols;
-  const uint16_t* x = args.a + int64_t(plan_row(pv, min(p0 + ln, p1 - 1), s.M)) * s.ld_a;
-  const uint16_t* arow[2];
+  const uint16_t *x[2], *a[2];
 #pragma unroll
-  for (int q = 0; q < 2; ++q)
-    arow[q] = args.lora_a + (int64_t(l) * cols + min(c0 + 16 * q + ln, cols - 1)) * s.K;
-  v4f acc[2] = {v4f{0.f, 0.f, 0.f, 0.f}, v4f{0.f, 0.f, 0.f, 0.f}};
-  for (int c = wave * kUPiece; c < s.K; c += kShrinkWaves * kUPiece) {
-    uint4 xv[kUSteps], av[2][kUSteps];
+  for (int q = 0; q < 2; ++q) {
+    x[q] = args.a + int64_t(plan_row(pv, min(p0 + 16 * q + ln, p1 - 1), s.M)) * s.ld_a;
+    a[q] = args.lora_a + (int64_t(l) * cols + min(c0 + 16 * q + ln, cols - 1)) * s.K;
+  }
+  v4f acc[2][2];
 #pragma unroll
-    for (int j = 0; j < kUSteps; ++j) {
-      const int k = c + 32 * j + 8 * kq;
-      xv[j] = load_in(x, k, s.K);
-      av[0][j] = load_in(arow[0], k, s.K);
-      av[1][j] = load_in(arow[1], k, s.K);
-    }
+  for (int i = 0; i < 4; ++i) acc[i >> 1][i & 1] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int c = (4 * blockIdx.z + wave) * kShrinkPiece; c < s.K; c += 4 * gridDim.z * kShrinkPiece) {
+    uint4 xv[2][kShrinkSteps], av[2][kShrinkSteps];
+#pragma unroll
+    for (int j = 0; j < kShrinkSteps; ++j)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        xv[q][j] = load_in(x[q], c + 32 * j + 8 * kq, s.K);
+        av[q][j] = load_in(a[q], c + 32 * j + 8 * kq, s.K);
+      }
     __builtin_amdgcn_sched_barrier(0);                   // all of them in flight
 #pragma unroll
-    for (int j = 0; j < kUSteps; ++j) {
+    for (int j = 0; j < kShrinkSteps; ++j) {
       const bool in = c + 32 * j + 8 * kq < s.K;
-      const uint4 v = keep(xv[j], in);
-      acc[0] = mfma(v, keep(av[0][j], in), acc[0]);
-      acc[1] = mfma(v, keep(av[1][j], in), acc[1]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        acc[i >> 1][i & 1] = mfma(keep(xv[i >> 1][j], in), keep(av[i & 1][j], in), acc[i >> 1][i & 1]);
     }
   }
-  red[wave][0][lane] = acc[0];
-  red[wave][1][lane] = acc[1];
-  __syncthreads();
-  if (wave > 1) return;
-  const int q = wave;                                    // wave q adds and stores columns 16 q ..
-  v4f sum = red[0][q][lane];
 #pragma unroll
-  for (int w = 1; w < kShrinkWaves; ++w) sum = sum + red[w][q][lane];
-  const int c = c0 + 16 * q + ln;
-  if (c >= cols) return;
+  for (int i = 0; i < 4; ++i) red[wave][i][lane] = acc[i >> 1][i & 1];
+  __syncthreads();
+  // wave w adds and stores block w: rows 16 (w / 2) .., columns 16 (w % 2) ..
+  const v4f sum = (red[0][wave][lane] + red[1][wave][lane]) + (red[2][wave][lane] + red[3][wave][lane]);
+  const int col = c0 + 16 * (wave & 1) + ln;
   const float scale = args.scale[l];
+  u += int64_t(blockIdx.z) * s.M * cols;
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
-    const int p = p0 + 4 * kq + v;
-    if (p >= p1) continue;
-    uint16_t* at = u + u_at(p, c / s.r, s.slices, s.r) + c % s.r;
-    split2(sum[v] * scale, at[0], at[s.r]);
+    const int p = p0 + 16 * (wave >> 1) + 4 * kq + v;
+    if (p < p1 && col < cols) u[int64_t(p) * cols + col] = sum[v] * scale;
   }
 }
 
@@ -134,55 +128,6 @@ __device__ __forceinline__ int adapter_at(const PlanView& pv, int L, int p, int 
   for (int a0 = 0; a0 <= L; a0 += kWave)
     n += __popcll(__ballot(a0 + lane <= L && pv.offsets[min(a0 + lane, L) + 1] <= p));
   return n;
-}
-
-// acc[i][q] += u B_l^T for the wave's rows p0 + 16 i .. and w rows wrow[q] .. + 15.  The
-// product of one adapter is formed by itself and added to its own rows only: what another
-// adapter holds, infinities and NaN too, does not reach them.  All operands of 32 ranks are loaded
-// at once; row blocks without a row of the adapter are left out.
-template <int MB, int NQ>
-__device__ __forceinline__ void add_adapters(v4f (&acc)[MB][NQ], const PlanView& pv,
-                                             const LoraArgs& args, const LoraShape& s,
-                                             const uint16_t* u, int p0, const int (&wrow)[NQ],
-                                             int lane) {
-  const int ln = lane & 15, kq = lane >> 4;
-  const int pend = min(p0 + 16 * MB, s.M);
-  for (int l = adapter_at(pv, s.L, p0, lane); l < s.L; ++l) {
-    const int lo = max(pv.offsets[l], p0), hi = min(pv.offsets[l + 1], pend);
-    if (lo >= pend) break;
-    if (lo >= hi) continue;
-    for (int k0 = 0; k0 < s.r; k0 += 32) {
-      const int k = k0 + 8 * kq;
-      uint4 b[NQ];
-#pragma unroll
-      for (int q = 0; q < NQ; ++q) b[q] = load_k(args.lora_b + (int64_t(l) * s.N + wrow[q] + ln) * s.r, k, s.r);
-      for (int slice = 0; slice < s.slices; ++slice) {
-        uint4 uh[MB], ul[MB];
-#pragma unroll
-        for (int i = 0; i < MB; ++i) {
-          const uint16_t* up = u + u_at(min(p0 + 16 * i + ln, s.M - 1), slice, s.slices, s.r);
-          uh[i] = load_k(up, k, s.r);
-          ul[i] = load_k(up + s.r, k, s.r);
-        }
-#pragma unroll
-        for (int i = 0; i < MB; ++i) {
-          if (p0 + 16 * i >= hi || p0 + 16 * i + 16 <= lo) continue;
-#pragma unroll
-          for (int q = 0; q < NQ; ++q) {
-            if (s.slices == 2 && (wrow[q] >= s.N / 2) != (slice == 1)) continue;
-            v4f d = v4f{0.f, 0.f, 0.f, 0.f};
-            d = mfma(uh[i], b[q], d);
-            d = mfma(ul[i], b[q], d);
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              const int p = p0 + 16 * i + 4 * kq + v;
-              acc[i][q][v] += p >= lo && p < hi ? d[v] : 0.0f;
-            }
-          }
-        }
-      }
-    }
-  }
 }
 
 // ------------------------------------------------------- operands through LDS
@@ -244,9 +189,116 @@ struct Tile {
   static_assert(kUnits >= 4, "two slots");
 };
 
+// acc[i][q] += u B_l^T for the wave's rows p0 + 16 i .. and w rows wrow[q] .. + 15, by all waves of
+// the workgroup together.  The tile's u, its parts summed, goes to LDS in two bf16 values, 64
+// ranks of every slice at a time, [row][slice][hi, lo]; B comes from memory.  The product of one adapter is formed by itself and added to its own rows
+// only: what another adapter holds, infinities and NaN too, does not reach them.
+template <typename T>
+__device__ __forceinline__ void add_adapters(v4f (&acc)[T::kM][T::kN], const PlanView& pv,
+                                             const LoraArgs& args, const LoraShape& s, const float* u,
+                                             int u_splits, uint8_t* lds, int m0, int p0,
+                                             const int (&wrow)[T::kN], int lane) {
+  constexpr int kM = T::kM, kN = T::kN;
+  const int ln = lane & 15, kq = lane >> 4;
+  const int pend = min(p0 + 16 * kM, s.M);
+  // the adapters of the wave's rows: the first, and the offsets of 64 groups from there
+  const int first = p0 < s.M ? adapter_at(pv, s.L, p0, lane) : s.L;
+  int window = first;
+  int off = pv.offsets[min(window + lane, s.L + 1)];
+  const auto offset = [&](int l) {
+    if (l < window || l - window >= kWave) {
+      window = l;
+      off = pv.offsets[min(window + lane, s.L + 1)];
+    }
+    return readlane(off, l - window);
+  };
+  // the next adapter with rows from l on (s.L: none)
+  int lo = 0, hi = 0;
+  const auto next_adapter = [&](int l) {
+    for (; l < s.L; ++l) {
+      lo = max(offset(l), p0);
+      hi = min(offset(l + 1), pend);
+      if (lo < hi) return l;
+      if (lo >= pend) break;
+    }
+    return s.L;
+  };
+  const int cols = s.slices * s.r;
+  for (int k0 = 0; k0 < s.r; k0 += 64) {
+    const int kc = s.r - k0 > 32 ? 64 : 32;              // ranks in LDS, zeros past r
+    const int plane = 2 * kc, row_bytes = s.slices * 2 * plane + 16;
+    const bool two = kc == 64;
+    uint4 b[2][kN];
+    const auto load_b = [&](int l) {
+#pragma unroll
+      for (int q = 0; q < kN; ++q) {
+        const uint16_t* at = args.lora_b + (int64_t(l) * s.N + wrow[q] + ln) * s.r;
+        b[0][q] = load_in(at, k0 + 8 * kq, s.r);
+        b[1][q] = load_in(at, k0 + 32 + 8 * kq, s.r);
+      }
+    };
+    int l = next_adapter(first);
+    if (l < s.L) load_b(l);
+    if (k0 > 0) __syncthreads();                         // the ranks before are done with
+    const int rows = min(T::kWM * T::kRows, s.M - m0), quads = kc / 4;
+    for (int i = threadIdx.x; i < rows * s.slices * quads; i += T::kThreads) {
+      const int row = i / (s.slices * quads), c = i - row * (s.slices * quads);
+      const int slice = c / quads, k = k0 + 4 * (c - slice * quads);
+      const float* at = u + int64_t(m0 + row) * cols + slice * s.r + min(k, s.r - 4);
+      v4f v[4], f;
+      f = *reinterpret_cast<const v4f*>(at);
+#pragma unroll
+      for (int j = 1; j < 4; ++j) v[j] = *reinterpret_cast<const v4f*>(at + min(j, u_splits - 1) * int64_t(s.M) * cols);
+#pragma unroll
+      for (int j = 1; j < 4; ++j)
+        if (j < u_splits) f = f + v[j];
+      uint16_t h[4], o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) split2(k < s.r ? f[j] : 0.0f, h[j], o[j]);
+      uint8_t* to = lds + row * row_bytes + slice * 2 * plane + (k - k0) * 2;
+      *reinterpret_cast<uint2*>(to) = make_uint2(h[0] | uint32_t(h[1]) << 16, h[2] | uint32_t(h[3]) << 16);
+      *reinterpret_cast<uint2*>(to + plane) = make_uint2(o[0] | uint32_t(o[1]) << 16, o[2] | uint32_t(o[3]) << 16);
+    }
+    __syncthreads();
+    while (l < s.L) {
+      const int from = lo, to = hi;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int q = 0; q < kN; ++q) b[j][q] = keep(b[j][q], k0 + 32 * j + 8 * kq < s.r);
+#pragma unroll
+      for (int i = 0; i < kM; ++i) {
+        const int pi = p0 + 16 * i;
+        if (pi < to && pi + 16 > from) {
+          bool mine[4];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) mine[v] = pi + 4 * kq + v >= from && pi + 4 * kq + v < to;
+          const uint8_t* at = lds + (pi - m0 + ln) * row_bytes + 16 * kq;
+#pragma unroll
+          for (int q = 0; q < kN; ++q) {
+            const int slice = s.slices == 2 && wrow[q] >= s.N / 2 ? 2 * plane : 0;
+            v4f d = v4f{0.f, 0.f, 0.f, 0.f};
+            d = mfma(*reinterpret_cast<const uint4*>(at + slice), b[0][q], d);
+            d = mfma(*reinterpret_cast<const uint4*>(at + slice + plane), b[0][q], d);
+            if (two) {
+              d = mfma(*reinterpret_cast<const uint4*>(at + slice + 64), b[1][q], d);
+              d = mfma(*reinterpret_cast<const uint4*>(at + slice + plane + 64), b[1][q], d);
+            }
+#pragma unroll
+            for (int v = 0; v < 4; ++v) acc[i][q][v] += mine[v] ? d[v] : 0.0f;
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      l = next_adapter(l + 1);
+      if (l < s.L) load_b(l);
+    }
+  }
+}
+
 template <int EPI, int B>
 __global__ void __launch_bounds__(Tile<B>::kThreads, 2)
-lora_gemm_kernel(LoraArgs args, LoraShape s, const uint16_t* __restrict__ u) {
+lora_gemm_kernel(LoraArgs args, LoraShape s, const float* __restrict__ u, int u_splits) {
   using T = Tile<B>;
   constexpr int kM = T::kM, kN = T::kN, kL = T::kLoads;  // kM x kN blocks of 16 x 16 per wave
   constexpr bool kSilu = EPI == MOEQ_EPI_SILU_MUL;
@@ -395,18 +447,23 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, const uint16_t* __restrict__ u) {
     wrow[q] = min(ocol[q], cols - 16) + (up ? cols : 0);
   }
   const int p0 = m0 + T::kRows * wm;
-  add_adapters<kM, kN>(acc, pv, args, s, u, p0, wrow, lane);
+  ring_barrier();                                        // the ring's LDS is free
+  add_adapters<T>(acc, pv, args, s, u, u_splits, lds, m0, p0, wrow, lane);
 #pragma unroll
   for (int i = 0; i < kM; ++i) {
+    // (four rows at a time: the rows' places hoisted together would take the accumulators' registers)
+    __builtin_amdgcn_sched_barrier(0);
+    int row[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) row[v] = plan_row(pv, p0 + 16 * i + 4 * kq + v, s.M);
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const int p = p0 + 16 * i + 4 * kq + v;
-      if (p >= s.M) continue;
-      uint16_t* o = args.out + int64_t(plan_row(pv, p, s.M)) * cols;
+      if (p0 + 16 * i + 4 * kq + v >= s.M) continue;
+      uint16_t* o = args.out + int64_t(row[v]) * cols + ln;
 #pragma unroll
       for (int q = 0; q < (kSilu ? kN / 2 : kN); ++q)
         if (ocol[q] < cols)
-          o[ocol[q] + ln] = to_bf16(kSilu ? silu_f32(acc[i][q][v]) * acc[i][q + (kSilu ? kN / 2 : 0)][v] : acc[i][q][v]);
+          o[ocol[q]] = to_bf16(kSilu ? silu_f32(acc[i][q][v]) * acc[i][q + (kSilu ? kN / 2 : 0)][v] : acc[i][q][v]);
     }
   }
 }
@@ -422,7 +479,7 @@ constexpr int kFewRows = 64, kFewCols = 64;
 
 // u parts: a wave takes 16 rows of one adapter x 16 columns x a piece of 512 K (several, if there
 // are more than 16)
-constexpr int kUSplits = 16;
+constexpr int kUPiece = 512, kUSteps = kUPiece / 32, kUSplits = 16;
 
 // the plan's tiles by lane (at most 64 of up to 64 rows), and the tile of a sorted row
 struct FewPlan {
@@ -845,19 +902,28 @@ hipError_t launch_few(const LoraArgs& args, const LoraShape& s, hipStream_t stre
   return hipGetLastError();
 }
 
+// splits of K of the parts of u, at most 4 (add_adapters): for up to 4096 rows, whose blocks of 32
+// alone would leave CUs idle
+int shrink_splits(const LoraShape& s) {
+  const int pieces = (s.K + 4 * kShrinkPiece - 1) / (4 * kShrinkPiece);
+  return s.M > 4096 ? 1 : pieces < 4 ? pieces : 4;
+}
+
 constexpr int64_t kEnoughTiles = 200;
 int64_t tiles_of(const LoraShape& s, int b) {
   return int64_t((s.M + b - 1) / b) * ((s.N + b - 1) / b);
 }
 
 template <int B>
-hipError_t launch_tiles(const LoraArgs& args, const LoraShape& s, const uint16_t* u, hipStream_t stream) {
+hipError_t launch_tiles(const LoraArgs& args, const LoraShape& s, const float* u, int u_splits,
+                        hipStream_t stream) {
   const bool silu = s.epilogue == MOEQ_EPI_SILU_MUL;
   const auto fn = silu ? lora_gemm_kernel<MOEQ_EPI_SILU_MUL, B> : lora_gemm_kernel<MOEQ_EPI_NONE, B>;
   const hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void*>(fn),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, Tile<B>::kLds);
   if (err != hipSuccess) return err;
-  hipLaunchKernelGGL(fn, dim3(unsigned(tiles_of(s, B))), dim3(Tile<B>::kThreads), Tile<B>::kLds, stream, args, s, u);
+  hipLaunchKernelGGL(fn, dim3(unsigned(tiles_of(s, B))), dim3(Tile<B>::kThreads), Tile<B>::kLds, stream, args, s, u,
+                     u_splits);
   return hipGetLastError();
 }
 
@@ -865,7 +931,7 @@ hipError_t launch_tiles(const LoraArgs& args, const LoraShape& s, const uint16_t
 
 size_t lora_ws_bytes(const LoraShape& s) {
   if (s.M <= kFewRows) return few_u_bytes(s) + align256(few_part_bytes(s)) + 256;
-  return align256(size_t(s.M) * s.slices * 2 * s.r * sizeof(uint16_t));
+  return align256(size_t(shrink_splits(s)) * s.M * s.slices * s.r * sizeof(float));
 }
 
 hipError_t launch_shared_gemm_lora(const LoraArgs& args, const LoraShape& s, hipStream_t stream) {
@@ -873,15 +939,16 @@ hipError_t launch_shared_gemm_lora(const LoraArgs& args, const LoraShape& s, hip
   if (s.M <= 16) return launch_few<1>(args, s, stream);
   if (s.M <= 32) return launch_few<2>(args, s, stream);
   if (s.M <= kFewRows) return launch_few<4>(args, s, stream);
-  uint16_t* u = static_cast<uint16_t*>(args.ws);
+  float* u = static_cast<float*>(args.ws);
+  const int splits = shrink_splits(s);
   const dim3 sgrid(unsigned(plan_max_tiles(s.L + 1, s.M)) * (MOEQ_TILE_M / kShrinkRows),
-                   unsigned((s.slices * s.r + kShrinkCols - 1) / kShrinkCols));
-  hipLaunchKernelGGL(lora_shrink_kernel, sgrid, dim3(64 * kShrinkWaves), 0, stream, args, s, u);
+                   unsigned((s.slices * s.r + kShrinkCols - 1) / kShrinkCols), unsigned(splits));
+  hipLaunchKernelGGL(lora_shrink_kernel, sgrid, dim3(256), 0, stream, args, s, u);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  if (tiles_of(s, 256) >= kEnoughTiles) return launch_tiles<256>(args, s, u, stream);
-  if (tiles_of(s, 128) >= kEnoughTiles) return launch_tiles<128>(args, s, u, stream);
-  return launch_tiles<64>(args, s, u, stream);
+  if (tiles_of(s, 256) >= kEnoughTiles) return launch_tiles<256>(args, s, u, splits, stream);
+  if (tiles_of(s, 128) >= kEnoughTiles) return launch_tiles<128>(args, s, u, splits, stream);
+  return launch_tiles<64>(args, s, u, splits, stream);
 }
 
 }  // namespace moeq

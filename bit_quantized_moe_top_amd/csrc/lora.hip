@@ -57,10 +57,10 @@ __device__ __forceinline__ int plan_row(const PlanView& pv, int p, int M) {
 
 // ------------------------------------------------------------------ shrink
 // Parts of u: 32 rows of one adapter x 32 columns x a share of K per workgroup, summed over its
-// four waves, [split][M][columns] in fp32.  A wave takes K in pieces of 256, all of a piece's loads
+// four waves, [split][M][columns] in fp32.  A wave takes K in pieces of 128, all of a piece's loads
 // in flight at once: the launch is a chain of memory latencies, not of work.
 constexpr int kShrinkRows = 32, kShrinkCols = 32;
-constexpr int kShrinkPiece = 256, kShrinkSteps = kShrinkPiece / 32;
+constexpr int kShrinkPiece = 128, kShrinkSteps = kShrinkPiece / 32;
 
 __global__ void __launch_bounds__(256)
 lora_shrink_kernel(LoraArgs args, LoraShape s, float* __restrict__ u) {
@@ -72,19 +72,21 @@ lora_shrink_kernel(LoraArgs args, LoraShape s, float* __restrict__ u) {
   // blockIdx.x: plan tile and its 32-row part; blockIdx.y: 32 columns of u; blockIdx.z: split of K
   constexpr int kParts = MOEQ_TILE_M / kShrinkRows;
   const int tile = blockIdx.x / kParts, part = blockIdx.x % kParts;
-  if (tile >= min(pv.base[kPlanTiles], pv.max_tiles)) return;
-  const int l = pv.tile_expert[tile];
-  if (l < 0 || l >= s.L) return;                         // rows without an adapter
-  const int p0 = pv.tile_row0[tile] + part * kShrinkRows;
-  const int p1 = min(min(pv.offsets[l + 1], s.M), pv.tile_row0[tile] + MOEQ_TILE_M);
-  if (p0 < 0 || p0 >= p1) return;
+  // (the plan's words in as few dependent loads as they take: adapter and first row of the tile, then
+  // the end of the adapter's rows and the rows' places, then the rows)
+  const int n_tiles = pv.base[kPlanTiles], l = pv.tile_expert[tile], row0 = pv.tile_row0[tile];
+  if (tile >= n_tiles || l < 0 || l >= s.L || row0 < 0 || row0 >= s.M) return;
+  const int p0 = row0 + part * kShrinkRows;
+  const int end = pv.offsets[l + 1];
   const int cols = s.slices * s.r, c0 = blockIdx.y * kShrinkCols;
   const uint16_t *x[2], *a[2];
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    x[q] = args.a + int64_t(plan_row(pv, min(p0 + 16 * q + ln, p1 - 1), s.M)) * s.ld_a;
+    x[q] = args.a + int64_t(plan_row(pv, p0 + 16 * q + ln, s.M)) * s.ld_a;
     a[q] = args.lora_a + (int64_t(l) * cols + min(c0 + 16 * q + ln, cols - 1)) * s.K;
   }
+  const int p1 = min(min(end, s.M), row0 + MOEQ_TILE_M);
+  if (p0 >= p1) return;
   v4f acc[2][2];
 #pragma unroll
   for (int i = 0; i < 4; ++i) acc[i >> 1][i & 1] = v4f{0.f, 0.f, 0.f, 0.f};
@@ -93,10 +95,11 @@ lora_shrink_kernel(LoraArgs args, LoraShape s, float* __restrict__ u) {
 #pragma unroll
     for (int j = 0; j < kShrinkSteps; ++j)
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        xv[q][j] = load_in(x[q], c + 32 * j + 8 * kq, s.K);
-        av[q][j] = load_in(a[q], c + 32 * j + 8 * kq, s.K);
-      }
+      for (int q = 0; q < 2; ++q) av[q][j] = load_in(a[q], c + 32 * j + 8 * kq, s.K);
+#pragma unroll
+    for (int j = 0; j < kShrinkSteps; ++j)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) xv[q][j] = load_in(x[q], c + 32 * j + 8 * kq, s.K);
     __builtin_amdgcn_sched_barrier(0);                   // all of them in flight
 #pragma unroll
     for (int j = 0; j < kShrinkSteps; ++j) {

@@ -372,29 +372,36 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, const float* __restrict__ u, int u_
 
   if (slots > 0) {
 #pragma unroll
-    for (int unit = 0; unit < T::kUnits; ++unit)
+    for (int unit = 0; unit + 1 < T::kUnits; ++unit)
 #pragma unroll
       for (int g = 0; g < kL; ++g) issue(unit & 1, g, unit);
-    wait_vmem<(T::kUnits - 2) * kL>();
+    wait_vmem<(T::kUnits - 3) * kL>();
     ring_barrier();
     int px = 0, pw = 1;                                  // ring places of the slot's units
     read_w(lds + T::kUnitB, 0);
 #pragma unroll
     for (int i = 0; i < kM; ++i) read_x(i, lds, 0);
-    const auto first_half = [&] {
+    // unit `unit`'s loads, spread over the rows from `first` on
+    const auto issue_row = [&](int i, int first, int unit, bool is_w) {
+      const int rows = kM - first, per = (kL + rows - 1) / rows;
+#pragma unroll
+      for (int j = 0; j < kL; ++j)
+        if (i >= first && j / per == i - first) issue(is_w, j, unit);
+    };
+    const auto first_half = [&](int st) {
       read_w(lds + pw * T::kUnitB, 1);
 #pragma unroll
       for (int i = 0; i < kM; ++i) {
         multiply(i, 0);
         read_x(i, lds + px * T::kUnitB, 1);
+        issue_row(i, 0, 2 * st + T::kUnits - 1, !(T::kUnits & 1));
         __builtin_amdgcn_sched_barrier(0);
       }
     };
     for (int st = 0; st + 1 < slots; ++st) {
-      first_half();
+      first_half(st);
       px = px + 2 >= T::kUnits ? px + 2 - T::kUnits : px + 2;
       pw = pw + 2 >= T::kUnits ? pw + 2 - T::kUnits : pw + 2;
-      const int unit = 2 * st + T::kUnits;
 #pragma unroll
       for (int i = 0; i < kM; ++i) {
         if (i == kOpen) {
@@ -407,15 +414,12 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, const float* __restrict__ u, int u_
         multiply(i, 1);
         if (i >= kOpen) {
           read_x(i, lds + px * T::kUnitB, 0);
-          constexpr int kPer = (2 * kL + kM - kOpen - 1) / (kM - kOpen);
-#pragma unroll
-          for (int j = kPer * (i - kOpen); j < kPer * (i - kOpen + 1); ++j)
-            if (j < 2 * kL) issue((T::kUnits + j / kL) & 1, j % kL, unit + j / kL);
+          issue_row(i, kOpen, 2 * st + T::kUnits, T::kUnits & 1);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-    first_half();
+    first_half(slots - 1);
 #pragma unroll
     for (int i = 0; i < kM; ++i) multiply(i, 1);
     wait_vmem<0>();                                      // the loads past the last slot

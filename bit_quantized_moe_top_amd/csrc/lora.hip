@@ -62,23 +62,30 @@ __device__ __forceinline__ int plan_row(const PlanView& pv, int p, int M) {
 constexpr int kShrinkRows = 32, kShrinkCols = 32;
 constexpr int kShrinkPiece = 128, kShrinkSteps = kShrinkPiece / 32;
 
-__global__ void __launch_bounds__(256)
-lora_shrink_kernel(LoraArgs args, LoraShape s, float* __restrict__ u) {
-  __shared__ v4f red[4][4][kWave];
+// Workgroups of one launch: (plan tile and its 32-row part, 32 columns, split of K)
+struct ShrinkGrid {
+  int parts, cols, splits;
+  __host__ __device__ int blocks() const { return parts * cols * splits; }
+};
+
+// workgroup b of the grid; red: 16 KB of LDS
+__device__ __forceinline__ void shrink(const LoraArgs& args, const LoraShape& s, float* u,
+                                       const ShrinkGrid& grid, int b, v4f (*red)[4][kWave]) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int ln = lane & 15, kq = lane >> 4;
   const PlanView pv = plan_view(args.plan, s.L + 1, s.M);
-  // blockIdx.x: plan tile and its 32-row part; blockIdx.y: 32 columns of u; blockIdx.z: split of K
+  const int split = b / (grid.parts * grid.cols), at = b - split * grid.parts * grid.cols;
+  const int cblock = at / grid.parts, piece = at - cblock * grid.parts;
   constexpr int kParts = MOEQ_TILE_M / kShrinkRows;
-  const int tile = blockIdx.x / kParts, part = blockIdx.x % kParts;
+  const int tile = piece / kParts, part = piece % kParts;
   // (the plan's words in as few dependent loads as they take: adapter and first row of the tile, then
   // the end of the adapter's rows and the rows' places, then the rows)
   const int n_tiles = pv.base[kPlanTiles], l = pv.tile_expert[tile], row0 = pv.tile_row0[tile];
   if (tile >= n_tiles || l < 0 || l >= s.L || row0 < 0 || row0 >= s.M) return;
   const int p0 = row0 + part * kShrinkRows;
   const int end = pv.offsets[l + 1];
-  const int cols = s.slices * s.r, c0 = blockIdx.y * kShrinkCols;
+  const int cols = s.slices * s.r, c0 = cblock * kShrinkCols;
   const uint16_t *x[2], *a[2];
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
@@ -90,7 +97,7 @@ lora_shrink_kernel(LoraArgs args, LoraShape s, float* __restrict__ u) {
   v4f acc[2][2];
 #pragma unroll
   for (int i = 0; i < 4; ++i) acc[i >> 1][i & 1] = v4f{0.f, 0.f, 0.f, 0.f};
-  for (int c = (4 * blockIdx.z + wave) * kShrinkPiece; c < s.K; c += 4 * gridDim.z * kShrinkPiece) {
+  for (int c = (4 * split + wave) * kShrinkPiece; c < s.K; c += 4 * grid.splits * kShrinkPiece) {
     uint4 xv[2][kShrinkSteps], av[2][kShrinkSteps];
 #pragma unroll
     for (int j = 0; j < kShrinkSteps; ++j)
@@ -116,12 +123,18 @@ lora_shrink_kernel(LoraArgs args, LoraShape s, float* __restrict__ u) {
   const v4f sum = (red[0][wave][lane] + red[1][wave][lane]) + (red[2][wave][lane] + red[3][wave][lane]);
   const int col = c0 + 16 * (wave & 1) + ln;
   const float scale = args.scale[l];
-  u += int64_t(blockIdx.z) * s.M * cols;
+  u += int64_t(split) * s.M * cols;
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
     const int p = p0 + 16 * (wave >> 1) + 4 * kq + v;
     if (p < p1 && col < cols) u[int64_t(p) * cols + col] = sum[v] * scale;
   }
+}
+
+__global__ void __launch_bounds__(256)
+lora_shrink_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, ShrinkGrid grid) {
+  __shared__ v4f red[4][4][kWave];
+  shrink(args, s, u, grid, blockIdx.x, red);
 }
 
 // ------------------------------------------------------- the adapters' part
@@ -202,6 +215,7 @@ __device__ __forceinline__ void add_adapters(v4f (&acc)[T::kM][T::kN], const Pla
                                              int u_splits, uint8_t* lds, int m0, int p0,
                                              const int (&wrow)[T::kN], int lane) {
   constexpr int kM = T::kM, kN = T::kN;
+  constexpr int kAtOnce = T::kRows == 128 ? 1 : 8 / kN;  // (what the registers hold)
   const int ln = lane & 15, kq = lane >> 4;
   const int pend = min(p0 + 16 * kM, s.M);
   // the adapters of the wave's rows: the first, and the offsets of 64 groups from there
@@ -231,17 +245,30 @@ __device__ __forceinline__ void add_adapters(v4f (&acc)[T::kM][T::kN], const Pla
     const int kc = s.r - k0 > 32 ? 64 : 32;              // ranks in LDS, zeros past r
     const int plane = 2 * kc, row_bytes = s.slices * 2 * plane + 16;
     const bool two = kc == 64;
-    uint4 b[2][kN];
+    // kAtOnce adapters' B at a time
+    int id[kAtOnce], from[kAtOnce], to[kAtOnce];
+    uint4 b[kAtOnce][2][kN];
     const auto load_b = [&](int l) {
 #pragma unroll
-      for (int q = 0; q < kN; ++q) {
-        const uint16_t* at = args.lora_b + (int64_t(l) * s.N + wrow[q] + ln) * s.r;
-        b[0][q] = load_in(at, k0 + 8 * kq, s.r);
-        b[1][q] = load_in(at, k0 + 32 + 8 * kq, s.r);
+      for (int a = 0; a < kAtOnce; ++a) {
+        l = next_adapter(l);
+        id[a] = l;
+        from[a] = lo;
+        to[a] = hi;
+        l = min(l + 1, s.L);
+      }
+#pragma unroll
+      for (int a = 0; a < kAtOnce; ++a) {
+        if (id[a] >= s.L) break;
+#pragma unroll
+        for (int q = 0; q < kN; ++q) {
+          const uint16_t* at = args.lora_b + (int64_t(id[a]) * s.N + wrow[q] + ln) * s.r;
+          b[a][0][q] = load_in(at, k0 + 8 * kq, s.r);
+          b[a][1][q] = load_in(at, k0 + 32 + 8 * kq, s.r);
+        }
       }
     };
-    int l = next_adapter(first);
-    if (l < s.L) load_b(l);
+    load_b(first);
     if (k0 > 0) __syncthreads();                         // the ranks before are done with
     const int rows = min(T::kWM * T::kRows, s.M - m0), quads = kc / 4;
     for (int i = threadIdx.x; i < rows * s.slices * quads; i += T::kThreads) {
@@ -263,46 +290,55 @@ __device__ __forceinline__ void add_adapters(v4f (&acc)[T::kM][T::kN], const Pla
       *reinterpret_cast<uint2*>(to + plane) = make_uint2(o[0] | uint32_t(o[1]) << 16, o[2] | uint32_t(o[3]) << 16);
     }
     __syncthreads();
-    while (l < s.L) {
-      const int from = lo, to = hi;
+    while (id[0] < s.L) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int a = 0; a < kAtOnce; ++a) {
+        if (id[a] >= s.L) break;
 #pragma unroll
-        for (int q = 0; q < kN; ++q) b[j][q] = keep(b[j][q], k0 + 32 * j + 8 * kq < s.r);
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int i = 0; i < kM; ++i) {
-        const int pi = p0 + 16 * i;
-        if (pi < to && pi + 16 > from) {
-          bool mine[4];
+          for (int q = 0; q < kN; ++q) b[a][j][q] = keep(b[a][j][q], k0 + 32 * j + 8 * kq < s.r);
 #pragma unroll
-          for (int v = 0; v < 4; ++v) mine[v] = pi + 4 * kq + v >= from && pi + 4 * kq + v < to;
-          const uint8_t* at = lds + (pi - m0 + ln) * row_bytes + 16 * kq;
+        for (int i = 0; i < kM; ++i) {
+          const int pi = p0 + 16 * i;
+          if (pi < to[a] && pi + 16 > from[a]) {
+            bool mine[4];
 #pragma unroll
-          for (int q = 0; q < kN; ++q) {
-            const int slice = s.slices == 2 && wrow[q] >= s.N / 2 ? 2 * plane : 0;
-            v4f d = v4f{0.f, 0.f, 0.f, 0.f};
-            d = mfma(*reinterpret_cast<const uint4*>(at + slice), b[0][q], d);
-            d = mfma(*reinterpret_cast<const uint4*>(at + slice + plane), b[0][q], d);
-            if (two) {
-              d = mfma(*reinterpret_cast<const uint4*>(at + slice + 64), b[1][q], d);
-              d = mfma(*reinterpret_cast<const uint4*>(at + slice + plane + 64), b[1][q], d);
+            for (int v = 0; v < 4; ++v) mine[v] = pi + 4 * kq + v >= from[a] && pi + 4 * kq + v < to[a];
+            const uint8_t* at = lds + (pi - m0 + ln) * row_bytes + 16 * kq;
+#pragma unroll
+            for (int q = 0; q < kN; ++q) {
+              const int slice = s.slices == 2 && wrow[q] >= s.N / 2 ? 2 * plane : 0;
+              v4f d = v4f{0.f, 0.f, 0.f, 0.f};
+              d = mfma(*reinterpret_cast<const uint4*>(at + slice), b[a][0][q], d);
+              d = mfma(*reinterpret_cast<const uint4*>(at + slice + plane), b[a][0][q], d);
+              if (two) {
+                d = mfma(*reinterpret_cast<const uint4*>(at + slice + 64), b[a][1][q], d);
+                d = mfma(*reinterpret_cast<const uint4*>(at + slice + plane + 64), b[a][1][q], d);
+              }
+#pragma unroll
+              for (int v = 0; v < 4; ++v) acc[i][q][v] += mine[v] ? d[v] : 0.0f;
             }
-#pragma unroll
-            for (int v = 0; v < 4; ++v) acc[i][q][v] += mine[v] ? d[v] : 0.0f;
           }
+          __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_barrier(0);
       }
-      l = next_adapter(l + 1);
-      if (l < s.L) load_b(l);
+      load_b(min(id[kAtOnce - 1] + 1, s.L));
     }
   }
 }
 
-template <int EPI, int B>
+// What a launch of the tile kernel does: the whole projection; a split of K of the product, to parts
+// (with the shrink); or the join of the parts, the adapters and the epilogue.
+enum TileMode { kWhole, kParts, kJoin };
+constexpr int kMaxSplits = 4;
+
+template <int EPI, int B, TileMode MODE>
 __global__ void __launch_bounds__(Tile<B>::kThreads, 2)
-lora_gemm_kernel(LoraArgs args, LoraShape s, const float* __restrict__ u, int u_splits) {
+lora_gemm_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restrict__ parts, int splits,
+                 ShrinkGrid sgrid) {
   using T = Tile<B>;
+  static_assert(MODE != kParts || EPI == MOEQ_EPI_NONE, "parts are of W's own columns");
   constexpr int kM = T::kM, kN = T::kN, kL = T::kLoads;  // kM x kN blocks of 16 x 16 per wave
   constexpr bool kSilu = EPI == MOEQ_EPI_SILU_MUL;
   extern __shared__ __align__(16) uint8_t lds[];
@@ -315,9 +351,22 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, const float* __restrict__ u, int u_
   constexpr int kOut = kSilu ? B / 2 : B;                // output columns per workgroup
   // Workgroups go round the XCDs: each takes a run of tiles, all row tiles of a column tile before
   // the next one, so that an XCD's tiles share their w rows in its L2.
-  const int mtiles = (s.M + B - 1) / B, tiles = gridDim.x;
-  const int xcd = blockIdx.x & 7;
-  const int tile = xcd * (tiles >> 3) + min(xcd, tiles & 7) + int(blockIdx.x >> 3);
+  int block = blockIdx.x, blocks = gridDim.x;
+  if constexpr (MODE == kParts) {
+    // (the shrink's workgroups last: ahead of the product's they kept half of those waiting for LDS)
+    blocks -= sgrid.blocks();
+    if (block >= blocks) {
+      shrink(args, s, u, sgrid, block - blocks, reinterpret_cast<v4f (*)[4][kWave]>(lds));
+      return;
+    }
+  }
+  const int mtiles = (s.M + B - 1) / B;
+  const int xcd = block & 7;
+  int tile = xcd * (blocks >> 3) + min(xcd, blocks & 7) + (block >> 3), split = 0;
+  if constexpr (MODE == kParts) {                        // the splits of a tile follow each other
+    split = tile % splits;
+    tile /= splits;
+  }
   const int nt = tile / mtiles, mt = tile - nt * mtiles;
   const int m0 = mt * B, n0 = nt * kOut;
 
@@ -342,10 +391,14 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, const float* __restrict__ u, int u_
     wsrc[g] = args.w + int64_t(w_row(row)) * s.K + c;
   }
   const uint32_t lds0 = lds_offset(lds) + 8 * kL * wave * kRowB;
-  const int slots = s.K / kSlotK;
+  // this launch's slots of 64 K: first, number
+  const int all_slots = s.K / kSlotK;
+  const int s0 = MODE == kParts ? int(int64_t(all_slots) * split / splits) : 0;
+  const int slots = MODE == kParts ? int(int64_t(all_slots) * (split + 1) / splits) - s0
+                                   : MODE == kJoin ? 0 : all_slots;
   // load g of unit `unit` (2 st: x, 2 st + 1: w of slot st); past the last slot, the last again
   const auto issue = [&](bool is_w, int g, int unit) {
-    const int k = min(unit >> 1, slots - 1) * kSlotK;
+    const int k = (s0 + min(unit >> 1, slots - 1)) * kSlotK;
     load_lds<false>((is_w ? wsrc[g] : xsrc[g]) + k,
                     lds0 + uint32_t(unit % T::kUnits) * T::kUnitB + 8 * g * kRowB);
   };
@@ -424,9 +477,9 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, const float* __restrict__ u, int u_
     for (int i = 0; i < kM; ++i) multiply(i, 1);
     wait_vmem<0>();                                      // the loads past the last slot
   }
-  if (s.K > slots * kSlotK) {                            // K past whole slots, zeros after it
-    ring_barrier();
-    const int k0 = slots * kSlotK;
+  if (MODE != kJoin && s.K > all_slots * kSlotK && (MODE == kWhole || split == splits - 1)) {
+    ring_barrier();                                      // K past whole slots, zeros after it
+    const int k0 = all_slots * kSlotK;
     for (int i = tid; i < 2 * B * 8; i += T::kThreads) {
       const int row = i >> 3, c = i & 7;
       const uint16_t* src = row < B ? args.a + int64_t(plan_row(pv, m0 + row, s.M)) * s.ld_a
@@ -454,8 +507,38 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, const float* __restrict__ u, int u_
     wrow[q] = min(ocol[q], cols - 16) + (up ? cols : 0);
   }
   const int p0 = m0 + T::kRows * wm;
+  if constexpr (MODE != kWhole) {                        // blocks [split][16 rows][16 w rows][lane]
+    const int mblocks = (s.M + 15) / 16, nb = s.N / 16;
+    const int64_t stride = int64_t(mblocks) * nb * kWave;
+    const auto part = [&](int i, int q) {
+      return parts + (int64_t(min(p0 / 16 + i, mblocks - 1)) * nb + wrow[q] / 16) * kWave + lane;
+    };
+    if constexpr (MODE == kParts) {
+#pragma unroll
+      for (int i = 0; i < kM; ++i)
+#pragma unroll
+        for (int q = 0; q < kN; ++q)
+          if (p0 / 16 + i < mblocks && ocol[q] < cols) part(i, q)[split * stride] = acc[i][q];
+    } else {
+      v4f v[kMaxSplits][kM][kN];                         // all loads at once
+#pragma unroll
+      for (int j = 0; j < kMaxSplits; ++j)
+#pragma unroll
+        for (int i = 0; i < kM; ++i)
+#pragma unroll
+          for (int q = 0; q < kN; ++q) v[j][i][q] = part(i, q)[min(j, splits - 1) * stride];
+#pragma unroll
+      for (int j = 0; j < kMaxSplits; ++j)
+#pragma unroll
+        for (int i = 0; i < kM; ++i)
+#pragma unroll
+          for (int q = 0; q < kN; ++q)
+            if (j < splits) acc[i][q] = acc[i][q] + v[j][i][q];
+    }
+    if constexpr (MODE == kParts) return;
+  }
   ring_barrier();                                        // the ring's LDS is free
-  add_adapters<T>(acc, pv, args, s, u, u_splits, lds, m0, p0, wrow, lane);
+  add_adapters<T>(acc, pv, args, s, u, sgrid.splits, lds, m0, p0, wrow, lane);
 #pragma unroll
   for (int i = 0; i < kM; ++i) {
     // (four rows at a time: the rows' places hoisted together would take the accumulators' registers)
@@ -488,13 +571,30 @@ constexpr int kFewRows = 64, kFewCols = 64;
 // are more than 16)
 constexpr int kUPiece = 512, kUSteps = kUPiece / 32, kUSplits = 16;
 
-// the plan's tiles by lane (at most 64 of up to 64 rows), and the tile of a sorted row
+// the plan's tiles by lane: all of them (at most 64 of up to 64 rows), or those from sorted row p0's on
 struct FewPlan {
   int n, row0, expert;
   __device__ __forceinline__ FewPlan(const PlanView& pv, int lane) {
     n = min(min(pv.base[kPlanTiles], pv.max_tiles), kWave);
     row0 = pv.tile_row0[min(lane, pv.max_tiles - 1)];
     expert = pv.tile_expert[min(lane, pv.max_tiles - 1)];
+  }
+  __device__ __forceinline__ FewPlan(const PlanView& pv, int p0, int lane) {
+    const int tiles = min(pv.base[kPlanTiles], pv.max_tiles);
+    constexpr int kAhead = 5;                            // the tiles of 256 rows at once
+    int before = 0;                                      // tiles that begin at or before p0
+    for (int t0 = 0; t0 < tiles; t0 += kAhead * kWave) {
+      int first[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) first[i] = pv.tile_row0[min(t0 + i * kWave + lane, pv.max_tiles - 1)];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        before += __popcll(__ballot(t0 + i * kWave + lane < tiles && first[i] <= p0));
+    }
+    const int t = max(before - 1, 0);
+    n = min(tiles - t, kWave);
+    row0 = pv.tile_row0[min(t + lane, pv.max_tiles - 1)];
+    expert = pv.tile_expert[min(t + lane, pv.max_tiles - 1)];
   }
   // adapter of sorted row p0 + lane, lane < 16 (the tile that holds it; -1: none)
   __device__ __forceinline__ int adapter16(int p0, int lane) const {
@@ -674,10 +774,10 @@ lora_few_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restri
     if (i < mblocks) parts[((int64_t(split) * mblocks + i) * nb + n0 / 16) * kWave + lane] = acc[i];
 }
 
-// at[0] + at[stride] + ... (n of them, in this order), eight loads at a time; the first eight go out
-// in load(), well ahead of sum()
+// at[0] + at[stride] + ... (n of them, in this order), kAhead loads at a time; the first ones go out in
+// load(), well ahead of sum()
+template <int kAhead>
 struct PartSum {
-  static constexpr int kAhead = 8;
   v4f v[kAhead];
   __device__ __forceinline__ void load(const v4f* at, int64_t stride, int i0, int n) {
 #pragma unroll
@@ -710,8 +810,8 @@ __host__ __device__ inline int join_u_row(int slices, int r) { return slices * (
 // is loaded at once, B as soon as the rows' adapters are known, and the adapters, up to 16, are
 // dealt over the four waves, so that none loads twice (four columns' worth per workgroup and all
 // adapters in each wave: 9.3 us instead of JOIN16 for 16 rows x 8192).
-template <int EPI>
-__global__ void __launch_bounds__(256, 2)
+template <int EPI, bool kFew>
+__global__ void __launch_bounds__(256, kFew ? 2 : 3)
 lora_join_kernel(LoraArgs args, LoraShape s, const float* __restrict__ u,
                  const v4f* __restrict__ parts, int splits, int u_splits) {
   extern __shared__ __align__(16) uint8_t us[];          // u: [16 rows][slice][hi, lo][r to 32]
@@ -725,11 +825,11 @@ lora_join_kernel(LoraArgs args, LoraShape s, const float* __restrict__ u,
   const int cblocks = cols / 16, mblocks = (s.M + 15) / 16, nb = s.N / 16;
   const int mb = blockIdx.y, cb = blockIdx.x;
   const PlanView pv = plan_view(args.plan, s.L + 1, s.M);
-  const FewPlan fp(pv, lane);
+  const FewPlan fp = kFew ? FewPlan(pv, lane) : FewPlan(pv, 16 * mb, lane);
   const int rows = min(16, s.M - 16 * mb);
   const int64_t part_stride = int64_t(mblocks) * nb * kWave, u_stride = int64_t(s.M) * s.slices * s.r / 4;
   const v4f* pat[kHalves];
-  PartSum ps[kHalves], pu;
+  PartSum<kFew ? 8 : kMaxSplits> ps[kHalves], pu;        // (more than 64 rows: 4 splits at most)
 #pragma unroll
   for (int h = 0; h < kHalves; ++h) {
     pat[h] = parts + (int64_t(mb) * nb + cb + h * cblocks) * kWave + lane;
@@ -884,6 +984,17 @@ size_t few_part_bytes(const LoraShape& s) {
   return size_t(few_split(s).splits) * ((s.M + 15) / 16 * 16) * s.N * sizeof(float);
 }
 
+template <bool kFew>
+hipError_t launch_join(const LoraArgs& args, const LoraShape& s, const float* u, const v4f* parts, int splits,
+                       int u_splits, hipStream_t stream) {
+  const bool silu = s.epilogue == MOEQ_EPI_SILU_MUL;
+  const int cblocks = (silu ? s.N / 2 : s.N) / 16;
+  const auto join = silu ? lora_join_kernel<MOEQ_EPI_SILU_MUL, kFew> : lora_join_kernel<MOEQ_EPI_NONE, kFew>;
+  hipLaunchKernelGGL(join, dim3(unsigned(cblocks), unsigned((s.M + 15) / 16)), dim3(256),
+                     unsigned(16 * join_u_row(s.slices, s.r)), stream, args, s, u, parts, splits, u_splits);
+  return hipGetLastError();
+}
+
 template <int MB>
 hipError_t launch_few(const LoraArgs& args, const LoraShape& s, hipStream_t stream) {
   const FewSplit fs = few_split(s);
@@ -894,51 +1005,73 @@ hipError_t launch_few(const LoraArgs& args, const LoraShape& s, hipStream_t stre
   const int u_cols = (s.slices * s.r + 15) / 16, items = row_pieces * u_cols * fs.u_splits;
   const int ntiles = (s.N + kFewCols - 1) / kFewCols;
   const unsigned lds = few_ring<MB>() * few_slot_bytes<MB>();
-  hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void*>(&lora_few_kernel<MB>),
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, int(lds));
-  if (err != hipSuccess) return err;
+  static_assert(few_ring<MB>() * few_slot_bytes<MB>() <= 64 * 1024, "no attribute needed");
   hipLaunchKernelGGL(lora_few_kernel<MB>, dim3(unsigned((items + 3) / 4 + ntiles * fs.splits)), dim3(256),
                      lds, stream, args, s, u, parts, items, u_cols, fs.u_splits, fs.u_pieces, fs.slots);
-  if ((err = hipGetLastError()) != hipSuccess) return err;
-  const bool silu = s.epilogue == MOEQ_EPI_SILU_MUL;
-  const int cblocks = (silu ? s.N / 2 : s.N) / 16;
-  const auto join = silu ? lora_join_kernel<MOEQ_EPI_SILU_MUL> : lora_join_kernel<MOEQ_EPI_NONE>;
-  hipLaunchKernelGGL(join, dim3(unsigned(cblocks), unsigned((s.M + 15) / 16)), dim3(256),
-                     unsigned(16 * join_u_row(s.slices, s.r)), stream, args, s, u, parts, fs.splits,
-                     fs.u_splits);
-  return hipGetLastError();
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  return launch_join<true>(args, s, u, parts, fs.splits, fs.u_splits, stream);
 }
 
-// splits of K of the parts of u, at most 4 (add_adapters): for up to 4096 rows, whose blocks of 32
-// alone would leave CUs idle
-int shrink_splits(const LoraShape& s) {
+// The grid of the shrink.  Splits of K, at most 4 (add_adapters): for up to 4096 rows, whose blocks
+// of 32 alone would leave CUs idle.
+ShrinkGrid shrink_grid(const LoraShape& s) {
   const int pieces = (s.K + 4 * kShrinkPiece - 1) / (4 * kShrinkPiece);
-  return s.M > 4096 ? 1 : pieces < 4 ? pieces : 4;
+  return {plan_max_tiles(s.L + 1, s.M) * (MOEQ_TILE_M / kShrinkRows),
+          (s.slices * s.r + kShrinkCols - 1) / kShrinkCols, s.M > 4096 ? 1 : pieces < 4 ? pieces : 4};
 }
 
-constexpr int64_t kEnoughTiles = 200;
 int64_t tiles_of(const LoraShape& s, int b) {
   return int64_t((s.M + b - 1) / b) * ((s.N + b - 1) / b);
 }
 
-template <int B>
-hipError_t launch_tiles(const LoraArgs& args, const LoraShape& s, const float* u, int u_splits,
-                        hipStream_t stream) {
-  const bool silu = s.epilogue == MOEQ_EPI_SILU_MUL;
-  const auto fn = silu ? lora_gemm_kernel<MOEQ_EPI_SILU_MUL, B> : lora_gemm_kernel<MOEQ_EPI_NONE, B>;
+constexpr int kJoinBlocks = 1700;
+
+// How more than 64 rows are multiplied: tiles of `tile` rows and columns, K split in `splits` (1:
+// whole tiles, the shrink ahead of them)
+struct TilePlan {
+  int tile, splits;
+};
+TilePlan tile_plan(const LoraShape& s) {
+  const int64_t t256 = tiles_of(s, 256), t128 = tiles_of(s, 128), t64 = tiles_of(s, 64);
+  if (t256 >= 150) return {256, 1};
+  if (t128 >= 350) return {128, 1};
+  if (t64 >= 200 && s.K <= 2048) return {64, 1};
+  if (t128 >= 64) return {128, t128 >= 128 ? 2 : 4};
+  return {64, t64 >= 100 ? 2 : 4};
+}
+size_t tile_u_bytes(const LoraShape& s) {
+  return align256(size_t(shrink_grid(s).splits) * s.M * s.slices * s.r * sizeof(float));
+}
+
+template <int EPI, int B, TileMode MODE>
+hipError_t launch_tile_kernel(const LoraArgs& args, const LoraShape& s, float* u, v4f* parts, int splits,
+                              hipStream_t stream) {
+  const auto fn = lora_gemm_kernel<EPI, B, MODE>;
   const hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void*>(fn),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, Tile<B>::kLds);
   if (err != hipSuccess) return err;
-  hipLaunchKernelGGL(fn, dim3(unsigned(tiles_of(s, B))), dim3(Tile<B>::kThreads), Tile<B>::kLds, stream, args, s, u,
-                     u_splits);
+  const ShrinkGrid sgrid = shrink_grid(s);
+  const int64_t blocks = MODE == kParts ? sgrid.blocks() + tiles_of(s, B) * splits : tiles_of(s, B);
+  hipLaunchKernelGGL(fn, dim3(unsigned(blocks)), dim3(Tile<B>::kThreads), Tile<B>::kLds, stream, args, s, u,
+                     parts, splits, sgrid);
   return hipGetLastError();
+}
+template <int B, TileMode MODE>
+hipError_t launch_tiles(const LoraArgs& args, const LoraShape& s, float* u, v4f* parts, int splits,
+                        hipStream_t stream) {
+  return s.epilogue == MOEQ_EPI_SILU_MUL
+             ? launch_tile_kernel<MOEQ_EPI_SILU_MUL, B, MODE>(args, s, u, parts, splits, stream)
+             : launch_tile_kernel<MOEQ_EPI_NONE, B, MODE>(args, s, u, parts, splits, stream);
 }
 
 }  // namespace
 
 size_t lora_ws_bytes(const LoraShape& s) {
   if (s.M <= kFewRows) return few_u_bytes(s) + align256(few_part_bytes(s)) + 256;
-  return align256(size_t(shrink_splits(s)) * s.M * s.slices * s.r * sizeof(float));
+  const TilePlan tp = tile_plan(s);
+  const size_t parts = tp.splits > 1 ? size_t(tp.splits) * ((s.M + 15) / 16 * 16) * s.N * sizeof(float) : 0;
+  return tile_u_bytes(s) + align256(parts);
 }
 
 hipError_t launch_shared_gemm_lora(const LoraArgs& args, const LoraShape& s, hipStream_t stream) {
@@ -947,15 +1080,24 @@ hipError_t launch_shared_gemm_lora(const LoraArgs& args, const LoraShape& s, hip
   if (s.M <= 32) return launch_few<2>(args, s, stream);
   if (s.M <= kFewRows) return launch_few<4>(args, s, stream);
   float* u = static_cast<float*>(args.ws);
-  const int splits = shrink_splits(s);
-  const dim3 sgrid(unsigned(plan_max_tiles(s.L + 1, s.M)) * (MOEQ_TILE_M / kShrinkRows),
-                   unsigned((s.slices * s.r + kShrinkCols - 1) / kShrinkCols), unsigned(splits));
-  hipLaunchKernelGGL(lora_shrink_kernel, sgrid, dim3(256), 0, stream, args, s, u);
-  hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return err;
-  if (tiles_of(s, 256) >= kEnoughTiles) return launch_tiles<256>(args, s, u, splits, stream);
-  if (tiles_of(s, 128) >= kEnoughTiles) return launch_tiles<128>(args, s, u, splits, stream);
-  return launch_tiles<64>(args, s, u, splits, stream);
+  v4f* parts = reinterpret_cast<v4f*>(static_cast<uint8_t*>(args.ws) + tile_u_bytes(s));
+  const TilePlan tp = tile_plan(s);
+  hipError_t err;
+  if (tp.splits > 1) {
+    err = tp.tile == 128 ? launch_tile_kernel<MOEQ_EPI_NONE, 128, kParts>(args, s, u, parts, tp.splits, stream)
+                         : launch_tile_kernel<MOEQ_EPI_NONE, 64, kParts>(args, s, u, parts, tp.splits, stream);
+    if (err != hipSuccess) return err;
+    const int64_t join_blocks = int64_t((s.M + 15) / 16) * ((s.epilogue == MOEQ_EPI_SILU_MUL ? s.N / 2 : s.N) / 16);
+    return join_blocks <= kJoinBlocks ? launch_join<false>(args, s, u, parts, tp.splits, shrink_grid(s).splits, stream)
+                            : launch_tiles<64, kJoin>(args, s, u, parts, tp.splits, stream);
+  }
+  const ShrinkGrid sgrid = shrink_grid(s);
+  hipLaunchKernelGGL(lora_shrink_kernel, dim3(unsigned(sgrid.blocks())), dim3(256), 0, stream, args, s, u,
+                     sgrid);
+  if ((err = hipGetLastError()) != hipSuccess) return err;
+  if (tp.tile == 256) return launch_tiles<256, kWhole>(args, s, u, parts, 1, stream);
+  if (tp.tile == 128) return launch_tiles<128, kWhole>(args, s, u, parts, 1, stream);
+  return launch_tiles<64, kWhole>(args, s, u, parts, 1, stream);
 }
 
 }  // namespace moeq

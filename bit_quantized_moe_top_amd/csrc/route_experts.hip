@@ -152,10 +152,114 @@ struct WideChoice {
   }
 };
 
+// NS values of consecutive experts; `whole`: NS of them, 4-element aligned (bf16: 8 bytes)
+template <int NS>
+__device__ __forceinline__ void load_slots(const float* p, int n, bool whole, float (&v)[NS]) {
+  if (NS >= 4 && whole) {
+#pragma unroll
+    for (int j = 0; j < NS / 4; ++j) {
+      const float4 f = reinterpret_cast<const float4*>(p)[j];
+      v[4 * j] = f.x; v[4 * j + 1 < NS ? 4 * j + 1 : 0] = f.y;
+      v[4 * j + 2 < NS ? 4 * j + 2 : 0] = f.z; v[4 * j + 3 < NS ? 4 * j + 3 : 0] = f.w;
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < NS; ++j) v[j] = p[min(j, max(n - 1, 0))];
+}
+template <int NS>
+__device__ __forceinline__ void load_slots(const uint16_t* p, int n, bool whole, float (&v)[NS]) {
+  if (NS >= 4 && whole) {
+#pragma unroll
+    for (int j = 0; j < NS / 4; ++j) {
+      const uint2 u = reinterpret_cast<const uint2*>(p)[j];
+      v[4 * j] = u2f(u.x << 16); v[4 * j + 1 < NS ? 4 * j + 1 : 0] = u2f(u.x & 0xFFFF0000u);
+      v[4 * j + 2 < NS ? 4 * j + 2 : 0] = u2f(u.y << 16);
+      v[4 * j + 3 < NS ? 4 * j + 3 : 0] = u2f(u.y & 0xFFFF0000u);
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < NS; ++j) v[j] = bf16_to_f32(p[min(j, max(n - 1, 0))]);
+}
+
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t umin(uint32_t a, uint32_t b) { return a < b ? a : b; }
+__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
+  return uint32_t(wave_reduce(int(v), [](int a, int b) { return int(umax(uint32_t(a), uint32_t(b))); }, 0));
+}
+
+// (b1, b2), b1 >= b2, of two lanes joined
+__device__ __forceinline__ void join2(uint32_t& b1, uint32_t& b2, uint32_t o1, uint32_t o2) {
+  b2 = umax(umin(b1, o1), umax(b2, o2));
+  b1 = umax(b1, o1);
+}
+template <int CTRL>
+__device__ __forceinline__ void join2_dpp(uint32_t& b1, uint32_t& b2) {
+  join2(b1, b2, uint32_t(dpp<CTRL>(0, int(b1))), uint32_t(dpp<CTRL>(0, int(b2))));
+}
+
+// A lane's experts as sorted lists of up to four (best first, the lower slot among equals), so that a
+// round of the selection looks at the heads only and taking one is a shift.  `order` holds a list's
+// slots, a byte each.
+template <int NS>
+struct SortedSlots {
+  static constexpr int kLen = NS < 4 ? NS : 4, kLists = NS / kLen;
+  uint32_t key[kLists][kLen], order[kLists];
+  __device__ __forceinline__ void sort(const uint32_t (&k)[NS]) {
+#pragma unroll
+    for (int i = 0; i < kLists; ++i) {
+#pragma unroll
+      for (int j = 0; j < kLen; ++j) key[i][j] = k[kLen * i + j];
+      order[i] = 0x03020100u;
+      // neighbours exchanged only where the later is larger: equal keys keep their order
+#pragma unroll
+      for (int end = 1; end < kLen; ++end)
+#pragma unroll
+        for (int j = end; j > 0; --j) exchange(i, j - 1);
+    }
+  }
+  // bytes j and j + 1 of `order` change places with the keys
+  __device__ __forceinline__ void exchange(int i, int j) {
+    const bool swap = key[i][j + 1] > key[i][j];
+    const uint32_t a = key[i][j], b = key[i][j + 1];
+    key[i][j] = swap ? b : a;
+    key[i][j + 1] = swap ? a : b;
+    const uint32_t sel = j == 0 ? 0x03020001u : j == 1 ? 0x03010200u : 0x02030100u;
+    const uint32_t moved = __builtin_amdgcn_perm(0u, order[i], sel);
+    order[i] = swap ? moved : order[i];
+  }
+  // the best left: its key, and its slot in `slot`
+  __device__ __forceinline__ uint32_t best(int& slot, int& list) const {
+    uint32_t k = key[0][0], o = order[0];
+    list = 0;
+#pragma unroll
+    for (int i = 1; i < kLists; ++i) {
+      const bool more = key[i][0] > k;
+      k = more ? key[i][0] : k;
+      o = more ? order[i] : o;
+      list = more ? i : list;
+    }
+    slot = kLen * list + int(o & 255u);
+    return k;
+  }
+  // takes the head of `list` (wave-uniform)
+  __device__ __forceinline__ void take(int list) {
+#pragma unroll
+    for (int i = 0; i < kLists; ++i) {
+      if (i != list) continue;
+#pragma unroll
+      for (int j = 0; j + 1 < kLen; ++j) key[i][j] = key[i][j + 1];
+      key[i][kLen - 1] = 0u;
+      order[i] >>= 8;
+    }
+  }
+};
+
 template <typename LT, int NS>
 __global__ void __launch_bounds__(64 * kRouteWaves)
 route_experts_kernel(const LT* __restrict__ logits, const float* __restrict__ bias, RouteShape p,
-                     int C, int width, int32_t* __restrict__ ids, float* __restrict__ w) {
+                     int C, int width, int whole, int32_t* __restrict__ ids, float* __restrict__ w) {
   extern __shared__ __align__(16) uint64_t wide_keys[];      // [waves][NS][64] where needed
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -166,12 +270,9 @@ route_experts_kernel(const LT* __restrict__ logits, const float* __restrict__ bi
   const Lanes ln(p, grouped, C, width, lane);
   const LT* row = logits + int64_t(t) * p.ld;
 
-  // every load issued before the first use, clamped instead of branched around
   float l[NS], c[NS];
-#pragma unroll
-  for (int j = 0; j < NS; ++j) l[j] = load1(row + ln.first + min(j, max(ln.n - 1, 0)));
-#pragma unroll
-  for (int j = 0; j < NS; ++j) c[j] = bias ? bias[ln.first + min(j, max(ln.n - 1, 0))] : 0.0f;
+  load_slots<NS>(row + ln.first, ln.n, whole, l);
+  if (bias) load_slots<NS>(bias + ln.first, ln.n, whole, c);
 #pragma unroll
   for (int j = 0; j < NS; ++j)
     if (j >= ln.n) l[j] = -INFINITY;
@@ -192,18 +293,26 @@ route_experts_kernel(const LT* __restrict__ logits, const float* __restrict__ bi
     }
   }
 
-  // what orders experts (without a bias the logits) and groups
+  // keys that order experts: c, or without a bias the logits (the fp32 scores are then needed for
+  // sums of two in groups only)
   const bool by_logit = bias == nullptr;
   const bool scores = !by_logit || (grouped && p.group_best == 2);
   const float rden = softmax ? 1.0f / den : 1.0f;
   const float smax = softmax ? rden : 0.125f;
+  const uint32_t none = score_key(-INFINITY);
+  uint32_t key[NS];
   if (scores) {
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
       const float s = softmax ? exp_fast(l[j] - top) * rden
                               : __builtin_amdgcn_rcpf(1.0f + exp_fast(-l[j]));
-      c[j] = l[j] == -INFINITY ? -INFINITY : s + c[j];
+      c[j] = l[j] == -INFINITY ? -INFINITY : by_logit ? s : s + c[j];
     }
+  }
+#pragma unroll
+  for (int j = 0; j < NS; ++j) {
+    key[j] = umax(score_key(scores ? c[j] : l[j]), 1u);      // (one NaN has key 0)
+    if (j >= ln.n) key[j] = 0u;
   }
 
   WideChoice<LT> wide{wide_keys + size_t(wave) * NS * kWave, ln, lane};
@@ -211,97 +320,101 @@ route_experts_kernel(const LT* __restrict__ logits, const float* __restrict__ bi
   double w1 = 0.0, w2 = 0.0;
   bool stays = true;
   if (grouped) {
-    float b1 = -INFINITY, b2 = -INFINITY;
+    uint32_t b1 = 0u, b2 = 0u;
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
-      const float v = j < ln.n ? (scores ? c[j] : l[j]) : -INFINITY;
-      b2 = fmaxf(b2, fminf(b1, v));
-      b1 = fmaxf(b1, v);
+      b2 = umax(b2, umin(b1, key[j]));
+      b1 = umax(b1, key[j]);
     }
-    for (int m = 1; m < width; m <<= 1) {
-      const float o1 = __shfl_xor(b1, m), o2 = __shfl_xor(b2, m);
-      b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
-      b1 = fmaxf(b1, o1);
-    }
+    if (width > 1) join2_dpp<kDppQuadSwap1>(b1, b2);
+    if (width > 2) join2_dpp<kDppQuadSwap2>(b1, b2);
+    if (width > 4) join2_dpp<kDppRowHalfMirror>(b1, b2);
+    if (width > 8) join2_dpp<kDppRowMirror>(b1, b2);
+    if (width > 16) join2(b1, b2, uint32_t(__shfl_xor(int(b1), 16)), uint32_t(__shfl_xor(int(b2), 16)));
+    const bool live = b1 > none;
     if (!scores) {                                           // best of the logits: exact
-      const uint32_t key = max(score_key(b1), 1u);
       int above = 0;
       for (int g = 0; g < ln.G; ++g) {
-        const uint32_t other = uint32_t(readlane(int(key), g * width));
-        above += other > key || (other == key && g < ln.g);
+        const uint32_t other = uint32_t(readlane(int(b1), g * width));
+        above += other > b1 || (other == b1 && g < ln.g);
       }
       stays = above < p.topk_group;
     } else {
-      const bool two = p.group_best == 2 && b2 > -INFINITY;
-      const float v = two ? b1 + b2 : b1;
-      const float half = 0x1p-17f * smax + 0x1p-22f * (fabsf(b1) + (two ? fabsf(b2) : 0.0f));
-      const bool live = b1 > -INFINITY;
-      const float lo = live ? v - half : -INFINITY, hi = live ? v + half : -INFINITY;
-      int sure = 0, maybe = 0, empty_below = 0, n_live = 0;
-      for (int g = 0; g < ln.G; ++g) {
-        const float olo = readlane(lo, g * width), ohi = readlane(hi, g * width);
-        const bool olive = ohi > -INFINITY;
-        sure += olo > hi;
-        maybe += ohi >= lo && g != ln.g;
-        n_live += olive;
-        empty_below += !olive && g < ln.g;
-      }
-      stays = live ? maybe < p.topk_group : n_live + empty_below < p.topk_group;
-      const bool open = live && !stays && sure < p.topk_group && ln.g < ln.G;
-      if (__ballot(open)) {
+      // A group stays for sure if at most topk_group - 1 others may be above it.  If as many stay
+      // for sure as are to stay, the choice is made.
+      const bool two = p.group_best == 2 && b2 > none;
+      const float f1 = key_score(b1), f2 = two ? key_score(b2) : 0.0f;
+      const float half = 0x1p-17f * smax + 0x1p-22f * (fabsf(f1) + fabsf(f2));
+      const float lo = f1 + f2 - half;
+      const float hi = live ? f1 + f2 + half : -INFINITY;
+      int maybe = 0;
+      for (int g = 0; g < ln.G; ++g) maybe += readlane(hi, g * width) >= lo ? 1 : 0;   // and itself
+      const uint64_t leads = __ballot(live && ln.g < ln.G && lane == ln.g * width);
+      const int n_live = __popcll(leads);
+      stays = live ? maybe <= p.topk_group
+                   // empty groups: after all the others, the lower first
+                   : n_live + __popcll(__ballot(!live && ln.g < ln.G && lane == ln.g * width) &
+                                       ((uint64_t(1) << (ln.g * width & 63)) - 1)) < p.topk_group;
+      const int sure = __popcll(__ballot(stays) & leads);
+      if (sure < min(p.topk_group, n_live)) {
         wide.fill(row, bias, p.scoring, w1, w2);
         filled = true;
         stays = wide.group_stays(w1, w2, p.group_best, p.topk_group);
       }
     }
   }
+  if (scores && by_logit) {
+#pragma unroll
+    for (int j = 0; j < NS; ++j) key[j] = j < ln.n ? umax(score_key(l[j]), 1u) : 0u;
+  }
+  if (grouped) {
+#pragma unroll
+    for (int j = 0; j < NS; ++j) key[j] = stays ? key[j] : umin(key[j], none);
+  }
 
-  // k rounds of a wave-wide argmax
-  uint32_t key[NS];
-#pragma unroll
-  for (int j = 0; j < NS; ++j) {
-    const float v = stays ? (by_logit ? l[j] : c[j]) : -INFINITY;
-    key[j] = j < ln.n ? max(score_key(v), 1u) : 0u;
-  }
-  int e = 0;
-  uint32_t ekey = 0;
+  // k rounds of a wave-wide argmax over the heads
+  SortedSlots<NS> left;
+  left.sort(key);
+  int e = 0, ekey = 0;
   for (int r = 0; r < p.k; ++r) {
-    uint32_t ck = 0;
-    int cj = 0;
-#pragma unroll
-    for (int j = 0; j < NS; ++j)
-      if (key[j] > ck) { ck = key[j]; cj = j; }
-    const uint32_t kmax = uint32_t(wave_reduce(
-        int(ck), [](int a, int b) { return int(max(uint32_t(a), uint32_t(b))); }, 0));
-    const int from = __ffsll(static_cast<unsigned long long>(__ballot(ck == kmax))) - 1;
-    const int be = readlane(ln.first + cj, from);
-    if (lane == from) {
-#pragma unroll
-      for (int j = 0; j < NS; ++j)
-        if (j == cj) key[j] = 0u;                            // taken
-    }
-    if (lane == r) { e = be; ekey = kmax; }
+    int slot, list;
+    const uint32_t mine = left.best(slot, list);
+    const uint32_t kmax = wave_umax(mine);
+    const int from = __ffsll(static_cast<unsigned long long>(__ballot(mine == kmax))) - 1;
+    const int be = readlane(ln.first + slot, from);
+    const int from_list = SortedSlots<NS>::kLists > 1 ? readlane(list, from) : 0;
+    if (lane == from) left.take(from_list);
+    e = lane == r ? be : e;
+    ekey = lane == r ? int(kmax) : ekey;
   }
-  const uint32_t none = score_key(-INFINITY);
   const bool pick = lane < p.k;
   float el = load1(row + e);
-  bool live = pick && ekey > none;
+  bool live = pick && uint32_t(ekey) > none;
 
   if (!by_logit) {
     // does the fp32 order stand?
-    const float ec = key_score(ekey), eb = bias[e];
+    const float ec = key_score(uint32_t(ekey)), eb = bias[e];
     const float tol = 0x1p-17f * smax + 0x1p-22f * fabsf(ec);
     const float nc = __shfl_down(ec, 1), nl = __shfl_down(el, 1), nb = __shfl_down(eb, 1);
     const bool nlive = __shfl_down(int(live), 1) != 0;
     bool open = live && nlive && lane + 1 < p.k && ec - nc < tol && !(nl == el && nb == eb);
     const int last = p.k - 1;
-    if (__ballot(live && lane == last)) {
-      const float lc = readlane(ec, last), ll = readlane(el, last), lb = readlane(eb, last);
-      const float edge = lc - readlane(tol, last);
+    if (uint32_t(readlane(ekey, last)) > none) {
+      const uint32_t edge = umax(score_key(readlane(ec - tol, last)), none);
+      bool near = false;
 #pragma unroll
-      for (int j = 0; j < NS; ++j)
-        if (key[j] > none && key_score(key[j]) > edge)
-          open |= !(l[j] == ll && bias[ln.first + j] == lb);
+      for (int i = 0; i < SortedSlots<NS>::kLists; ++i) near |= left.key[i][0] > edge;
+      if (__ballot(near)) {                                  // equal to the last pick in both parts?
+        const float ll = readlane(el, last), lb = readlane(eb, last);
+#pragma unroll
+        for (int i = 0; i < SortedSlots<NS>::kLists; ++i)
+#pragma unroll
+          for (int j = 0; j < SortedSlots<NS>::kLen; ++j)
+            if (left.key[i][j] > edge) {
+              const int at = ln.first + SortedSlots<NS>::kLen * i + int(left.order[i] >> (8 * j) & 255u);
+              open |= !(load1(row + at) == ll && bias[at] == lb);
+            }
+      }
     }
     if (__ballot(open)) {
       if (!filled) wide.fill(row, bias, p.scoring, w1, w2);
@@ -350,8 +463,13 @@ hipError_t launch_slots(const LT* logits, const float* bias, const RouteShape& s
   // the 64-bit choice may be needed where fp32 scores decide
   const bool scores = bias || (s.topk_group < s.n_group && s.group_best == 2);
   const size_t lds = scores ? size_t(kRouteWaves) * NS * kWave * sizeof(uint64_t) : 0;
+  // every lane with experts has NS of them, on the alignment of the wide loads
+  const int S = s.E / (s.topk_group < s.n_group ? s.n_group : 1);
+  const int whole = at.C == NS && S % NS == 0 && s.ld % 4 == 0 &&
+                    reinterpret_cast<uintptr_t>(logits) % (4 * sizeof(LT)) == 0 &&
+                    reinterpret_cast<uintptr_t>(bias) % 16 == 0;
   hipLaunchKernelGGL((route_experts_kernel<LT, NS>), dim3(unsigned((s.T + kRouteWaves - 1) / kRouteWaves)),
-                     dim3(64 * kRouteWaves), lds, stream, logits, bias, s, at.C, at.width, ids, w);
+                     dim3(64 * kRouteWaves), lds, stream, logits, bias, s, at.C, at.width, whole, ids, w);
   return hipGetLastError();
 }
 

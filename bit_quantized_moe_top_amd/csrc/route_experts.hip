@@ -1,26 +1,27 @@
-// moe_route_experts: one wave64 per token.
+// moe_route_experts: a token takes 64 or 16 lanes of a wave.
 //
-// Layout.  A group of experts lies on whole lanes, a power of two of them: with Gp the
-// groups rounded up to a power of two, lane l holds experts sub C .. sub C + C - 1 of
-// group l / (64 / Gp), sub = l % (64 / Gp), C = the group's experts per lane.  Lanes
-// ascend with the expert index, so the lowest tied lane (then the lowest slot of it)
-// is the lowest tied expert.  Without a group step (all groups stay) there is one group.
+// Layout.  A group of experts lies on whole lanes, a power of two of them: with Gp the groups rounded
+// up to a power of two, lane l of the token's holds experts sub C .. sub C + C - 1 of group l / (lanes /
+// Gp), sub = l % (lanes / Gp), C = the group's experts per lane.  Lanes ascend with the expert index,
+// so the lowest tied lane (then the lowest slot of it) is the lowest tied expert.  Without a group step
+// (all groups stay) there is one group.
 //
 // Choice.  The order wanted is that of the real numbers c = s + bias.
 //  * No bias: s grows with the logit, so experts are ordered by their logits, exactly.
-//  * Bias: c is formed in fp32 within an error of tol / 2 (below).  The fp32 order of the k
-//    picks stands if neighbours among them, and the last pick and every expert left, are
-//    at least tol apart or are the same number (equal logit and equal bias, hence a tie
-//    that the index decides).  Otherwise, and likewise for groups, the wave computes the
-//    token's c in 64 bits into LDS and picks there.
+//  * Bias: c is formed in fp32 within an error of tol / 2 (below).  The fp32 order of the k picks stands
+//    if neighbours among them, and the last pick and every expert left, are at least tol apart or are
+//    the same number (equal logit and equal bias, hence a tie that the index decides).  Otherwise the
+//    experts within tol of the last pick or above it, the only ones the true choice can be among, are
+//    ranked by their c in 64 bits.  Likewise for groups.  (For random logits some 3 tokens in 10000.)
 //
-// tol: with u = 2^-24, exp by the hardware's 2^x is within (1.5 |x| + 2) u of its value
-// (the product with log2 e, its rounding, 1 ulp).  Sigmoid: s (1 - s) |l| < 0.23, so
-// |ds| <= (0.9 + 1 + 2) u with the sum and the reciprocal.  Softmax: p |l - max| <= 0.37
-// pmax, pmax the largest score; its denominator's relative error is the p-weighted mean of
-// (2.5 |x| + 2) u, |x| <= 7 on average for 1024 experts, plus NS + 6 roundings: |dp| <=
-// 60 u pmax.  The sum with the bias: u |c|.  Twice that, and some: 2^-17 smax + 2^-22 |c|
-// with smax = pmax, or 1/8 for sigmoid.
+// tol: with u = 2^-24, exp by the hardware's 2^x is within (1.5 |x| + 2) u of its value (the product
+// with log2 e, its rounding, 1 ulp).  Sigmoid: s (1 - s) |l| < 0.23, so |ds| <= (0.9 + 1 + 2) u with the
+// sum and the reciprocal.  Softmax: p |l - max| <= 0.37 pmax, pmax the largest score; its denominator's
+// relative error is the p-weighted mean of (2.5 |x| + 2) u, |x| <= 7 on average for 1024 experts, plus
+// NS + 6 roundings: |dp| <= 60 u pmax.  The sum with the bias: u |c|.  Twice that, and some: 2^-17 smax +
+// 2^-22 |c| with smax = pmax, or 1/8 for sigmoid.
+//
+// Bound by VALU issue, a token's scores, sorts and k rounds against 4 E bytes read.  BOUNDNOTE
 #include "front.hpp"
 #include "serve_kernels.hpp"
 
@@ -28,7 +29,10 @@ namespace moeq {
 
 namespace {
 
-constexpr int kRouteWaves = 4;                 // tokens per workgroup
+constexpr int kRouteWaves = 4;                 // waves per workgroup
+static_assert(MOEQ_MAX_TOPK <= 16, "a token's picks lie in the first 16 lanes");
+constexpr int kDppRowShl1 = 0x101;             // lane i takes lane i + 1 of its 16
+constexpr int kDppRowRor = 0x120;              // + n: lane i takes lane (i - n) % 16
 
 // natural exponential by the hardware's 2^x
 __device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
@@ -36,119 +40,161 @@ __device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp
 __device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ float load1(const uint16_t* p) { return bf16_to_f32(*p); }
 
-// order-preserving key of a double (as score_key), at least 1 so that 0 marks "no candidate"
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t umin(uint32_t a, uint32_t b) { return a < b ? a : b; }
+// key of a score (as score_key), at least 1 (one NaN's is 0) so that 0 marks "no candidate"
+__device__ __forceinline__ uint32_t slot_key(float v) { return umax(score_key(v), 1u); }
 __device__ __forceinline__ uint64_t wide_key(double v) {
   const uint64_t b = __builtin_bit_cast(uint64_t, v + 0.0);
   const uint64_t k = b ^ ((b >> 63) ? ~0ull : 0x8000000000000000ull);
   return k ? k : 1ull;
 }
-
-__device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int m) {
-  const int lo = __shfl_xor(int(uint32_t(v)), m), hi = __shfl_xor(int(uint32_t(v >> 32)), m);
+__device__ __forceinline__ uint64_t shfl64(uint64_t v, int from) {
+  const int lo = __shfl(int(uint32_t(v)), from), hi = __shfl(int(uint32_t(v >> 32)), from);
   return uint64_t(uint32_t(lo)) | (uint64_t(uint32_t(hi)) << 32);
 }
-__device__ __forceinline__ double shfl_xor64(double v, int m) {
-  return __builtin_bit_cast(double, shfl_xor64(__builtin_bit_cast(uint64_t, v), m));
+__device__ __forceinline__ double shfl64(double v, int from) {
+  return __builtin_bit_cast(double, shfl64(__builtin_bit_cast(uint64_t, v), from));
 }
 
-// where a lane's experts are
-struct Lanes {
-  int G, S, C;                // groups (1 without a group step), experts per group and per lane
-  int width;                  // lanes per group
-  int g, first, n;            // this lane's group, its first expert, its experts
-  __device__ __forceinline__ Lanes(const RouteShape& s, bool grouped, int c, int w, int lane)
-      : G(grouped ? s.n_group : 1), S(s.E / G), C(c), width(w) {
-    g = lane / width;
-    const int at = (lane - g * width) * C;
-    first = g * S + at;
-    n = g < G ? min(max(S - at, 0), C) : 0;
-    if (n == 0) first = 0;
+// score of a logit in fp32: softmax relative to `top`, times 1 / denominator
+__device__ __forceinline__ float fast_score(float l, bool softmax, float top, float rden) {
+  return softmax ? exp_fast(l - top) * rden : __builtin_amdgcn_rcpf(1.0f + exp_fast(-l));
+}
+
+// ---------------------------------------------------- the choice in 64 bits
+// One token by a whole wave, from memory: rare, so short rather than fast.
+template <typename LT>
+struct WideChoice {
+  const LT* row;
+  const float* bias;
+  const RouteShape& p;
+  int lane;
+  double top, den;             // softmax
+
+  __device__ __forceinline__ WideChoice(const LT* row, const float* bias, const RouteShape& p, int lane)
+      : row(row), bias(bias), p(p), lane(lane), top(0.0), den(1.0) {
+    if (p.scoring != MOEQ_SCORE_SOFTMAX) return;
+    float m = -INFINITY;
+#pragma unroll 1
+    for (int e = lane; e < p.E; e += kWave) m = fmaxf(m, load1(row + e));
+    for (int i = 1; i < kWave; i <<= 1) m = fmaxf(m, __shfl_xor(m, i));
+    top = double(m);
+    den = 0.0;
+#pragma unroll 1
+    for (int e = lane; e < p.E; e += kWave) den += exp(double(load1(row + e)) - top);
+    for (int i = 1; i < kWave; i <<= 1) den += shfl64(den, lane ^ i);
+  }
+  __device__ __forceinline__ double c(int e) const {
+    const float l = load1(row + e);
+    if (l == -INFINITY) return -INFINITY;
+    const double s = p.scoring == MOEQ_SCORE_SOFTMAX ? exp(double(l) - top) / den
+                                                     : 1.0 / (1.0 + exp(-double(l)));
+    return bias ? s + double(bias[e]) : s;
+  }
+
+  // bit g: group g stays
+  __device__ __forceinline__ uint64_t groups() const {
+    const int S = p.E / p.n_group;
+    uint64_t mine = 0;                                   // lane g: group g's value
+    for (int g = 0; g < p.n_group; ++g) {
+      double b1 = -INFINITY, b2 = -INFINITY;
+#pragma unroll 1
+      for (int e = lane; e < S; e += kWave) {
+        const double v = c(g * S + e);
+        if (v > b1) { b2 = b1; b1 = v; }
+        else if (v > b2) b2 = v;
+      }
+      for (int i = 1; i < kWave; i <<= 1) {
+        const double o1 = shfl64(b1, lane ^ i), o2 = shfl64(b2, lane ^ i);
+        b2 = fmax(fmin(b1, o1), fmax(b2, o2));
+        b1 = fmax(b1, o1);
+      }
+      const uint64_t key = wide_key(p.group_best == 2 && b2 > -INFINITY ? b1 + b2 : b1);
+      if (lane == g) mine = key;
+    }
+    int above = 0;
+    for (int g = 0; g < p.n_group; ++g) {
+      const uint64_t other = shfl64(mine, g);
+      above += other > mine || (other == mine && g < lane);
+    }
+    return __ballot(lane < p.n_group && above < p.topk_group);
+  }
+
+  // The k best of the experts whose fp32 sum is above `edge` in the groups of `stay`: lane r returns
+  // the r-th (-1: there are fewer).  cand: 64 ints of LDS.
+  __device__ __forceinline__ int picks(uint64_t stay, float edge, float ftop, float rden, int* cand) const {
+    const int S = p.E / p.n_group;
+    const auto in = [&](int e) {
+      const float l = load1(row + e);
+      const float f = fast_score(l, p.scoring == MOEQ_SCORE_SOFTMAX, ftop, rden) + bias[e];
+      return l != -INFINITY && !(f <= edge) && (stay >> (e / S) & 1);
+    };
+    int m = 0;
+#pragma unroll 1
+    for (int e0 = 0; e0 < p.E; e0 += kWave) {
+      const bool take = e0 + lane < p.E && in(e0 + lane);
+      const uint64_t takers = __ballot(take);
+      const int at = m + __popcll(takers & ((uint64_t(1) << lane) - 1));
+      if (take && at < kWave) cand[at] = e0 + lane;
+      m += __popcll(takers);
+    }
+    lds_wave_sync();
+    if (m <= kWave) {
+      const int e = lane < m ? cand[lane] : -1;
+      const uint64_t key = e >= 0 ? wide_key(c(e)) : 0;
+      int rank = 0;                                      // (candidates ascend with the lane)
+      for (int i = 0; i < m; ++i) {
+        const uint64_t other = shfl64(key, i);
+        rank += other > key || (other == key && i < lane);
+      }
+      lds_wave_sync();
+      if (lane < m && rank < p.k) cand[rank] = e;
+      lds_wave_sync();
+      return lane < min(m, p.k) ? cand[lane] : -1;
+    }
+    // more candidates than lanes: round by round, the best after the last taken
+    uint64_t last = ~0ull;
+    int last_e = -1, mine = -1;
+    for (int r = 0; r < p.k; ++r) {
+      uint64_t best = 0;
+      int at = -1;
+#pragma unroll 1
+      for (int e = lane; e < p.E; e += kWave) {
+        if (!in(e)) continue;
+        const uint64_t key = wide_key(c(e));
+        if ((key < last || (key == last && e > last_e)) && key > best) { best = key; at = e; }
+      }
+      for (int i = 1; i < kWave; i <<= 1) {
+        const uint64_t o = shfl64(best, lane ^ i);
+        const int oe = __shfl(at, lane ^ i);
+        if (o > best || (o == best && oe < at)) { best = o; at = oe; }
+      }
+      last = best;
+      last_e = at;
+      if (lane == r) mine = at;
+    }
+    return mine;
   }
 };
 
-// The token's choice in 64 bits, for the lanes' experts: keys in LDS at [slot][lane].
-template <typename LT>
-struct WideChoice {
-  uint64_t* keys;
-  const Lanes& ln;
-  int lane;
-
-  // c of every expert, and the lane's two best unmasked (-inf: none)
-  __device__ __forceinline__ void fill(const LT* row, const float* bias, int scoring, double& b1,
-                                       double& b2) {
-    double top = 0.0, den = 1.0;
-    if (scoring == MOEQ_SCORE_SOFTMAX) {
-      top = -INFINITY;
-#pragma unroll 1
-      for (int j = 0; j < ln.n; ++j) top = fmax(top, double(load1(row + ln.first + j)));
-      for (int m = 1; m < kWave; m <<= 1) top = fmax(top, shfl_xor64(top, m));
-      double part = 0.0;
-#pragma unroll 1
-      for (int j = 0; j < ln.n; ++j) part += exp(double(load1(row + ln.first + j)) - top);
-      for (int m = 1; m < kWave; m <<= 1) part += shfl_xor64(part, m);
-      den = part;
-    }
-    b1 = b2 = -INFINITY;
-#pragma unroll 1
-    for (int j = 0; j < ln.n; ++j) {
-      const float l = load1(row + ln.first + j);
-      const double s = scoring == MOEQ_SCORE_SOFTMAX ? exp(double(l) - top) / den
-                                                     : 1.0 / (1.0 + exp(-double(l)));
-      double c = bias ? s + double(bias[ln.first + j]) : s;
-      if (l == -INFINITY) c = -INFINITY;
-      keys[j * kWave + lane] = wide_key(c);
-      if (c > b1) { b2 = b1; b1 = c; }
-      else if (c > b2) b2 = c;
-    }
-  }
-
-  // whether the lane's group stays
-  __device__ __forceinline__ bool group_stays(double b1, double b2, int best, int topk_group) const {
-    for (int m = 1; m < ln.width; m <<= 1) {
-      const double o1 = shfl_xor64(b1, m), o2 = shfl_xor64(b2, m);
-      b2 = fmax(fmin(b1, o1), fmax(b2, o2));
-      b1 = fmax(b1, o1);
-    }
-    const double v = best == 2 && b2 > -INFINITY ? b1 + b2 : b1;
-    const uint64_t key = wide_key(v);
-    int above = 0;
-    for (int g = 0; g < ln.G; ++g) {
-      const uint32_t lo = uint32_t(readlane(int(uint32_t(key)), g * ln.width));
-      const uint32_t hi = uint32_t(readlane(int(uint32_t(key >> 32)), g * ln.width));
-      const uint64_t other = uint64_t(lo) | (uint64_t(hi) << 32);
-      above += other > key || (other == key && g < ln.g);
-    }
-    return above < topk_group;
-  }
-
-  // the k best; lane r returns the r-th
-  __device__ __forceinline__ int pick(bool stays, int k, bool* live) {
-    const uint64_t none = wide_key(-INFINITY);
-    int mine = 0;
-    *live = false;
-    for (int r = 0; r < k; ++r) {
-      uint64_t best = 0;
-      int at = 0;
-#pragma unroll 1
-      for (int j = 0; j < ln.n; ++j) {
-        uint64_t key = keys[j * kWave + lane];
-        if (!stays && key != 0) key = none;
-        if (key > best) { best = key; at = j; }
-      }
-      uint64_t top = best;
-      for (int m = 1; m < kWave; m <<= 1) {
-        const uint64_t o = shfl_xor64(top, m);
-        top = o > top ? o : top;
-      }
-      const int from = __ffsll(static_cast<unsigned long long>(__ballot(best == top))) - 1;
-      const int e = readlane(ln.first + at, from);
-      if (lane == from) keys[at * kWave + lane] = 0;
-      if (lane == r) {
-        mine = e;
-        *live = top > none;
-      }
-    }
-    return mine;
+// where a lane's experts are
+struct Lanes {
+  int g, first, n;            // the lane's group, its first expert, its experts
+};
+// the shape's layout on the token's lanes, made by the host
+struct RouteLayout {
+  int G, S, C;                // groups (1 without a group step), experts per group and per lane
+  int shift;                  // log2 of the lanes per group
+  int whole;                  // every lane with experts has NS of them, aligned for wide loads
+  __device__ __forceinline__ Lanes lanes(int sub) const {
+    Lanes ln;
+    ln.g = sub >> shift;
+    const int at = (sub & ((1 << shift) - 1)) * C;
+    ln.first = ln.g * S + at;
+    ln.n = ln.g < G ? min(max(S - at, 0), C) : 0;
+    if (ln.n == 0) ln.first = 0;
+    return ln;
   }
 };
 
@@ -183,12 +229,6 @@ __device__ __forceinline__ void load_slots(const uint16_t* p, int n, bool whole,
   for (int j = 0; j < NS; ++j) v[j] = bf16_to_f32(p[min(j, max(n - 1, 0))]);
 }
 
-__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
-__device__ __forceinline__ uint32_t umin(uint32_t a, uint32_t b) { return a < b ? a : b; }
-__device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
-  return uint32_t(wave_reduce(int(v), [](int a, int b) { return int(umax(uint32_t(a), uint32_t(b))); }, 0));
-}
-
 // (b1, b2), b1 >= b2, of two lanes joined
 __device__ __forceinline__ void join2(uint32_t& b1, uint32_t& b2, uint32_t o1, uint32_t o2) {
   b2 = umax(umin(b1, o1), umax(b2, o2));
@@ -198,6 +238,43 @@ template <int CTRL>
 __device__ __forceinline__ void join2_dpp(uint32_t& b1, uint32_t& b2) {
   join2(b1, b2, uint32_t(dpp<CTRL>(0, int(b1))), uint32_t(dpp<CTRL>(0, int(b2))));
 }
+
+// The W lanes of a token, W = 64 (a wave per token) or 16 (a DPP row).
+template <int W>
+struct Token {
+  static_assert(W == 64 || W == 16, "a wave or a row");
+  template <typename T, typename Op>
+  static __device__ __forceinline__ T reduce(T v, Op op, T ident) {
+    if constexpr (W == 64) {
+      return wave_reduce(v, op, ident);
+    } else {
+      v = op(v, dpp<kDppQuadSwap1>(ident, v));
+      v = op(v, dpp<kDppQuadSwap2>(ident, v));
+      v = op(v, dpp<kDppRowHalfMirror>(ident, v));
+      return op(v, dpp<kDppRowMirror>(ident, v));
+    }
+  }
+  static __device__ __forceinline__ float max(float v) {
+    return reduce(v, [](float a, float b) { return fmaxf(a, b); }, -INFINITY);
+  }
+  static __device__ __forceinline__ float sum(float v) {
+    return reduce(v, [](float a, float b) { return a + b; }, 0.0f);
+  }
+  static __device__ __forceinline__ uint32_t max(uint32_t v) {
+    return uint32_t(reduce(int(v), [](int a, int b) { return int(umax(uint32_t(a), uint32_t(b))); }, 0));
+  }
+  // bit i: the condition of the token's lane i
+  static __device__ __forceinline__ uint64_t ballot(bool v, int lane) {
+    const uint64_t b = __ballot(v);
+    return W == 64 ? b : b >> (lane & 48) & 0xFFFFu;
+  }
+  // the value of the token's lane i (the same i in every lane)
+  template <typename T>
+  static __device__ __forceinline__ T from(T v, int i, int lane) {
+    if constexpr (W == 64) return readlane(v, i);
+    else return __shfl(v, (lane & 48) + i);
+  }
+};
 
 // A lane's experts as sorted lists of up to four (best first, the lower slot among equals), so that a
 // round of the selection looks at the heads only and taking one is a shift.  `order` holds a list's
@@ -243,6 +320,17 @@ struct SortedSlots {
     slot = kLen * list + int(o & 255u);
     return k;
   }
+  // takes the head of the lane's own `list`
+  __device__ __forceinline__ void take_own(int list) {
+#pragma unroll
+    for (int i = 0; i < kLists; ++i) {
+      const bool it = i == list;
+#pragma unroll
+      for (int j = 0; j + 1 < kLen; ++j) key[i][j] = it ? key[i][j + 1] : key[i][j];
+      key[i][kLen - 1] = it ? 0u : key[i][kLen - 1];
+      order[i] = it ? order[i] >> 8 : order[i];
+    }
+  }
   // takes the head of `list` (wave-uniform)
   __device__ __forceinline__ void take(int list) {
 #pragma unroll
@@ -256,23 +344,28 @@ struct SortedSlots {
   }
 };
 
-template <typename LT, int NS>
+// W = 64: tokens are few or their experts many.  W = 16: four tokens share a wave's instructions, but
+// a lane's lists are four times as many.
+template <typename LT, int W, int NS>
 __global__ void __launch_bounds__(64 * kRouteWaves)
 route_experts_kernel(const LT* __restrict__ logits, const float* __restrict__ bias, RouteShape p,
-                     int C, int width, int whole, int32_t* __restrict__ ids, float* __restrict__ w) {
-  extern __shared__ __align__(16) uint64_t wide_keys[];      // [waves][NS][64] where needed
-  const int lane = threadIdx.x & 63;
+                     RouteLayout lay, int32_t* __restrict__ ids, float* __restrict__ w) {
+  using Tok = Token<W>;
+  constexpr int kTokens = kWave / W;                         // of a wave
+  __shared__ int s_cand[kRouteWaves][kWave];
+  const int lane = threadIdx.x & 63, sub = lane & (W - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int t = blockIdx.x * kRouteWaves + wave;
-  if (t >= p.T) return;                                      // whole wave exits together
+  const int t0 = (blockIdx.x * kRouteWaves + wave) * kTokens;
+  if (t0 >= p.T) return;                                     // whole wave exits together
+  const int t = W == 64 ? t0 : min(t0 + lane / W, p.T - 1);  // (past the end the last token again)
   const bool grouped = p.topk_group < p.n_group;
   const bool softmax = p.scoring == MOEQ_SCORE_SOFTMAX;
-  const Lanes ln(p, grouped, C, width, lane);
+  const Lanes ln = lay.lanes(sub);
   const LT* row = logits + int64_t(t) * p.ld;
 
   float l[NS], c[NS];
-  load_slots<NS>(row + ln.first, ln.n, whole, l);
-  if (bias) load_slots<NS>(bias + ln.first, ln.n, whole, c);
+  load_slots<NS>(row + ln.first, ln.n, lay.whole, l);
+  if (bias) load_slots<NS>(bias + ln.first, ln.n, lay.whole, c);
 #pragma unroll
   for (int j = 0; j < NS; ++j)
     if (j >= ln.n) l[j] = -INFINITY;
@@ -283,13 +376,13 @@ route_experts_kernel(const LT* __restrict__ logits, const float* __restrict__ bi
     float m = -INFINITY;
 #pragma unroll
     for (int j = 0; j < NS; ++j) m = fmaxf(m, l[j]);
-    top = wave_reduce(m, [](float a, float b) { return fmaxf(a, b); }, -INFINITY);
+    top = Tok::max(m);
     if (top == -INFINITY) top = 0.0f;                        // every expert masked
     if (bias || !p.renormalize || (grouped && p.group_best == 2)) {
       float part = 0.0f;
 #pragma unroll
       for (int j = 0; j < NS; ++j) part += exp_fast(l[j] - top);
-      den = wave_sum(part);
+      den = Tok::sum(part);
     }
   }
 
@@ -302,22 +395,24 @@ route_experts_kernel(const LT* __restrict__ logits, const float* __restrict__ bi
   const uint32_t none = score_key(-INFINITY);
   uint32_t key[NS];
   if (scores) {
+    if (by_logit) {
 #pragma unroll
-    for (int j = 0; j < NS; ++j) {
-      const float s = softmax ? exp_fast(l[j] - top) * rden
-                              : __builtin_amdgcn_rcpf(1.0f + exp_fast(-l[j]));
-      c[j] = l[j] == -INFINITY ? -INFINITY : by_logit ? s : s + c[j];
+      for (int j = 0; j < NS; ++j) c[j] = 0.0f;
     }
-  }
+    if (softmax) {
 #pragma unroll
-  for (int j = 0; j < NS; ++j) {
-    key[j] = umax(score_key(scores ? c[j] : l[j]), 1u);      // (one NaN has key 0)
-    if (j >= ln.n) key[j] = 0u;
+      for (int j = 0; j < NS; ++j) c[j] = l[j] == -INFINITY ? -INFINITY : fast_score(l[j], true, top, rden) + c[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < NS; ++j) c[j] = l[j] == -INFINITY ? -INFINITY : fast_score(l[j], false, top, rden) + c[j];
+    }
+#pragma unroll
+    for (int j = 0; j < NS; ++j) key[j] = j < ln.n ? slot_key(c[j]) : 0u;
+  } else {
+#pragma unroll
+    for (int j = 0; j < NS; ++j) key[j] = j < ln.n ? slot_key(l[j]) : 0u;
   }
 
-  WideChoice<LT> wide{wide_keys + size_t(wave) * NS * kWave, ln, lane};
-  bool filled = false;
-  double w1 = 0.0, w2 = 0.0;
   bool stays = true;
   if (grouped) {
     uint32_t b1 = 0u, b2 = 0u;
@@ -326,68 +421,93 @@ route_experts_kernel(const LT* __restrict__ logits, const float* __restrict__ bi
       b2 = umax(b2, umin(b1, key[j]));
       b1 = umax(b1, key[j]);
     }
-    if (width > 1) join2_dpp<kDppQuadSwap1>(b1, b2);
-    if (width > 2) join2_dpp<kDppQuadSwap2>(b1, b2);
-    if (width > 4) join2_dpp<kDppRowHalfMirror>(b1, b2);
-    if (width > 8) join2_dpp<kDppRowMirror>(b1, b2);
-    if (width > 16) join2(b1, b2, uint32_t(__shfl_xor(int(b1), 16)), uint32_t(__shfl_xor(int(b2), 16)));
+    if (lay.shift > 0) join2_dpp<kDppQuadSwap1>(b1, b2);
+    if (lay.shift > 1) join2_dpp<kDppQuadSwap2>(b1, b2);
+    if (lay.shift > 2) join2_dpp<kDppRowHalfMirror>(b1, b2);
+    if (W == 64 && lay.shift > 3) join2_dpp<kDppRowMirror>(b1, b2);
+    if (W == 64 && lay.shift > 4)
+      join2(b1, b2, uint32_t(__shfl_xor(int(b1), 16)), uint32_t(__shfl_xor(int(b2), 16)));
+    if (ln.g >= lay.G) b1 = b2 = 0u;
     const bool live = b1 > none;
-    if (!scores) {                                           // best of the logits: exact
-      int above = 0;
-      for (int g = 0; g < ln.G; ++g) {
-        const uint32_t other = uint32_t(readlane(int(b1), g * width));
-        above += other > b1 || (other == b1 && g < ln.g);
+    const bool two = p.group_best == 2 && b2 > none;
+    const float f1 = key_score(b1), f2 = two ? key_score(b2) : 0.0f;
+    const float half = scores ? 0x1p-17f * smax + 0x1p-22f * (fabsf(f1) + fabsf(f2)) : 0.0f;
+    const float lo = scores ? f1 + f2 - half : f1;
+    const float hi = live ? (scores ? f1 + f2 + half : f1) : -INFINITY;
+    // A group stays for sure if at most topk_group - 1 others may be above it.  If as many stay for
+    // sure as are to stay, the choice is made.  (The best of the logits are exact: equal ones count
+    // if their group is lower.)
+    int maybe = 0;                                           // groups, itself among them
+    if constexpr (W == 64) {
+      for (int g = 0; g < lay.G; ++g) {
+        const float other = readlane(hi, g << lay.shift);
+        maybe += other > lo || (other == lo && (scores || g <= ln.g)) ? 1 : 0;
       }
-      stays = above < p.topk_group;
-    } else {
-      // A group stays for sure if at most topk_group - 1 others may be above it.  If as many stay
-      // for sure as are to stay, the choice is made.
-      const bool two = p.group_best == 2 && b2 > none;
-      const float f1 = key_score(b1), f2 = two ? key_score(b2) : 0.0f;
-      const float half = 0x1p-17f * smax + 0x1p-22f * (fabsf(f1) + fabsf(f2));
-      const float lo = f1 + f2 - half;
-      const float hi = live ? f1 + f2 + half : -INFINITY;
-      int maybe = 0;
-      for (int g = 0; g < ln.G; ++g) maybe += readlane(hi, g * width) >= lo ? 1 : 0;   // and itself
-      const uint64_t leads = __ballot(live && ln.g < ln.G && lane == ln.g * width);
-      const int n_live = __popcll(leads);
-      stays = live ? maybe <= p.topk_group
-                   // empty groups: after all the others, the lower first
-                   : n_live + __popcll(__ballot(!live && ln.g < ln.G && lane == ln.g * width) &
-                                       ((uint64_t(1) << (ln.g * width & 63)) - 1)) < p.topk_group;
-      const int sure = __popcll(__ballot(stays) & leads);
-      if (sure < min(p.topk_group, n_live)) {
-        wide.fill(row, bias, p.scoring, w1, w2);
-        filled = true;
-        stays = wide.group_stays(w1, w2, p.group_best, p.topk_group);
-      }
+    } else {                                                 // lanes of groups, by rotation of the row
+      const auto count = [&](auto n) {
+        const float other = dpp<kDppRowRor + decltype(n)::value>(0.0f, hi);
+        const int og = ((sub - decltype(n)::value) & 15) >> lay.shift;
+        maybe += other > lo || (other == lo && (scores || og <= ln.g)) ? 1 : 0;
+      };
+      maybe += hi >= lo ? 1 : 0;
+      count(SlotsTag<1>{}); count(SlotsTag<2>{}); count(SlotsTag<3>{}); count(SlotsTag<4>{});
+      count(SlotsTag<5>{}); count(SlotsTag<6>{}); count(SlotsTag<7>{}); count(SlotsTag<8>{});
+      count(SlotsTag<9>{}); count(SlotsTag<10>{}); count(SlotsTag<11>{}); count(SlotsTag<12>{});
+      count(SlotsTag<13>{}); count(SlotsTag<14>{}); count(SlotsTag<15>{});
+      maybe >>= lay.shift;
     }
-  }
-  if (scores && by_logit) {
+    const bool lead = ln.g < lay.G && sub == ln.g << lay.shift;
+    const int n_live = __popcll(Tok::ballot(live && lead, lane));
+    // empty groups: after all the others, the lower first
+    const uint64_t empty = Tok::ballot(!live && lead, lane);
+    stays = live ? maybe <= p.topk_group
+                 : n_live + __popcll(empty & ((uint64_t(1) << (ln.g << lay.shift & 63)) - 1)) < p.topk_group;
+    const bool open = __popcll(Tok::ballot(stays && live && lead, lane)) < min(p.topk_group, n_live);
+    for (uint64_t tokens = __ballot(open && sub == 0); tokens; tokens &= tokens - 1) {
+      const int at = __ffsll(static_cast<unsigned long long>(tokens)) - 1;     // the token's first lane
+      const WideChoice<LT> wide(logits + int64_t(min(t0 + at / W, p.T - 1)) * p.ld, bias, p, lane);
+      const uint64_t stay = wide.groups();
+      if (lane / W == at / W) stays = stay >> (ln.g & 63) & 1;
+    }
+    if (scores && by_logit) {
 #pragma unroll
-    for (int j = 0; j < NS; ++j) key[j] = j < ln.n ? umax(score_key(l[j]), 1u) : 0u;
-  }
-  if (grouped) {
+      for (int j = 0; j < NS; ++j) key[j] = j < ln.n ? slot_key(l[j]) : 0u;
+    }
 #pragma unroll
     for (int j = 0; j < NS; ++j) key[j] = stays ? key[j] : umin(key[j], none);
   }
 
-  // k rounds of a wave-wide argmax over the heads
+  // k rounds of an argmax over the heads
   SortedSlots<NS> left;
   left.sort(key);
-  int e = 0, ekey = 0;
+  int e = 0, ekey = 0;                                       // lane r: the r-th pick and its key
   for (int r = 0; r < p.k; ++r) {
     int slot, list;
     const uint32_t mine = left.best(slot, list);
-    const uint32_t kmax = wave_umax(mine);
-    const int from = __ffsll(static_cast<unsigned long long>(__ballot(mine == kmax))) - 1;
-    const int be = readlane(ln.first + slot, from);
-    const int from_list = SortedSlots<NS>::kLists > 1 ? readlane(list, from) : 0;
-    if (lane == from) left.take(from_list);
-    e = lane == r ? be : e;
-    ekey = lane == r ? int(kmax) : ekey;
+    const uint32_t kmax = Tok::max(mine);
+    if constexpr (W == 64) {
+      const int from = __ffsll(static_cast<unsigned long long>(__ballot(mine == kmax))) - 1;
+      const int be = readlane(ln.first + slot, from);
+      const int from_list = SortedSlots<NS>::kLists > 1 ? readlane(list, from) : 0;
+      if (lane == from) left.take(from_list);
+      e = lane == r ? be : e;
+      ekey = lane == r ? int(kmax) : ekey;
+    } else {
+      // the row's lowest lane at the maximum takes its head and leaves the expert in LDS
+      const uint64_t tied = Tok::ballot(mine == kmax, lane);
+      if ((tied & ((2u << sub) - 1u)) == (1u << sub)) {
+        s_cand[wave][(lane & 48) + r] = ln.first + slot;
+        left.take_own(list);
+      }
+      ekey = sub == r ? int(kmax) : ekey;
+    }
   }
-  const bool pick = lane < p.k;
+  if constexpr (W == 16) {
+    lds_wave_sync();
+    e = sub < p.k ? s_cand[wave][lane] : 0;
+    lds_wave_sync();
+  }
+  const bool pick = sub < p.k;
   float el = load1(row + e);
   bool live = pick && uint32_t(ekey) > none;
 
@@ -395,40 +515,56 @@ route_experts_kernel(const LT* __restrict__ logits, const float* __restrict__ bi
     // does the fp32 order stand?
     const float ec = key_score(uint32_t(ekey)), eb = bias[e];
     const float tol = 0x1p-17f * smax + 0x1p-22f * fabsf(ec);
-    const float nc = __shfl_down(ec, 1), nl = __shfl_down(el, 1), nb = __shfl_down(eb, 1);
-    const bool nlive = __shfl_down(int(live), 1) != 0;
-    bool open = live && nlive && lane + 1 < p.k && ec - nc < tol && !(nl == el && nb == eb);
+    const float nc = dpp<kDppRowShl1>(0.0f, ec), nl = dpp<kDppRowShl1>(0.0f, el), nb = dpp<kDppRowShl1>(0.0f, eb);
+    const bool nlive = dpp<kDppRowShl1>(0, int(live)) != 0;
+    bool open = live && nlive && sub + 1 < p.k && ec - nc < tol && !(nl == el && nb == eb);
     const int last = p.k - 1;
-    if (uint32_t(readlane(ekey, last)) > none) {
-      const uint32_t edge = umax(score_key(readlane(ec - tol, last)), none);
-      bool near = false;
+    const bool last_live = Tok::from(int(live), last, lane) != 0;
+    const float edge = last_live ? Tok::from(ec - tol, last, lane) : -INFINITY;
+    const uint32_t edge_key = last_live ? umax(score_key(edge), none) : 0xFFFFFFFFu;
+    bool near = false;
 #pragma unroll
-      for (int i = 0; i < SortedSlots<NS>::kLists; ++i) near |= left.key[i][0] > edge;
-      if (__ballot(near)) {                                  // equal to the last pick in both parts?
-        const float ll = readlane(el, last), lb = readlane(eb, last);
+    for (int i = 0; i < SortedSlots<NS>::kLists; ++i) near |= left.key[i][0] > edge_key;
+    if (__ballot(near)) {                                    // equal to the last pick in both parts?
+      const float ll = Tok::from(el, last, lane), lb = Tok::from(eb, last, lane);
 #pragma unroll
-        for (int i = 0; i < SortedSlots<NS>::kLists; ++i)
+      for (int i = 0; i < SortedSlots<NS>::kLists; ++i)
 #pragma unroll
-          for (int j = 0; j < SortedSlots<NS>::kLen; ++j)
-            if (left.key[i][j] > edge) {
-              const int at = ln.first + SortedSlots<NS>::kLen * i + int(left.order[i] >> (8 * j) & 255u);
-              open |= !(load1(row + at) == ll && bias[at] == lb);
-            }
-      }
+        for (int j = 0; j < SortedSlots<NS>::kLen; ++j)
+          if (left.key[i][j] > edge_key) {
+            const int at = ln.first + SortedSlots<NS>::kLen * i + int(left.order[i] >> (8 * j) & 255u);
+            open |= !(load1(row + at) == ll && bias[at] == lb);
+          }
     }
     if (__ballot(open)) {
-      if (!filled) wide.fill(row, bias, p.scoring, w1, w2);
-      e = wide.pick(stays, p.k, &live);
-      live = live && pick;
-      el = load1(row + e);
+      // tokens in turn, each by the whole wave
+      for (int i = 0; i < kTokens; ++i) {
+        const uint64_t mine = W == 64 ? ~0ull : uint64_t(0xFFFFu) << (16 * i);
+        if ((__ballot(open) & mine) == 0) continue;
+        uint64_t stay = ~0ull;                               // groups of the public numbering
+        if (grouped) {
+          const uint64_t lanes = __ballot(stays) >> (W * i & 63);
+          stay = 0;
+          for (int g = 0; g < lay.G; ++g) stay |= (lanes >> (g << lay.shift) & 1) << g;
+        }
+        const WideChoice<LT> wide(logits + int64_t(min(t0 + i, p.T - 1)) * p.ld, bias, p, lane);
+        int got = wide.picks(stay, readlane(edge, W * i), readlane(top, W * i), readlane(rden, W * i), s_cand[wave]);
+        // (as many as have a score: with a NaN among the values not always, and then the fp32 picks,
+        // which are distinct, stay)
+        const bool all = __popcll(__ballot(got >= 0)) == __popcll(__ballot(live) & mine);
+        got = __shfl(got, lane & (W - 1));
+        if (lane / W == i && pick && got >= 0 && all) {
+          e = got;
+          el = load1(row + e);
+        }
+      }
     }
   }
 
   // weights, lane r the r-th expert's: sigmoid scores 1 / (1 + exp(-l)); where only their ratios
   // count and all are below 1/2 the common factor exp(max l) is left out, so that none
   // underflows.  Softmax scores relative to the largest chosen, or to the largest of all.
-  const float lmax = wave_reduce(live ? el : -INFINITY,
-                                 [](float a, float b) { return fmaxf(a, b); }, -INFINITY);
+  const float lmax = Tok::max(live ? el : -INFINITY);
   float s = 0.0f;
   if (live) {
     if (softmax)
@@ -438,51 +574,57 @@ route_experts_kernel(const LT* __restrict__ logits, const float* __restrict__ bi
     else
       s = 1.0f / (1.0f + expf(-el));
   }
-  const float sum = p.renormalize ? wave_sum(s) : den;
-  if (pick) {
-    ids[int64_t(t) * p.k + lane] = e;
-    w[int64_t(t) * p.k + lane] = live ? s / sum * p.scale : 0.0f;
+  const float sum = p.renormalize ? Tok::sum(s) : den;
+  if (pick && (W == 64 || t0 + lane / W < p.T)) {
+    ids[int64_t(t) * p.k + sub] = e;
+    w[int64_t(t) * p.k + sub] = live ? s / sum * p.scale : 0.0f;
   }
 }
 
-// lanes per group and experts per lane
-struct RouteLayout {
-  int width, C;
-};
-RouteLayout route_layout(const RouteShape& s) {
-  const int G = s.topk_group < s.n_group ? s.n_group : 1;
-  int gp = 1;
-  while (gp < G) gp *= 2;
-  const int width = kWave / gp;
-  return {width, (s.E / G + width - 1) / width};
+// the layout on W lanes (W not enough for the groups: C = 0)
+RouteLayout route_layout(const RouteShape& s, int W) {
+  RouteLayout at;
+  at.G = s.topk_group < s.n_group ? s.n_group : 1;
+  at.S = s.E / at.G;
+  at.shift = 0;
+  while ((W >> at.shift) > 1 && at.G <= (W >> (at.shift + 1))) ++at.shift;
+  at.C = at.G <= W ? (at.S + (1 << at.shift) - 1) >> at.shift : 0;
+  at.whole = 0;
+  return at;
 }
 
-template <typename LT, int NS>
+template <typename LT, int W, int NS>
 hipError_t launch_slots(const LT* logits, const float* bias, const RouteShape& s, RouteLayout at,
                         int32_t* ids, float* w, hipStream_t stream) {
-  // the 64-bit choice may be needed where fp32 scores decide
-  const bool scores = bias || (s.topk_group < s.n_group && s.group_best == 2);
-  const size_t lds = scores ? size_t(kRouteWaves) * NS * kWave * sizeof(uint64_t) : 0;
-  // every lane with experts has NS of them, on the alignment of the wide loads
-  const int S = s.E / (s.topk_group < s.n_group ? s.n_group : 1);
-  const int whole = at.C == NS && S % NS == 0 && s.ld % 4 == 0 &&
-                    reinterpret_cast<uintptr_t>(logits) % (4 * sizeof(LT)) == 0 &&
-                    reinterpret_cast<uintptr_t>(bias) % 16 == 0;
-  hipLaunchKernelGGL((route_experts_kernel<LT, NS>), dim3(unsigned((s.T + kRouteWaves - 1) / kRouteWaves)),
-                     dim3(64 * kRouteWaves), lds, stream, logits, bias, s, at.C, at.width, whole, ids, w);
+  at.whole = at.C == NS && at.S % NS == 0 && s.ld % 4 == 0 &&
+             reinterpret_cast<uintptr_t>(logits) % (4 * sizeof(LT)) == 0 &&
+             reinterpret_cast<uintptr_t>(bias) % 16 == 0;
+  constexpr int kPerBlock = kRouteWaves * (kWave / W);
+  hipLaunchKernelGGL((route_experts_kernel<LT, W, NS>), dim3(unsigned((s.T + kPerBlock - 1) / kPerBlock)),
+                     dim3(64 * kRouteWaves), 0, stream, logits, bias, s, at, ids, w);
   return hipGetLastError();
 }
+
+// Four tokens a wave from this many tokens on: fewer waves than that leave SIMDs without work, and a
+// wave takes longer.  SHARENOTE
+constexpr int kShareTokens = 4096;
 
 template <typename LT>
 hipError_t launch_typed(const LT* logits, const float* bias, const RouteShape& s, int32_t* ids,
                         float* w, hipStream_t stream) {
-  const RouteLayout at = route_layout(s);
-  if (at.C <= 1) return launch_slots<LT, 1>(logits, bias, s, at, ids, w, stream);
-  if (at.C <= 2) return launch_slots<LT, 2>(logits, bias, s, at, ids, w, stream);
-  if (at.C <= 4) return launch_slots<LT, 4>(logits, bias, s, at, ids, w, stream);
-  if (at.C <= 8) return launch_slots<LT, 8>(logits, bias, s, at, ids, w, stream);
-  if (at.C <= 16) return launch_slots<LT, 16>(logits, bias, s, at, ids, w, stream);
-  return launch_slots<LT, 32>(logits, bias, s, at, ids, w, stream);   // C <= 31: E <= 1024
+  RouteLayout at = route_layout(s, 16);
+  if (s.T >= kShareTokens && at.C >= 1 && at.C <= 16) {
+    if (at.C <= 4) return launch_slots<LT, 16, 4>(logits, bias, s, at, ids, w, stream);
+    if (at.C <= 8) return launch_slots<LT, 16, 8>(logits, bias, s, at, ids, w, stream);
+    return launch_slots<LT, 16, 16>(logits, bias, s, at, ids, w, stream);
+  }
+  at = route_layout(s, 64);
+  if (at.C <= 1) return launch_slots<LT, 64, 1>(logits, bias, s, at, ids, w, stream);
+  if (at.C <= 2) return launch_slots<LT, 64, 2>(logits, bias, s, at, ids, w, stream);
+  if (at.C <= 4) return launch_slots<LT, 64, 4>(logits, bias, s, at, ids, w, stream);
+  if (at.C <= 8) return launch_slots<LT, 64, 8>(logits, bias, s, at, ids, w, stream);
+  if (at.C <= 16) return launch_slots<LT, 64, 16>(logits, bias, s, at, ids, w, stream);
+  return launch_slots<LT, 64, 32>(logits, bias, s, at, ids, w, stream);   // C <= 31: E <= 1024
 }
 
 }  // namespace

@@ -241,3 +241,83 @@ def test_captured_and_replayed_and_on_another_stream():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(ids, ref[0]) and torch.equal(w, ref[1])
+
+
+def check_many(rows, bias, k, **kw):
+    """The rows again and again up to a call of many tokens: each time what the oracle says of them,
+    to the bit the same wherever in the call they stand."""
+    n = rows.shape[0]
+    times = -(-4103 // n)
+    T = 4103 + n                                                     # no multiple of a wave's tokens
+    logits = rows.repeat(times + 1, 1)[:T]
+    ids, w = mq.moe_route_experts(logits.to(DEV), k, bias=None if bias is None else bias.to(DEV), **kw)
+    ids, w = ids.cpu(), w.cpu()
+    again = torch.arange(T) % n
+    assert torch.equal(ids, ids[:n][again]) and torch.equal(w, w[:n][again])
+    small = check(rows, bias, k, **kw)                               # (both against the oracle)
+    assert torch.equal(small[0].cpu(), ids[:n])
+    z = to_np(rows).astype(np.float64)
+    _, rw = R.route_experts(z, k, bias=None if bias is None else bias.numpy(), **kw)
+    fin = np.where(np.isfinite(z), z, np.nan)
+    with np.errstate(all="ignore"):
+        spread = np.nan_to_num(np.nanmax(fin, 1) - np.nanmin(fin, 1))[:, None]
+    tol = (80 + 2 * spread) * U * np.abs(rw) + 2.0 ** -126 * max(1.0, abs(kw.get("scale", 1.0)))
+    assert (np.abs(w[:n].numpy().astype(np.float64) - rw) <= tol).all()
+
+
+@pytest.mark.parametrize("E,k,G,tg", [(1, 1, 1, 1), (7, 3, 7, 3), (16, 8, 16, 9), (40, 8, 10, 10), (64, 8, 8, 3),
+                                      (65, 8, 1, 1), (128, 8, 1, 1), (150, 5, 5, 3), (250, 8, 2, 1),
+                                      (256, 8, 8, 4), (256, 8, 1, 1), (256, 6, 16, 5), (257, 4, 1, 1)])
+@pytest.mark.parametrize("scoring", [SOFT, SIGM])
+def test_many_tokens(E, k, G, tg, scoring):
+    g = gen(E * k)
+    rows = torch.randn(37, E, generator=g) * 1.5
+    rows[3] = -INF                                                   # masked: all,
+    rows[4, 1:] = -INF                                               # all but one,
+    rows[5, :E // 2] = -INF                                          # half,
+    rows[6:9][torch.rand(3, E, generator=g) < 0.8] = -INF            # most
+    bias = torch.randn(E, generator=g) * (0.2 if scoring == SIGM else 2.0 / E)
+    for best in (1, 2):
+        kw = dict(scoring=scoring, n_group=G, topk_group=tg, group_best=best)
+        check_many(rows, bias, k, **kw)
+        check_many(rows.to(torch.bfloat16), None, k, renormalize=False, scale=2.5, **kw)
+
+
+@pytest.mark.parametrize("E,G,tg", [(64, 1, 1), (256, 8, 4), (150, 5, 2), (256, 1, 1)])
+@pytest.mark.parametrize("scoring", [SOFT, SIGM])
+def test_many_tokens_too_close_for_fp32(E, G, tg, scoring):
+    g = gen(E + G)
+    row = torch.randn(1, E, generator=g)
+    s = R.scores(row.numpy(), scoring)[0]
+    bias = torch.from_numpy((0.75 - s).astype(np.float32))
+    rows = row.repeat(29, 1)
+    rows[1::2] += torch.randn(14, E, generator=g) * 1e-7
+    rows[2::4] = torch.randn(7, E, generator=g)                      # some tokens of a wave are clear
+    for k in (1, 8):
+        for best in (1, 2):
+            check_many(rows, bias, k, scoring=scoring, n_group=G, topk_group=tg, group_best=best)
+
+
+@pytest.mark.parametrize("scoring", [SOFT, SIGM])
+def test_many_tokens_ties_and_nonfinite(scoring):
+    g = gen(17)
+    rows = (torch.randn(31, 256, generator=g) * 2).round() / 2
+    rows[0] = 1.0
+    bias = (torch.randn(256, generator=g) * 2).round() / 16
+    for G, tg in ((1, 1), (8, 3)):
+        for b in (None, bias):
+            check_many(rows, b, 8, scoring=scoring, n_group=G, topk_group=tg, group_best=2)
+            z = rows.repeat(140, 1)
+            kw = dict(scoring=scoring, n_group=G, topk_group=tg, bias=None if b is None else b.to(DEV))
+            clean = mq.moe_route_experts(z.to(DEV), 8, **kw)
+            bad = torch.arange(5, z.shape[0], 97)
+            z[bad, 3] = float("nan")
+            z[bad[1::3], 200] = INF
+            z[bad[2::3]] = -float("nan")
+            ids, w = mq.moe_route_experts(z.to(DEV), 8, **kw)
+            ids, w = ids.cpu(), w.cpu()
+            assert ((ids >= 0) & (ids < 256)).all()
+            assert all(len(set(r)) == 8 for r in ids[bad].tolist())
+            keep = torch.ones(z.shape[0], dtype=torch.bool)
+            keep[bad] = False
+            assert torch.equal(ids[keep], clean[0].cpu()[keep]) and torch.equal(w[keep], clean[1].cpu()[keep])

@@ -22,6 +22,8 @@
 // 2^-22 |c| with smax = pmax, or 1/8 for sigmoid.
 //
 // Bound by VALU issue, a token's scores, sorts and k rounds against 4 E bytes read.  BOUNDNOTE
+#include <algorithm>
+
 #include "front.hpp"
 #include "serve_kernels.hpp"
 
@@ -63,86 +65,99 @@ __device__ __forceinline__ float fast_score(float l, bool softmax, float top, fl
 }
 
 // ---------------------------------------------------- the choice in 64 bits
-// One token by a whole wave, from memory: rare, so short rather than fast.
+// One token by a whole wave.  Rare, but a wave that comes here ends last: experts are read four a lane at
+// a time and the candidates ranked side by side (4096 tokens of 1024 experts, six of them here: 15.3 us
+// against 18.5 with one expert a lane at a time and a pass over them for each pick).  Few registers, for
+// these are the whole kernel's: with the row kept in them that case took 16.2 us, but 16384 tokens of 256
+// experts 18.5 against 15.3.
 template <typename LT>
 struct WideChoice {
   const LT* row;
   const float* bias;
   const RouteShape& p;
   int lane;
-  double top, den;             // softmax
+  bool softmax;
+  double top, den;                                       // softmax
 
-  __device__ __forceinline__ WideChoice(const LT* row, const float* bias, const RouteShape& p, int lane)
-      : row(row), bias(bias), p(p), lane(lane), top(0.0), den(1.0) {
-    if (p.scoring != MOEQ_SCORE_SOFTMAX) return;
-    float m = -INFINITY;
-#pragma unroll 1
-    for (int e = lane; e < p.E; e += kWave) m = fmaxf(m, load1(row + e));
-    for (int i = 1; i < kWave; i <<= 1) m = fmaxf(m, __shfl_xor(m, i));
-    top = double(m);
+  __device__ __forceinline__ WideChoice(const LT* row, const float* bias, const RouteShape& p, int lane,
+                                        float ftop)
+      : row(row), bias(bias), p(p), lane(lane), softmax(p.scoring == MOEQ_SCORE_SOFTMAX), top(ftop), den(1.0) {
+    if (!softmax) return;
     den = 0.0;
-#pragma unroll 1
-    for (int e = lane; e < p.E; e += kWave) den += exp(double(load1(row + e)) - top);
+    each(lane, kWave, p.E, [&](int, float l, float) { den += exp(double(l) - top); });
     for (int i = 1; i < kWave; i <<= 1) den += shfl64(den, lane ^ i);
   }
-  __device__ __forceinline__ double c(int e) const {
-    const float l = load1(row + e);
+  // fn(expert, logit, bias) for the experts first, first + step, ... below end; past it the logit is
+  // -inf, so that the wave's lanes stay together
+  template <typename Fn>
+  __device__ __forceinline__ void each(int first, int step, int end, Fn fn) const {
+#pragma unroll 1
+    for (int e0 = first; __ballot(e0 < end); e0 += 4 * step) {
+      float l[4], b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int e = min(e0 + step * j, p.E - 1);
+        l[j] = load1(row + e);
+        b[j] = bias ? bias[e] : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int e = e0 + step * j;
+        fn(e, e < end ? l[j] : -INFINITY, b[j]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+  __device__ __forceinline__ double c(float l, float b) const {
     if (l == -INFINITY) return -INFINITY;
-    const double s = p.scoring == MOEQ_SCORE_SOFTMAX ? exp(double(l) - top) / den
-                                                     : 1.0 / (1.0 + exp(-double(l)));
-    return bias ? s + double(bias[e]) : s;
+    return (softmax ? exp(double(l) - top) / den : 1.0 / (1.0 + exp(-double(l)))) + double(b);
   }
 
-  // bit g: group g stays
-  __device__ __forceinline__ uint64_t groups() const {
-    const int S = p.E / p.n_group;
-    uint64_t mine = 0;                                   // lane g: group g's value
-    for (int g = 0; g < p.n_group; ++g) {
-      double b1 = -INFINITY, b2 = -INFINITY;
-#pragma unroll 1
-      for (int e = lane; e < S; e += kWave) {
-        const double v = c(g * S + e);
-        if (v > b1) { b2 = b1; b1 = v; }
-        else if (v > b2) b2 = v;
-      }
-      for (int i = 1; i < kWave; i <<= 1) {
-        const double o1 = shfl64(b1, lane ^ i), o2 = shfl64(b2, lane ^ i);
-        b2 = fmax(fmin(b1, o1), fmax(b2, o2));
-        b1 = fmax(b1, o1);
-      }
-      const uint64_t key = wide_key(p.group_best == 2 && b2 > -INFINITY ? b1 + b2 : b1);
-      if (lane == g) mine = key;
+  // bit g: group g stays.  Groups lie on whole lanes, 2^shift of them.
+  __device__ __forceinline__ uint64_t groups(int shift) const {
+    const int S = p.E / p.n_group, C = (S + (1 << shift) - 1) >> shift;
+    const int g = lane >> shift, at = (lane & ((1 << shift) - 1)) * C;
+    const int first = g * S + at;
+    double b1 = -INFINITY, b2 = -INFINITY;
+    each(first, 1, g < p.n_group ? min(first + C, (g + 1) * S) : 0, [&](int, float l, float b) {
+      const double x = c(l, b);
+      b2 = fmax(b2, fmin(b1, x));
+      b1 = fmax(b1, x);
+    });
+    for (int i = 0; i < shift; ++i) {
+      const double o1 = shfl64(b1, lane ^ 1 << i), o2 = shfl64(b2, lane ^ 1 << i);
+      b2 = fmax(fmin(b1, o1), fmax(b2, o2));
+      b1 = fmax(b1, o1);
     }
+    const uint64_t value = wide_key(p.group_best == 2 && b2 > -INFINITY ? b1 + b2 : b1);
+    const uint64_t mine = shfl64(value, lane << shift & 63);             // lane g: group g's
     int above = 0;
-    for (int g = 0; g < p.n_group; ++g) {
-      const uint64_t other = shfl64(mine, g);
-      above += other > mine || (other == mine && g < lane);
+    for (int o = 0; o < p.n_group; ++o) {
+      const uint64_t other = shfl64(mine, o);
+      above += other > mine || (other == mine && o < lane);
     }
     return __ballot(lane < p.n_group && above < p.topk_group);
   }
 
   // The k best of the experts whose fp32 sum is above `edge` in the groups of `stay`: lane r returns
   // the r-th (-1: there are fewer).  cand: 64 ints of LDS.
-  __device__ __forceinline__ int picks(uint64_t stay, float edge, float ftop, float rden, int* cand) const {
+  __device__ __forceinline__ int picks(uint64_t stay, float edge, float rden, int* cand) const {
     const int S = p.E / p.n_group;
-    const auto in = [&](int e) {
-      const float l = load1(row + e);
-      const float f = fast_score(l, p.scoring == MOEQ_SCORE_SOFTMAX, ftop, rden) + bias[e];
-      return l != -INFINITY && !(f <= edge) && (stay >> (e / S) & 1);
+    const auto in = [&](int e, float l, float b) {
+      return l != -INFINITY && !(fast_score(l, softmax, float(top), rden) + b <= edge) && (stay >> (e / S & 63) & 1);
     };
     int m = 0;
-#pragma unroll 1
-    for (int e0 = 0; e0 < p.E; e0 += kWave) {
-      const bool take = e0 + lane < p.E && in(e0 + lane);
+    each(lane, kWave, p.E, [&](int e, float l, float b) {
+      const bool take = in(e, l, b);
       const uint64_t takers = __ballot(take);
       const int at = m + __popcll(takers & ((uint64_t(1) << lane) - 1));
-      if (take && at < kWave) cand[at] = e0 + lane;
+      if (take && at < kWave) cand[at] = e;
       m += __popcll(takers);
-    }
+    });
     lds_wave_sync();
     if (m <= kWave) {
       const int e = lane < m ? cand[lane] : -1;
-      const uint64_t key = e >= 0 ? wide_key(c(e)) : 0;
+      const uint64_t key = e >= 0 ? wide_key(c(load1(row + e), bias[e])) : 0;
       int rank = 0;                                      // (candidates ascend with the lane)
       for (int i = 0; i < m; ++i) {
         const uint64_t other = shfl64(key, i);
@@ -151,7 +166,9 @@ struct WideChoice {
       lds_wave_sync();
       if (lane < m && rank < p.k) cand[rank] = e;
       lds_wave_sync();
-      return lane < min(m, p.k) ? cand[lane] : -1;
+      const int got = lane < min(m, p.k) ? cand[lane] : -1;
+      lds_wave_sync();                                   // (the next token's candidates)
+      return got;
     }
     // more candidates than lanes: round by round, the best after the last taken
     uint64_t last = ~0ull;
@@ -159,16 +176,20 @@ struct WideChoice {
     for (int r = 0; r < p.k; ++r) {
       uint64_t best = 0;
       int at = -1;
-#pragma unroll 1
-      for (int e = lane; e < p.E; e += kWave) {
-        if (!in(e)) continue;
-        const uint64_t key = wide_key(c(e));
-        if ((key < last || (key == last && e > last_e)) && key > best) { best = key; at = e; }
-      }
+      each(lane, kWave, p.E, [&](int e, float l, float b) {
+        const uint64_t key = in(e, l, b) ? wide_key(c(l, b)) : 0;
+        if ((key < last || (key == last && e > last_e)) && key > best) {
+          best = key;
+          at = e;
+        }
+      });
       for (int i = 1; i < kWave; i <<= 1) {
         const uint64_t o = shfl64(best, lane ^ i);
         const int oe = __shfl(at, lane ^ i);
-        if (o > best || (o == best && oe < at)) { best = o; at = oe; }
+        if (o > best || (o == best && oe < at)) {
+          best = o;
+          at = oe;
+        }
       }
       last = best;
       last_e = at;
@@ -465,8 +486,9 @@ route_experts_kernel(const LT* __restrict__ logits, const float* __restrict__ bi
     const bool open = __popcll(Tok::ballot(stays && live && lead, lane)) < min(p.topk_group, n_live);
     for (uint64_t tokens = __ballot(open && sub == 0); tokens; tokens &= tokens - 1) {
       const int at = __ffsll(static_cast<unsigned long long>(tokens)) - 1;     // the token's first lane
-      const WideChoice<LT> wide(logits + int64_t(min(t0 + at / W, p.T - 1)) * p.ld, bias, p, lane);
-      const uint64_t stay = wide.groups();
+      const WideChoice<LT> wide(logits + int64_t(min(t0 + at / W, p.T - 1)) * p.ld, bias, p, lane,
+                                __shfl(top, at));
+      const uint64_t stay = wide.groups(lay.shift + (W == 64 ? 0 : 2));
       if (lane / W == at / W) stays = stay >> (ln.g & 63) & 1;
     }
     if (scores && by_logit) {
@@ -547,8 +569,9 @@ route_experts_kernel(const LT* __restrict__ logits, const float* __restrict__ bi
           stay = 0;
           for (int g = 0; g < lay.G; ++g) stay |= (lanes >> (g << lay.shift) & 1) << g;
         }
-        const WideChoice<LT> wide(logits + int64_t(min(t0 + i, p.T - 1)) * p.ld, bias, p, lane);
-        int got = wide.picks(stay, readlane(edge, W * i), readlane(top, W * i), readlane(rden, W * i), s_cand[wave]);
+        const WideChoice<LT> wide(logits + int64_t(min(t0 + i, p.T - 1)) * p.ld, bias, p, lane,
+                                  readlane(top, W * i));
+        int got = wide.picks(stay, readlane(edge, W * i), readlane(rden, W * i), s_cand[wave]);
         // (as many as have a score: with a NaN among the values not always, and then the fp32 picks,
         // which are distinct, stay)
         const bool all = __popcll(__ballot(got >= 0)) == __popcll(__ballot(live) & mine);
@@ -605,15 +628,18 @@ hipError_t launch_slots(const LT* logits, const float* bias, const RouteShape& s
   return hipGetLastError();
 }
 
-// Four tokens a wave from this many tokens on: fewer waves than that leave SIMDs without work, and a
-// wave takes longer.  SHARENOTE
-constexpr int kShareTokens = 4096;
+// Four tokens a wave from this many tokens on for each expert of a lane: before that there are fewer
+// waves than SIMDs want, and one takes longer.  us at 1024 / 2048 / 4096 / 8192 / 16384 tokens, four
+// against one: 64 experts 3.4 / 3.4 / 3.5 / 3.6 / 5.0 against 3.4 / 3.5 / 4.4 / 6.1 / 10.4; 128 with a
+// bias 5.1 / 5.7 / 6.5 / 7.7 / 9.7 against 4.5 / 5.1 / 6.4 / 8.7 / 13.4; 256 in 8 groups 7.7 / 8.8 / 10.1 /
+// 12.9 / 17.7 against 5.7 / 6.8 / 8.9 / 13.3 / 20.6.
+constexpr int kShareTokens = 512;
 
 template <typename LT>
 hipError_t launch_typed(const LT* logits, const float* bias, const RouteShape& s, int32_t* ids,
                         float* w, hipStream_t stream) {
   RouteLayout at = route_layout(s, 16);
-  if (s.T >= kShareTokens && at.C >= 1 && at.C <= 16) {
+  if (at.C >= 1 && at.C <= 16 && s.T >= kShareTokens * std::max(at.C, 4)) {
     if (at.C <= 4) return launch_slots<LT, 16, 4>(logits, bias, s, at, ids, w, stream);
     if (at.C <= 8) return launch_slots<LT, 16, 8>(logits, bias, s, at, ids, w, stream);
     return launch_slots<LT, 16, 16>(logits, bias, s, at, ids, w, stream);

@@ -247,9 +247,9 @@ def check_many(rows, bias, k, **kw):
     """The rows again and again up to a call of many tokens: each time what the oracle says of them,
     to the bit the same wherever in the call they stand."""
     n = rows.shape[0]
-    times = -(-4103 // n)
-    T = 4103 + n                                                     # no multiple of a wave's tokens
-    logits = rows.repeat(times + 1, 1)[:T]
+    T = 8195 + n                                                     # no multiple of a wave's tokens
+    times = -(-T // n)
+    logits = rows.repeat(times, 1)[:T]
     ids, w = mq.moe_route_experts(logits.to(DEV), k, bias=None if bias is None else bias.to(DEV), **kw)
     ids, w = ids.cpu(), w.cpu()
     again = torch.arange(T) % n
@@ -307,7 +307,7 @@ def test_many_tokens_ties_and_nonfinite(scoring):
     for G, tg in ((1, 1), (8, 3)):
         for b in (None, bias):
             check_many(rows, b, 8, scoring=scoring, n_group=G, topk_group=tg, group_best=2)
-            z = rows.repeat(140, 1)
+            z = rows.repeat(270, 1)
             kw = dict(scoring=scoring, n_group=G, topk_group=tg, bias=None if b is None else b.to(DEV))
             clean = mq.moe_route_experts(z.to(DEV), 8, **kw)
             bad = torch.arange(5, z.shape[0], 97)

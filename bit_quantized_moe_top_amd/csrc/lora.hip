@@ -184,28 +184,31 @@ __device__ __forceinline__ uint32_t lds_offset(const uint8_t* p) {
 }
 
 // ------------------------------------------------------------- shared product
-// B x B tiles; kWM x kWN waves of B / kWM rows x B / kWN columns.  The ring holds units: the 128-byte
-// pieces (64 K) of the tile's x rows or of its w rows, in turn.  The kUnits first go out up front.
-// A slot (an x unit and the w unit after it) is multiplied in two halves of 32 K, row block by row
-// block.  A row block's x operand is read anew, for the next half, as soon as its products are
-// issued, so it has a half's time to arrive and needs no second register; the w operands, used by
-// all row blocks, have two sets.  The ring moves on after kOpen row blocks of the second half of
-// slot st: by then its operands are in registers (lgkmcnt(0), which waits for nothing), and this
-// wave's loads of slot st + 1 have landed (all but the kUnits - 4 units issued after them); after
-// the barrier the same holds for every wave, so slot st + 1 can be read, and the next two units
-// take slot st's places.
-template <int B>
+// B x B tiles by G groups of kWM x kWN waves, each wave B / kWM rows x B / kWN columns.  A group has a
+// ring of its own and a G-th of K; the groups' sums meet in LDS.  The ring holds units: the 128-byte
+// pieces (64 K) of the tile's w rows or of its x rows, in turn (w first: it comes from farther and has
+// half a slot more time).  The first kUnits - 1 go out up front.  A slot (a w unit and the x unit after
+// it) is multiplied in two halves of 32 K, row block by row block.  A row block's x operand is read
+// anew, for the next half, as soon as its products are issued, so it has a half's time to arrive and
+// needs no second register; the w operands, used by all row blocks, have two sets.  The ring moves on
+// after kOpen row blocks of the second half of slot st: by then its operands are in registers
+// (lgkmcnt(0), which waits for nothing), and this wave's loads of slot st + 1 have landed (all but those
+// of the kUnits - 4 units issued after them); after the barrier the same holds for every wave, so slot
+// st + 1 can be read, and the next two units take slot st's places.
+template <int B, int G>
 struct Tile {
-  static constexpr int kWM = 2, kWN = B == 256 ? 4 : 2, kWaves = kWM * kWN;
+  static constexpr int kSize = B, kGroups = G;
+  static constexpr int kWM = 2, kWN = B == 256 ? 4 : 2, kGroupWaves = kWM * kWN;
   static constexpr int kRows = B / kWM, kCols = B / kWN, kM = kRows / 16, kN = kCols / 16;
-  static constexpr int kUnitB = B * kRowB, kLoads = B / 8 / kWaves;    // loads of a unit per wave
-  // a CU's 160 KB for one workgroup of 256 x 256, half of them for smaller tiles
+  static constexpr int kEndM = kM / G;                   // row blocks that a wave finishes
+  static constexpr int kUnitB = B * kRowB, kLoads = B / 8 / kGroupWaves;   // loads of a unit per wave
+  // a CU's 160 KB for one workgroup of 256 x 256 or of two groups, half of them for the others
   static constexpr int kUnits = B == 256 ? 5 : 80 * 1024 / kUnitB;
-  static constexpr int kLds = kUnits * kUnitB, kThreads = 64 * kWaves;
+  static constexpr int kRingB = kUnits * kUnitB, kLds = G * kRingB, kThreads = 64 * kGroupWaves * G;
   static_assert(kUnits >= 4, "two slots");
 };
 
-// acc[i][q] += u B_l^T for the wave's rows p0 + 16 i .. and w rows wrow[q] .. + 15, by all waves of
+// acc[i][q] += u B_l^T, i < kEndM, for the rows p0 + 16 i .. and w rows wrow[q] .. + 15, by all waves of
 // the workgroup together.  The tile's u, its parts summed, goes to LDS in two bf16 values, 64
 // ranks of every slice at a time, [row][slice][hi, lo]; B comes from memory.  The product of one adapter is formed by itself and added to its own rows
 // only: what another adapter holds, infinities and NaN too, does not reach them.
@@ -214,7 +217,7 @@ __device__ __forceinline__ void add_adapters(v4f (&acc)[T::kM][T::kN], const Pla
                                              const LoraArgs& args, const LoraShape& s, const float* u,
                                              int u_splits, uint8_t* lds, int m0, int p0,
                                              const int (&wrow)[T::kN], int lane) {
-  constexpr int kM = T::kM, kN = T::kN;
+  constexpr int kM = T::kEndM, kN = T::kN;
   constexpr int kAtOnce = T::kRows == 128 ? 1 : 8 / kN;  // (what the registers hold)
   const int ln = lane & 15, kq = lane >> 4;
   const int pend = min(p0 + 16 * kM, s.M);
@@ -270,24 +273,46 @@ __device__ __forceinline__ void add_adapters(v4f (&acc)[T::kM][T::kN], const Pla
     };
     load_b(first);
     if (k0 > 0) __syncthreads();                         // the ranks before are done with
-    const int rows = min(T::kWM * T::kRows, s.M - m0), quads = kc / 4;
-    for (int i = threadIdx.x; i < rows * s.slices * quads; i += T::kThreads) {
-      const int row = i / (s.slices * quads), c = i - row * (s.slices * quads);
-      const int slice = c / quads, k = k0 + 4 * (c - slice * quads);
-      const float* at = u + int64_t(m0 + row) * cols + slice * s.r + min(k, s.r - 4);
-      v4f v[4], f;
-      f = *reinterpret_cast<const v4f*>(at);
+    // u's elements, four at a time, those of kU quads in flight together
+    constexpr int kU = T::kSize == 256 ? 1 : 2;          // (what the registers hold)
+    const int rows = min(T::kSize, s.M - m0), quads = min(s.r - k0, 64) / 4, pads = kc / 4 - quads;
+    const int n = rows * s.slices * quads;
+    const int64_t u_stride = int64_t(s.M) * cols;
+    const auto place = [&](int i, int per, int& k) {     // quad i of rows x slices x `per` quads
+      const int at = i / per, row = s.slices == 2 ? at >> 1 : at;
+      k = 4 * (i - at * per);
+      return lds + row * row_bytes + (s.slices == 2 ? at & 1 : 0) * 2 * plane;
+    };
+    for (int i0 = threadIdx.x; i0 < n; i0 += kU * T::kThreads) {
+      v4f v[kU][4];
 #pragma unroll
-      for (int j = 1; j < 4; ++j) v[j] = *reinterpret_cast<const v4f*>(at + min(j, u_splits - 1) * int64_t(s.M) * cols);
+      for (int a = 0; a < kU; ++a) {
+        const int i = min(i0 + a * T::kThreads, n - 1), at = i / quads;
+        const float* src = u + int64_t(m0) * cols + int64_t(at) * s.r + k0 + 4 * (i - at * quads);
 #pragma unroll
-      for (int j = 1; j < 4; ++j)
-        if (j < u_splits) f = f + v[j];
-      uint16_t h[4], o[4];
+        for (int j = 0; j < 4; ++j)
+          if (j < u_splits) v[a][j] = *reinterpret_cast<const v4f*>(src + j * u_stride);
+      }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) split2(k < s.r ? f[j] : 0.0f, h[j], o[j]);
-      uint8_t* to = lds + row * row_bytes + slice * 2 * plane + (k - k0) * 2;
-      *reinterpret_cast<uint2*>(to) = make_uint2(h[0] | uint32_t(h[1]) << 16, h[2] | uint32_t(h[3]) << 16);
-      *reinterpret_cast<uint2*>(to + plane) = make_uint2(o[0] | uint32_t(o[1]) << 16, o[2] | uint32_t(o[3]) << 16);
+      for (int a = 0; a < kU; ++a) {
+        if (i0 + a * T::kThreads >= n) break;
+        v4f f = v[a][0];
+#pragma unroll
+        for (int j = 1; j < 4; ++j)
+          if (j < u_splits) f = f + v[a][j];
+        uint16_t h[4], o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) split2(f[j], h[j], o[j]);
+        int k;
+        uint8_t* to = place(i0 + a * T::kThreads, quads, k) + 2 * k;
+        *reinterpret_cast<uint2*>(to) = make_uint2(h[0] | uint32_t(h[1]) << 16, h[2] | uint32_t(h[3]) << 16);
+        *reinterpret_cast<uint2*>(to + plane) = make_uint2(o[0] | uint32_t(o[1]) << 16, o[2] | uint32_t(o[3]) << 16);
+      }
+    }
+    for (int i = threadIdx.x; i < rows * s.slices * pads; i += T::kThreads) {
+      int k;
+      uint8_t* to = place(i, pads, k) + 2 * (k + 4 * quads);
+      *reinterpret_cast<uint2*>(to) = *reinterpret_cast<uint2*>(to + plane) = make_uint2(0u, 0u);
     }
     __syncthreads();
     while (id[0] < s.L) {
@@ -333,19 +358,21 @@ __device__ __forceinline__ void add_adapters(v4f (&acc)[T::kM][T::kN], const Pla
 enum TileMode { kWhole, kParts, kJoin };
 constexpr int kMaxSplits = 4;
 
-template <int EPI, int B, TileMode MODE>
-__global__ void __launch_bounds__(Tile<B>::kThreads, 2)
+template <int EPI, typename T, TileMode MODE>
+__global__ void __launch_bounds__(T::kThreads, 2)
 lora_gemm_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restrict__ parts, int splits,
                  ShrinkGrid sgrid) {
-  using T = Tile<B>;
   static_assert(MODE != kParts || EPI == MOEQ_EPI_NONE, "parts are of W's own columns");
-  constexpr int kM = T::kM, kN = T::kN, kL = T::kLoads;  // kM x kN blocks of 16 x 16 per wave
+  static_assert(MODE == kWhole || T::kGroups == 1, "groups are for whole tiles");
+  constexpr int kM = T::kM, kN = T::kN, kG = T::kGroups;       // kM x kN blocks of 16 x 16 per wave
+  constexpr int B = T::kSize, kL = T::kLoads, kEndM = T::kEndM;
   constexpr bool kSilu = EPI == MOEQ_EPI_SILU_MUL;
   extern __shared__ __align__(16) uint8_t lds[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int ln = lane & 15, kq = lane >> 4, lr = lane >> 3;
-  const int wm = wave / T::kWN, wn = wave % T::kWN;
+  const int group = kG == 1 ? 0 : wave / T::kGroupWaves, gw = kG == 1 ? wave : wave % T::kGroupWaves;
+  const int wm = gw / T::kWN, wn = gw % T::kWN;
   const PlanView pv = plan_view(args.plan, s.L + 1, s.M);
   const int cols = kSilu ? s.N / 2 : s.N;                // output columns, a multiple of 16
   constexpr int kOut = kSilu ? B / 2 : B;                // output columns per workgroup
@@ -382,25 +409,26 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restr
                  : T::kCols * wn + 16 * q;
   };
 
-  // loads: wave v moves rows 8 (kL v + g) + lr, lane's chunk (lane % 8) ^ swz(row)
+  // loads: wave v of a group moves rows 8 (kL v + g) + lr, lane's chunk (lane % 8) ^ swz(row)
   const uint16_t *xsrc[kL], *wsrc[kL];
 #pragma unroll
   for (int g = 0; g < kL; ++g) {
-    const int row = 8 * (kL * wave + g) + lr, c = ((lane & 7) ^ swz(row & 15)) * 8;
+    const int row = 8 * (kL * gw + g) + lr, c = ((lane & 7) ^ swz(row & 15)) * 8;
     xsrc[g] = args.a + int64_t(plan_row(pv, m0 + row, s.M)) * s.ld_a + c;
     wsrc[g] = args.w + int64_t(w_row(row)) * s.K + c;
   }
-  const uint32_t lds0 = lds_offset(lds) + 8 * kL * wave * kRowB;
-  // this launch's slots of 64 K: first, number
+  const uint8_t* const ring = lds + group * T::kRingB;
+  const uint32_t ring0 = lds_offset(ring) + 8 * kL * gw * kRowB;
+  // this group's (or launch's) slots of 64 K: first, number
   const int all_slots = s.K / kSlotK;
-  const int s0 = MODE == kParts ? int(int64_t(all_slots) * split / splits) : 0;
+  const int s0 = MODE == kParts ? int(int64_t(all_slots) * split / splits) : group * (all_slots / kG);
   const int slots = MODE == kParts ? int(int64_t(all_slots) * (split + 1) / splits) - s0
-                                   : MODE == kJoin ? 0 : all_slots;
-  // load g of unit `unit` (2 st: x, 2 st + 1: w of slot st); past the last slot, the last again
+                                   : MODE == kJoin ? 0 : all_slots / kG;
+  // load g of unit `unit` (2 st: w, 2 st + 1: x of slot st); past the last slot, the last again
   const auto issue = [&](bool is_w, int g, int unit) {
     const int k = (s0 + min(unit >> 1, slots - 1)) * kSlotK;
     load_lds<false>((is_w ? wsrc[g] : xsrc[g]) + k,
-                    lds0 + uint32_t(unit % T::kUnits) * T::kUnitB + 8 * g * kRowB);
+                    ring0 + uint32_t(unit % T::kUnits) * T::kUnitB + 8 * g * kRowB);
   };
 
   v4f acc[kM][kN];
@@ -427,13 +455,13 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restr
 #pragma unroll
     for (int unit = 0; unit + 1 < T::kUnits; ++unit)
 #pragma unroll
-      for (int g = 0; g < kL; ++g) issue(unit & 1, g, unit);
+      for (int g = 0; g < kL; ++g) issue(!(unit & 1), g, unit);
     wait_vmem<(T::kUnits - 3) * kL>();
     ring_barrier();
-    int px = 0, pw = 1;                                  // ring places of the slot's units
-    read_w(lds + T::kUnitB, 0);
+    int px = 1, pw = 0;                                  // ring places of the slot's units
+    read_w(ring, 0);
 #pragma unroll
-    for (int i = 0; i < kM; ++i) read_x(i, lds, 0);
+    for (int i = 0; i < kM; ++i) read_x(i, ring + T::kUnitB, 0);
     // unit `unit`'s loads, spread over the rows from `first` on
     const auto issue_row = [&](int i, int first, int unit, bool is_w) {
       const int rows = kM - first, per = (kL + rows - 1) / rows;
@@ -442,12 +470,12 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restr
         if (i >= first && j / per == i - first) issue(is_w, j, unit);
     };
     const auto first_half = [&](int st) {
-      read_w(lds + pw * T::kUnitB, 1);
+      read_w(ring + pw * T::kUnitB, 1);
 #pragma unroll
       for (int i = 0; i < kM; ++i) {
         multiply(i, 0);
-        read_x(i, lds + px * T::kUnitB, 1);
-        issue_row(i, 0, 2 * st + T::kUnits - 1, !(T::kUnits & 1));
+        read_x(i, ring + px * T::kUnitB, 1);
+        issue_row(i, 0, 2 * st + T::kUnits - 1, T::kUnits & 1);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
@@ -460,14 +488,14 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restr
         if (i == kOpen) {
           wait_vmem<(T::kUnits - 4) * kL>();
           ring_barrier();
-          read_w(lds + pw * T::kUnitB, 0);
+          read_w(ring + pw * T::kUnitB, 0);
 #pragma unroll
-          for (int j = 0; j < kOpen; ++j) read_x(j, lds + px * T::kUnitB, 0);
+          for (int j = 0; j < kOpen; ++j) read_x(j, ring + px * T::kUnitB, 0);
         }
         multiply(i, 1);
         if (i >= kOpen) {
-          read_x(i, lds + px * T::kUnitB, 0);
-          issue_row(i, kOpen, 2 * st + T::kUnits, T::kUnits & 1);
+          read_x(i, ring + px * T::kUnitB, 0);
+          issue_row(i, kOpen, 2 * st + T::kUnits, !(T::kUnits & 1));
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -477,23 +505,29 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restr
     for (int i = 0; i < kM; ++i) multiply(i, 1);
     wait_vmem<0>();                                      // the loads past the last slot
   }
-  if (MODE != kJoin && s.K > all_slots * kSlotK && (MODE == kWhole || split == splits - 1)) {
-    ring_barrier();                                      // K past whole slots, zeros after it
-    const int k0 = all_slots * kSlotK;
-    for (int i = tid; i < 2 * B * 8; i += T::kThreads) {
-      const int row = i >> 3, c = i & 7;
-      const uint16_t* src = row < B ? args.a + int64_t(plan_row(pv, m0 + row, s.M)) * s.ld_a
-                                    : args.w + int64_t(w_row(row - B)) * s.K;
-      *reinterpret_cast<uint4*>(lds + row * kRowB + ((c ^ swz(row & 15)) * 16)) = load_k(src, k0 + 8 * c, s.K);
-    }
-    __syncthreads();
+  // K past the groups' slots, zeros after its end: by the first group
+  if (MODE == kWhole || (MODE == kParts && split == splits - 1)) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      read_w(lds + B * kRowB, h);
+    for (int rest = 0; rest < kG; ++rest) {
+      const int k0 = (all_slots / kG * kG + rest) * kSlotK;
+      if (k0 >= s.K) break;
+      ring_barrier();
+      for (int i = tid; i < 2 * B * 8; i += T::kThreads) {
+        const int row = i >> 3, c = i & 7;
+        const uint16_t* src = row < B ? args.a + int64_t(plan_row(pv, m0 + row, s.M)) * s.ld_a
+                                       : args.w + int64_t(w_row(row - B)) * s.K;
+        *reinterpret_cast<uint4*>(lds + row * kRowB + ((c ^ swz(row & 15)) * 16)) = load_k(src, k0 + 8 * c, s.K);
+      }
+      __syncthreads();
+      if (group > 0) continue;
 #pragma unroll
-      for (int i = 0; i < kM; ++i) {
-        read_x(i, lds, h);
-        multiply(i, h);
+      for (int h = 0; h < 2; ++h) {
+        read_w(lds + B * kRowB, h);
+#pragma unroll
+        for (int i = 0; i < kM; ++i) {
+          read_x(i, lds, h);
+          multiply(i, h);
+        }
       }
     }
   }
@@ -506,7 +540,7 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restr
     ocol[q] = n0 + block_row(q) - (up ? B / 2 : 0);
     wrow[q] = min(ocol[q], cols - 16) + (up ? cols : 0);
   }
-  const int p0 = m0 + T::kRows * wm;
+  const int p0 = m0 + T::kRows * wm + 16 * kEndM * group;
   if constexpr (MODE != kWhole) {                        // blocks [split][16 rows][16 w rows][lane]
     const int mblocks = (s.M + 15) / 16, nb = s.N / 16;
     const int64_t stride = int64_t(mblocks) * nb * kWave;
@@ -526,7 +560,8 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restr
 #pragma unroll
         for (int i = 0; i < kM; ++i)
 #pragma unroll
-          for (int q = 0; q < kN; ++q) v[j][i][q] = part(i, q)[min(j, splits - 1) * stride];
+          for (int q = 0; q < kN; ++q)
+            if (j < splits) v[j][i][q] = part(i, q)[j * stride];
 #pragma unroll
       for (int j = 0; j < kMaxSplits; ++j)
 #pragma unroll
@@ -538,9 +573,28 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restr
     if constexpr (MODE == kParts) return;
   }
   ring_barrier();                                        // the ring's LDS is free
-  add_adapters<T>(acc, pv, args, s, u, sgrid.splits, lds, m0, p0, wrow, lane);
+  constexpr int kMeet = kG == 1 ? 0 : B * B * 4 / kG;  // LDS of the groups' exchange
+  if constexpr (kG > 1) {
+    // group g finishes row blocks g kEndM ...: it leaves its sums of the others to their group
+    static_assert(kG == 2, "one other group");
+    v4f* const meet = reinterpret_cast<v4f*>(lds) + lane;
 #pragma unroll
-  for (int i = 0; i < kM; ++i) {
+    for (int i = 0; i < kEndM; ++i)
+#pragma unroll
+      for (int q = 0; q < kN; ++q) {
+        meet[((wave * kEndM + i) * kN + q) * kWave] = group ? acc[i][q] : acc[kEndM + i][q];
+        acc[i][q] = group ? acc[kEndM + i][q] : acc[i][q];
+      }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kEndM; ++i)
+#pragma unroll
+      for (int q = 0; q < kN; ++q)
+        acc[i][q] = acc[i][q] + meet[(((wave ^ T::kGroupWaves) * kEndM + i) * kN + q) * kWave];
+  }
+  add_adapters<T>(acc, pv, args, s, u, sgrid.splits, lds + kMeet, m0, p0, wrow, lane);
+#pragma unroll
+  for (int i = 0; i < kEndM; ++i) {
     // (four rows at a time: the rows' places hoisted together would take the accumulators' registers)
     __builtin_amdgcn_sched_barrier(0);
     int row[4];
@@ -1027,42 +1081,43 @@ int64_t tiles_of(const LoraShape& s, int b) {
 
 constexpr int kJoinBlocks = 1700;
 
-// How more than 64 rows are multiplied: tiles of `tile` rows and columns, K split in `splits` (1:
-// whole tiles, the shrink ahead of them)
+// How more than 64 rows are multiplied: tiles of `size` rows and columns by `groups` groups of waves, K
+// split over `splits` workgroups (1: whole tiles, the shrink ahead of them)
 struct TilePlan {
-  int tile, splits;
+  int size, groups, splits;
 };
 TilePlan tile_plan(const LoraShape& s) {
   const int64_t t256 = tiles_of(s, 256), t128 = tiles_of(s, 128), t64 = tiles_of(s, 64);
-  if (t256 >= 150) return {256, 1};
-  if (t128 >= 350) return {128, 1};
-  if (t64 >= 200 && s.K <= 2048) return {64, 1};
-  if (t128 >= 64) return {128, t128 >= 128 ? 2 : 4};
-  return {64, t64 >= 100 ? 2 : 4};
+  if (t256 >= 150) return {256, 1, 1};
+  if (t128 >= 350) return {128, 1, 1};
+  if (t64 >= 200 && s.K <= 2048) return {64, 1, 1};
+  if (t128 >= 200 && t128 <= 256) return {128, 2, 1};
+  if (t128 >= 64) return {128, 1, t128 >= 128 ? 2 : 4};
+  return {64, 1, t64 >= 100 ? 2 : 4};
 }
 size_t tile_u_bytes(const LoraShape& s) {
   return align256(size_t(shrink_grid(s).splits) * s.M * s.slices * s.r * sizeof(float));
 }
 
-template <int EPI, int B, TileMode MODE>
+template <int EPI, typename T, TileMode MODE>
 hipError_t launch_tile_kernel(const LoraArgs& args, const LoraShape& s, float* u, v4f* parts, int splits,
                               hipStream_t stream) {
-  const auto fn = lora_gemm_kernel<EPI, B, MODE>;
+  const auto fn = lora_gemm_kernel<EPI, T, MODE>;
   const hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void*>(fn),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, Tile<B>::kLds);
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
   if (err != hipSuccess) return err;
   const ShrinkGrid sgrid = shrink_grid(s);
-  const int64_t blocks = MODE == kParts ? sgrid.blocks() + tiles_of(s, B) * splits : tiles_of(s, B);
-  hipLaunchKernelGGL(fn, dim3(unsigned(blocks)), dim3(Tile<B>::kThreads), Tile<B>::kLds, stream, args, s, u,
-                     parts, splits, sgrid);
+  const int64_t tiles = tiles_of(s, T::kSize), blocks = MODE == kParts ? sgrid.blocks() + tiles * splits : tiles;
+  hipLaunchKernelGGL(fn, dim3(unsigned(blocks)), dim3(T::kThreads), T::kLds, stream, args, s, u, parts, splits,
+                     sgrid);
   return hipGetLastError();
 }
-template <int B, TileMode MODE>
+template <typename T, TileMode MODE>
 hipError_t launch_tiles(const LoraArgs& args, const LoraShape& s, float* u, v4f* parts, int splits,
                         hipStream_t stream) {
   return s.epilogue == MOEQ_EPI_SILU_MUL
-             ? launch_tile_kernel<MOEQ_EPI_SILU_MUL, B, MODE>(args, s, u, parts, splits, stream)
-             : launch_tile_kernel<MOEQ_EPI_NONE, B, MODE>(args, s, u, parts, splits, stream);
+             ? launch_tile_kernel<MOEQ_EPI_SILU_MUL, T, MODE>(args, s, u, parts, splits, stream)
+             : launch_tile_kernel<MOEQ_EPI_NONE, T, MODE>(args, s, u, parts, splits, stream);
 }
 
 }  // namespace
@@ -1084,20 +1139,22 @@ hipError_t launch_shared_gemm_lora(const LoraArgs& args, const LoraShape& s, hip
   const TilePlan tp = tile_plan(s);
   hipError_t err;
   if (tp.splits > 1) {
-    err = tp.tile == 128 ? launch_tile_kernel<MOEQ_EPI_NONE, 128, kParts>(args, s, u, parts, tp.splits, stream)
-                         : launch_tile_kernel<MOEQ_EPI_NONE, 64, kParts>(args, s, u, parts, tp.splits, stream);
+    err = tp.size == 128
+              ? launch_tile_kernel<MOEQ_EPI_NONE, Tile<128, 1>, kParts>(args, s, u, parts, tp.splits, stream)
+              : launch_tile_kernel<MOEQ_EPI_NONE, Tile<64, 1>, kParts>(args, s, u, parts, tp.splits, stream);
     if (err != hipSuccess) return err;
     const int64_t join_blocks = int64_t((s.M + 15) / 16) * ((s.epilogue == MOEQ_EPI_SILU_MUL ? s.N / 2 : s.N) / 16);
     return join_blocks <= kJoinBlocks ? launch_join<false>(args, s, u, parts, tp.splits, shrink_grid(s).splits, stream)
-                            : launch_tiles<64, kJoin>(args, s, u, parts, tp.splits, stream);
+                            : launch_tiles<Tile<64, 1>, kJoin>(args, s, u, parts, tp.splits, stream);
   }
   const ShrinkGrid sgrid = shrink_grid(s);
   hipLaunchKernelGGL(lora_shrink_kernel, dim3(unsigned(sgrid.blocks())), dim3(256), 0, stream, args, s, u,
                      sgrid);
   if ((err = hipGetLastError()) != hipSuccess) return err;
-  if (tp.tile == 256) return launch_tiles<256, kWhole>(args, s, u, parts, 1, stream);
-  if (tp.tile == 128) return launch_tiles<128, kWhole>(args, s, u, parts, 1, stream);
-  return launch_tiles<64, kWhole>(args, s, u, parts, 1, stream);
+  if (tp.size == 256) return launch_tiles<Tile<256, 1>, kWhole>(args, s, u, parts, 1, stream);
+  if (tp.size == 64) return launch_tiles<Tile<64, 1>, kWhole>(args, s, u, parts, 1, stream);
+  if (tp.groups == 2) return launch_tiles<Tile<128, 2>, kWhole>(args, s, u, parts, 1, stream);
+  return launch_tiles<Tile<128, 1>, kWhole>(args, s, u, parts, 1, stream);
 }
 
 }  // namespace moeq

@@ -98,6 +98,9 @@ SHAPES = [
     # enough tiles for the larger ones, ragged in every direction
     (260, 8544, 200, 5, 2, 16), (2500, 5408, 136, 4, 2, 24), (1300, 10272, 328, 70, 1, 64),
     (1500, 8736, 48, 3, 2, 8),
+    # about as many tiles of 128 as there are CUs: K in halves, whole, odd, with a rest
+    (300, 8736, 2248, 30, 2, 24), (513, 5920, 2176, 9, 1, 72), (1024, 4096, 2120, 5, 2, 16),
+    (129, 13088, 2112, 40, 2, 136),
 ]
 
 

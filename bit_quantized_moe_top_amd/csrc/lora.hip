@@ -15,6 +15,8 @@
 //
 // The matrix instruction's lane layout: operand lane (row l % 16, kq = l / 16) holds k = 8 kq
 // .. 8 kq + 7; result lane l holds column l % 16 of rows 4 (l / 16) .. 4 (l / 16) + 3.
+#include <algorithm>
+
 #include "common.hpp"
 #include "lora_kernels.hpp"
 
@@ -1016,7 +1018,15 @@ lora_join_kernel(LoraArgs args, LoraShape s, const float* __restrict__ u,
 
 size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
-// Splits of K of the few-row product: about 512 workgroups, two per CU; and of u.
+// Splits of K of the few-row product: 16 slots (1024 K) each, as that is long enough for a ring's start
+// to weigh little and short enough for the parts (8 bytes of traffic an element and split), but at least
+// 128 workgroups and at most 8 splits, which the join loads at once.  us by splits 2 / 3 / 4 / 8:
+// 16 rows x 8192 x 4096 23.4 / 21.3 / 20.5 / 23.0, 64 x 4096 x 4096 24.5 / 21.4 / 19.4 / 20.6, 16 x 2048 x
+// 2048 11.5 / 11.0 / 10.9 / 12.4, 16 x 1024 x 4096 14.6 / 13.0 / 11.6 / 11.0, 16 x 2048 x 8192 22.5 / 18.5 /
+// 17.5 / 16.2, 1 x 16384 x 4096 38.0 / 31.2 / 30.5 / 33.6.  (About 512 workgroups whatever K: 64 x 4096
+// 20.6, 16 x 2048 14.4, 1 x 16384 37.7.)
+// Splits of u: one piece each.  16 splits against 4: 19.2 against 21.1 us for 1 row, 20.6 against 22.2
+// for 16 (x 8192 x 4096).
 struct FewSplit {
   int splits, slots;                                     // slots of 64 K per split
   int u_splits, u_pieces;                                // pieces of 512 K per split of u
@@ -1024,8 +1034,7 @@ struct FewSplit {
 FewSplit few_split(const LoraShape& s) {
   const int ntiles = (s.N + kFewCols - 1) / kFewCols;
   const int slots = s.K / kSlotK > 0 ? s.K / kSlotK : 1;
-  int want = (512 + ntiles - 1) / ntiles;
-  if (want > slots) want = slots;
+  const int want = std::min(slots, std::min(8, std::max(slots / 16, (128 + ntiles - 1) / ntiles)));
   const int per = (slots + want - 1) / want;
   const int pieces = (s.K + kUPiece - 1) / kUPiece;
   const int u_per = (pieces + kUSplits - 1) / kUSplits;
@@ -1131,9 +1140,9 @@ size_t lora_ws_bytes(const LoraShape& s) {
 
 hipError_t launch_shared_gemm_lora(const LoraArgs& args, const LoraShape& s, hipStream_t stream) {
   if (s.M == 0) return hipSuccess;
-  if (s.M <= 16) return launch_few<1>(args, s, stream);
-  if (s.M <= 32) return launch_few<2>(args, s, stream);
-  if (s.M <= kFewRows) return launch_few<4>(args, s, stream);
+  if (s.M <= kFewRows)
+    return s.M <= 16 ? launch_few<1>(args, s, stream)
+                     : s.M <= 32 ? launch_few<2>(args, s, stream) : launch_few<4>(args, s, stream);
   float* u = static_cast<float*>(args.ws);
   v4f* parts = reinterpret_cast<v4f*>(static_cast<uint8_t*>(args.ws) + tile_u_bytes(s));
   const TilePlan tp = tile_plan(s);

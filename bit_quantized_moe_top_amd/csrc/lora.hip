@@ -208,6 +208,7 @@ struct Tile {
   static constexpr int kUnits = B == 256 ? 5 : 80 * 1024 / kUnitB;
   static constexpr int kRingB = kUnits * kUnitB, kLds = G * kRingB, kThreads = 64 * kGroupWaves * G;
   static_assert(kUnits >= 4, "two slots");
+  static_assert((G == 1 ? 0 : B * B * 4) + B * (2 * 2 * 128 + 16) <= kLds, "the exchange, and 64 ranks of u");
 };
 
 // acc[i][q] += u B_l^T, i < kEndM, for the rows p0 + 16 i .. and w rows wrow[q] .. + 15, by all waves of
@@ -575,7 +576,7 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restr
     if constexpr (MODE == kParts) return;
   }
   ring_barrier();                                        // the ring's LDS is free
-  constexpr int kMeet = kG == 1 ? 0 : B * B * 4 / kG;  // LDS of the groups' exchange
+  constexpr int kMeet = kG == 1 ? 0 : B * B * 4;       // LDS of the groups' exchange: half of either's sums
   if constexpr (kG > 1) {
     // group g finishes row blocks g kEndM ...: it leaves its sums of the others to their group
     static_assert(kG == 2, "one other group");

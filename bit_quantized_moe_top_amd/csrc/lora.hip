@@ -5,13 +5,20 @@
 // place; so a block of rows meets few adapters, and a row tile of the shared product reads
 // gathered rows at no extra cost (each lane has its row's address anyway).
 //
-//   lora_shrink_kernel   u of 16 rows of one adapter x 32 columns: four waves share K.  u is
-//                        stored as two bf16 values, hi = bf16(u) and lo = bf16(u - hi), 16
-//                        significant bits, since the second product's matrix instruction
-//                        takes bf16: the error left, 2^-17 of the adapter's part, is small
-//                        against the rounding of out (2^-9).
-//   lora_gemm_kernel     64 x 64 tiles of the shared product, then the adapters' part onto
-//                        the same accumulators, then the epilogue.
+// u is summed in fp32, in parts over shares of K that the reader adds in their order.  For the
+// second product, whose matrix instruction takes bf16, it is split into hi = bf16(u) and lo =
+// bf16(u - hi), 16 significant bits: the error left, 2^-17 of the adapter's part, is small against
+// the rounding of out (2^-9).
+//
+// Up to 64 rows the stream of W bounds the call: lora_few_kernel forms parts of the product over
+// shares of K next to the parts of u, lora_join_kernel adds them, the adapters' product and the
+// epilogue.  More rows: lora_gemm_kernel, in tiles, with the adapters' product onto the tile's
+// accumulators; u by lora_shrink_kernel ahead of it, or, where tiles are too few for the card, K is
+// split over workgroups too and u's parts are formed by the same launch, and a second one joins.
+//
+//   8192 x 4096, 16 rows on 32 adapters of rank 16: 20.3 us, 74 MB read (3.6 TB/s; W's stream alone
+//   10.7 at the 6.3 TB/s that a plain read reaches); 1 row 18.6.  2048 rows: 128 us, 1.08 PFLOP/s
+//   (a library product of these sizes without adapters: 107 us, 1.29).
 //
 // The matrix instruction's lane layout: operand lane (row l % 16, kq = l / 16) holds k = 8 kq
 // .. 8 kq + 7; result lane l holds column l % 16 of rows 4 (l / 16) .. 4 (l / 16) + 3.
@@ -60,7 +67,8 @@ __device__ __forceinline__ int plan_row(const PlanView& pv, int p, int M) {
 // ------------------------------------------------------------------ shrink
 // Parts of u: 32 rows of one adapter x 32 columns x a share of K per workgroup, summed over its
 // four waves, [split][M][columns] in fp32.  A wave takes K in pieces of 128, all of a piece's loads
-// in flight at once: the launch is a chain of memory latencies, not of work.
+// in flight at once: the launch is a chain of memory latencies, not of work (2048 rows x 32 columns,
+// K = 4096: 11.3 us, 17 MB; 777 x 24, K = 1448: 4.7).
 constexpr int kShrinkRows = 32, kShrinkCols = 32;
 constexpr int kShrinkPiece = 128, kShrinkSteps = kShrinkPiece / 32;
 
@@ -213,8 +221,9 @@ struct Tile {
 
 // acc[i][q] += u B_l^T, i < kEndM, for the rows p0 + 16 i .. and w rows wrow[q] .. + 15, by all waves of
 // the workgroup together.  The tile's u, its parts summed, goes to LDS in two bf16 values, 64
-// ranks of every slice at a time, [row][slice][hi, lo]; B comes from memory.  The product of one adapter is formed by itself and added to its own rows
-// only: what another adapter holds, infinities and NaN too, does not reach them.
+// ranks of every slice at a time, [row][slice][hi, lo]; B comes from memory.  The product of one
+// adapter is formed by itself and added to its own rows only: what another adapter holds, infinities
+// and NaN too, does not reach them.
 template <typename T>
 __device__ __forceinline__ void add_adapters(v4f (&acc)[T::kM][T::kN], const PlanView& pv,
                                              const LoraArgs& args, const LoraShape& s, const float* u,
@@ -622,6 +631,9 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restr
 // and applies the epilogue.
 //
 // Parts are stored as the matrix instruction leaves them: 16 bytes per lane, 1 KB per block.
+//
+// Against the tiles, us: 33 rows x 8192 x 4096 25.1 against 27.0, 48 rows 27.3 and 28.8, 64 rows 30.6 and
+// 32.0 (65 rows by tiles 32.5), 64 rows of rank 64 x 4096 x 4096 21.9 and 32.6.
 constexpr int kFewRows = 64, kFewCols = 64;
 
 // u parts: a wave takes 16 rows of one adapter x 16 columns x a piece of 512 K (several, if there
@@ -866,7 +878,7 @@ __host__ __device__ inline int join_u_row(int slices, int r) { return slices * (
 // over: 11.7 us for 64 rows of rank 64 x 4096 columns.)  This launch is latency: everything but B
 // is loaded at once, B as soon as the rows' adapters are known, and the adapters, up to 16, are
 // dealt over the four waves, so that none loads twice (four columns' worth per workgroup and all
-// adapters in each wave: 9.3 us instead of JOIN16 for 16 rows x 8192).
+// adapters in each wave: 9.3 us instead of 4.8 for 16 rows x 8192).
 template <int EPI, bool kFew>
 __global__ void __launch_bounds__(256, kFew ? 2 : 3)
 lora_join_kernel(LoraArgs args, LoraShape s, const float* __restrict__ u,
@@ -1078,7 +1090,9 @@ hipError_t launch_few(const LoraArgs& args, const LoraShape& s, hipStream_t stre
 }
 
 // The grid of the shrink.  Splits of K, at most 4 (add_adapters): for up to 4096 rows, whose blocks
-// of 32 alone would leave CUs idle.
+// of 32 alone would leave CUs idle.  Call, us, by splits 1 / 2 / 4: 777 rows x 1504 x 1448 23.2 / 22.0 /
+// 20.9, 1024 x 8192 x 4096 93.6 / 87.3 / 84.7, 2048 x 8192 x 4096 135.8 / 129.0 / 130.1, 8192 x 4096 x
+// 4096 274.0 / 275.5 / 279.1.
 ShrinkGrid shrink_grid(const LoraShape& s) {
   const int pieces = (s.K + 4 * kShrinkPiece - 1) / (4 * kShrinkPiece);
   return {plan_max_tiles(s.L + 1, s.M) * (MOEQ_TILE_M / kShrinkRows),
@@ -1089,10 +1103,32 @@ int64_t tiles_of(const LoraShape& s, int b) {
   return int64_t((s.M + b - 1) / b) * ((s.N + b - 1) / b);
 }
 
+// Parts are joined by lora_join_kernel up to this many of its workgroups, by 64 x 64 tiles from there
+// on: its workgroups end sooner, but one per 16 rows and columns each read u and the plan (128 rows x
+// 2048, 1024 workgroups: 15.4 us for the call against 19.3; x 4096, 2048: 26.4 against 26.7; x 8192:
+// 40.5 against 35.7).
 constexpr int kJoinBlocks = 1700;
 
 // How more than 64 rows are multiplied: tiles of `size` rows and columns by `groups` groups of waves, K
-// split over `splits` workgroups (1: whole tiles, the shrink ahead of them)
+// split over `splits` workgroups (1: whole tiles, the shrink ahead of them).  The larger the tile the
+// fewer bytes reach LDS per product, and a CU takes in some 45 KB of them a microsecond whatever it has in
+// flight (rows that L2 has wait behind the w rows that it has not); but there are 256 CUs to fill.  So
+// the largest tile that is met often enough, and below that K is divided: between two groups of waves
+// of a workgroup while one tile a CU fills the card in one go, else between workgroups.  us, K = 4096,
+// rows x columns:
+//                 256 whole  128 whole  128, 2 groups  128 / 2  128 / 4  64 whole  64 / 2  64 / 4
+//    2048 x 8192      128        160          182         240      310      330
+//    1280 x 8192      108        125          130         148      187      201
+//    1024 x 8192      105         83           95         116      150      154     202     231
+//     768 x 8192      106         79           93          94      112      120     142     172
+//     512 x 8192      107         62           53          67       78       84      99     127
+//     512 x 4096      105         58           51          39       44       47      53      66
+//     256 x 8192      111         60           55          42       48       51      57      65
+//     128 x 8192      113         62           57          39       36       37      41      44
+//     128 x 4096      112         60           55          33       29       34      27      29
+//     128 x 2048      101         51           40          24       18       26      17      15
+// and 64 whole for short K while it fills the card: 512 x 4096 x 2048 25.5 against 27.2 (128, 2 groups)
+// and 27.6 (128 / 2); x 1024 19.4, 21.3, 21.5.
 struct TilePlan {
   int size, groups, splits;
 };

@@ -21,7 +21,9 @@
 // NS + 6 roundings: |dp| <= 60 u pmax.  The sum with the bias: u |c|.  Twice that, and some: 2^-17 smax +
 // 2^-22 |c| with smax = pmax, or 1/8 for sigmoid.
 //
-// Bound by VALU issue, a token's scores, sorts and k rounds against 4 E bytes read.  BOUNDNOTE
+// Bound by VALU issue, a token's scores, sorts and k rounds against 2 or 4 E bytes read: 16384 tokens of
+// 256 experts in 8 groups 15.3 us (17.8 MB, 1.2 TB/s; some 1340 vector instructions a wave of four tokens),
+// 4096 of 1024 experts with a bias 15.3 us (0.57 TB/s; 1160 a wave of one), 64 of 256 3.6 us, a launch.
 #include <algorithm>
 
 #include "front.hpp"

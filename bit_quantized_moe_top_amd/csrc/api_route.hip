@@ -22,7 +22,7 @@ int moe_route_experts(const void* logits, int logits_dtype, int64_t ld_logits, c
   if (logits_dtype != MOEQ_F32 && logits_dtype != MOEQ_BF16) return MOEQ_ERR_INVALID_ARG;
   if (scoring != MOEQ_SCORE_SOFTMAX && scoring != MOEQ_SCORE_SIGMOID) return MOEQ_ERR_INVALID_ARG;
   if (group_best != 1 && group_best != 2) return MOEQ_ERR_INVALID_ARG;
-  if (E > MOEQ_MAX_EXPERTS || k > MOEQ_MAX_TOPK || n_group > MOEQ_MAX_GROUPS || T >= 1 << 26 ||
+  if (E > MOEQ_MAX_EXPERTS || k > MOEQ_MAX_TOPK || n_group > MOEQ_MAX_GROUPS || T > 1 << 25 ||
       ld_logits > int64_t(1) << 40)
     return MOEQ_ERR_UNSUPPORTED;
   if (E % n_group != 0 || topk_group > n_group || k > topk_group * (E / n_group))

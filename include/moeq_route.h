@@ -47,7 +47,7 @@ extern "C" {
  *   logits   [T, E] fp32 or bf16 (logits_dtype), row stride ld_logits elements
  *   bias     [E] fp32 or NULL
  *   topk_ids [T, k] int32 (out)        topk_w [T, k] fp32 (out)
- * Limits: 0 <= T < 2^26, 1 <= E <= MOEQ_MAX_EXPERTS, 1 <= n_group <= MOEQ_MAX_GROUPS, E %
+ * Limits: 0 <= T <= 2^25, 1 <= E <= MOEQ_MAX_EXPERTS, 1 <= n_group <= MOEQ_MAX_GROUPS, E %
  * n_group == 0, 1 <= topk_group <= n_group, group_best 1 or 2, 1 <= k <=
  * min(MOEQ_MAX_TOPK, topk_group * E / n_group), ld_logits >= E, scale finite;
  * every pointer aligned to its elements; outputs do not overlap inputs.

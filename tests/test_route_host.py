@@ -93,7 +93,7 @@ def test_refusals():
                 dict(bias=at((1 << 20) + 2)), dict(ids=at((1 << 30) + 2)), dict(w=at((1 << 32) + 1)),
                 dict(E=8, topk_group=4, k=5)):                     # four groups of one expert
         assert call(**bad) == INVALID, bad
-    for bad in (dict(E=1025, ld=2000, n_group=1, topk_group=1), dict(k=9), dict(T=1 << 26),
+    for bad in (dict(E=1025, ld=2000, n_group=1, topk_group=1), dict(k=9), dict(T=1 << 26), dict(T=(1 << 26) - 1), dict(T=(1 << 25) + 1),
                 dict(E=130, ld=130, n_group=65, topk_group=4), dict(ld=1 << 41)):
         assert call(**bad) == UNSUPPORTED, bad
     assert call(T=0, logits=N, ids=N, w=N) == OK

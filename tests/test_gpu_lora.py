@@ -321,3 +321,30 @@ def test_a_plan_of_zeros_stays_inside():
     got = c.run(plan=plan)
     assert got.shape == (100, 96)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("M", [3, 70])
+def test_offsets_past_32_bits(M):
+    """Adapters, and rows of a, that lie more than 2^32 bytes (and elements) from their tensor's start:
+    as the same adapters and rows in small tensors."""
+    n, N, K, r = 600, 16384, 16384, 256
+    g = torch.Generator(device=DEV).manual_seed(M)
+    rnd = lambda *s: (torch.randn(*s, generator=g, device=DEV) / 64).to(BF)  # noqa: E731
+    used = [0, 417, n - 1]
+    big_a = torch.empty(n, 1, r, K, dtype=BF, device=DEV)
+    big_b = torch.empty(n, N, r, dtype=BF, device=DEV)
+    assert big_a[-1].data_ptr() - big_a.data_ptr() > 2 ** 32 < big_b[-1].data_ptr() - big_b.data_ptr()
+    for l in used:
+        big_a[l], big_b[l] = rnd(1, r, K), rnd(N, r)
+    w, scale = rnd(N, K), torch.rand(n, generator=g, device=DEV) + 0.5
+    ld = 2 ** 33 // M // 8 * 8
+    a = torch.empty(M * ld, dtype=BF, device=DEV).view(M, ld)[:, :K]
+    a.copy_(rnd(M, K))
+    which = torch.arange(M, device=DEV) % 4
+    ids = torch.tensor(used + [-1], dtype=torch.int32, device=DEV)[which]
+    got = mq.moe_shared_gemm_lora_bf16(a, w, big_a, big_b, scale, mq.moe_adapter_plan(ids, n))
+    few = torch.tensor([0, 1, 2, -1], dtype=torch.int32, device=DEV)[which]
+    ref = mq.moe_shared_gemm_lora_bf16(a.contiguous(), w, big_a[used], big_b[used], scale[used],
+                                       mq.moe_adapter_plan(few, 3))
+    assert got.abs().max() > 0
+    assert torch.equal(got, ref)

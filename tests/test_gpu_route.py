@@ -321,3 +321,15 @@ def test_many_tokens_ties_and_nonfinite(scoring):
             keep = torch.ones(z.shape[0], dtype=torch.bool)
             keep[bad] = False
             assert torch.equal(ids[keep], clean[0].cpu()[keep]) and torch.equal(w[keep], clean[1].cpu()[keep])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_past_32_bits(dtype):
+    """Rows of a matrix wider than 2^31 elements."""
+    ld, E = 2 ** 31 + 8, 96
+    z = torch.empty(3 * ld, dtype=dtype, device=DEV).view(3, ld)[:, :E]
+    rows = torch.randn(3, E, generator=gen(23)).to(dtype)
+    z.copy_(rows)
+    ids, w = mq.moe_route_experts(z, 5, scoring=SIGM)
+    ref = mq.moe_route_experts(rows.to(DEV), 5, scoring=SIGM)
+    assert torch.equal(ids, ref[0]) and torch.equal(w, ref[1])

@@ -59,6 +59,19 @@ __device__ __forceinline__ void split2(float f, uint16_t& hi, uint16_t& lo) {
   lo = to_bf16(fabsf(f) == INFINITY ? 0.0f : f - bf16_to_f32(hi));
 }
 
+// Lane l of a quad holds f of four rows in column l, and leaves with row l of the four columns in bf16:
+// one place and one store of 8 bytes a lane, instead of four and four of 2.  (All lanes take part.)
+__device__ __forceinline__ uint2 quad_rows(const float (&f)[4], int lane) {
+  const uint32_t a = to_bf16(f[0]) | uint32_t(to_bf16(f[1])) << 16, b = to_bf16(f[2]) | uint32_t(to_bf16(f[3])) << 16;
+  // rows of the lane's own parity, from it and its neighbour
+  const uint32_t sel = lane & 1 ? 0x03020706u : 0x05040100u;
+  const uint32_t p0 = __builtin_amdgcn_perm(uint32_t(dpp<kDppQuadSwap1>(0, int(a))), a, sel);
+  const uint32_t p1 = __builtin_amdgcn_perm(uint32_t(dpp<kDppQuadSwap1>(0, int(b))), b, sel);
+  const bool up = lane & 2;
+  const uint32_t other = uint32_t(dpp<kDppQuadSwap2>(0, int(up ? p0 : p1)));
+  return up ? make_uint2(other, p1) : make_uint2(p0, other);
+}
+
 // sorted position -> row, inside [0, M) whatever the plan holds
 __device__ __forceinline__ int plan_row(const PlanView& pv, int p, int M) {
   return min(max(pv.sorted_rows[min(p, M - 1)], 0), M - 1);
@@ -607,19 +620,18 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restr
   add_adapters<T>(acc, pv, args, s, u, sgrid.splits, lds + kMeet, m0, p0, wrow, lane);
 #pragma unroll
   for (int i = 0; i < kEndM; ++i) {
-    // (four rows at a time: the rows' places hoisted together would take the accumulators' registers)
+    // (a row block at a time: the rows' places hoisted together would take the accumulators' registers)
     __builtin_amdgcn_sched_barrier(0);
-    int row[4];
+    const int p = p0 + 16 * i + 4 * kq + (ln & 3);
+    uint16_t* o = args.out + int64_t(plan_row(pv, p, s.M)) * cols + (ln & 12);
 #pragma unroll
-    for (int v = 0; v < 4; ++v) row[v] = plan_row(pv, p0 + 16 * i + 4 * kq + v, s.M);
+    for (int q = 0; q < (kSilu ? kN / 2 : kN); ++q) {
+      float f[4];
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      if (p0 + 16 * i + 4 * kq + v >= s.M) continue;
-      uint16_t* o = args.out + int64_t(row[v]) * cols + ln;
-#pragma unroll
-      for (int q = 0; q < (kSilu ? kN / 2 : kN); ++q)
-        if (ocol[q] < cols)
-          o[ocol[q]] = to_bf16(kSilu ? silu_f32(acc[i][q][v]) * acc[i][q + (kSilu ? kN / 2 : 0)][v] : acc[i][q][v]);
+      for (int v = 0; v < 4; ++v)
+        f[v] = kSilu ? silu_f32(acc[i][q][v]) * acc[i][q + (kSilu ? kN / 2 : 0)][v] : acc[i][q][v];
+      const uint2 four = quad_rows(f, lane);
+      if (p < s.M && ocol[q] < cols) *reinterpret_cast<uint2*>(o + ocol[q]) = four;
     }
   }
 }
@@ -917,9 +929,7 @@ lora_join_kernel(LoraArgs args, LoraShape s, const float* __restrict__ u,
   int urow, uslice, uk;
   const v4f* uat = u_quad(min(tid, 16 * quads - 1), urow, uslice, uk);
   pu.load(uat, u_stride, 0, u_splits);
-  int orow[4];
-#pragma unroll
-  for (int v = 0; v < 4; ++v) orow[v] = plan_row(pv, 16 * mb + 4 * kq + v, s.M);
+  const int out_row = plan_row(pv, 16 * mb + 4 * kq + (ln & 3), s.M);
 
   // lane i < 16: the adapter of row 16 mb + i (-1: none).  Rows are sorted by adapter, so each
   // adapter's rows follow its first one.
@@ -1021,12 +1031,12 @@ lora_join_kernel(LoraArgs args, LoraShape s, const float* __restrict__ u,
 #pragma unroll
   for (int h = 0; h < kHalves; ++h)
     acc[h] = acc[h] + (red[0][h][lane] + (red[1][h][lane] + red[2][h][lane]));
+  float f[4];
 #pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    if (4 * kq + v >= rows) continue;
-    const float f = kSilu ? silu_f32(acc[0][v]) * acc[kHalves - 1][v] : acc[0][v];
-    args.out[int64_t(orow[v]) * cols + cb * 16 + ln] = to_bf16(f);
-  }
+  for (int v = 0; v < 4; ++v) f[v] = kSilu ? silu_f32(acc[0][v]) * acc[kHalves - 1][v] : acc[0][v];
+  const uint2 four = quad_rows(f, lane);
+  if (4 * kq + (ln & 3) < rows)
+    *reinterpret_cast<uint2*>(args.out + int64_t(out_row) * cols + cb * 16 + (ln & 12)) = four;
 }
 
 size_t align256(size_t n) { return (n + 255) & ~size_t(255); }

@@ -15,6 +15,7 @@
 // epilogue.  More rows: lora_gemm_kernel, in tiles, with the adapters' product onto the tile's
 // accumulators; u by lora_shrink_kernel ahead of it, or, where tiles are too few for the card, K is
 // split over workgroups too and u's parts are formed by the same launch, and a second one joins.
+// Small problems of short K: lora_short_kernel, everything in one launch.
 //
 //   8192 x 4096, 16 rows on 32 adapters of rank 16: 20.3 us, 74 MB read (3.6 TB/s; W's stream alone
 //   10.7 at the 6.3 TB/s that a plain read reaches); 1 row 18.6.  2048 rows: 128 us, 1.08 PFLOP/s
@@ -1039,6 +1040,167 @@ lora_join_kernel(LoraArgs args, LoraShape s, const float* __restrict__ u,
     *reinterpret_cast<uint2*>(args.out + int64_t(out_row) * cols + cb * 16 + (ln & 12)) = four;
 }
 
+// ------------------------------------------------------------------ short K
+// Everything in one launch: a workgroup forms 16 rows x 64 output columns, a wave 16 of them (of the gate
+// and the up half with SILU_MUL) over all of K, whose operands go out at once.  u of the 16 rows is formed
+// by every workgroup that needs it, the adapters' pieces of 16 ranks dealt over its waves.
+constexpr int kShortK = 256, kShortItems = 8, kShortGrid = 768;
+
+template <int EPI>
+__global__ void __launch_bounds__(256)
+lora_short_kernel(LoraArgs args, LoraShape s) {
+  extern __shared__ __align__(16) uint8_t us[];          // u as in lora_join_kernel
+  constexpr bool kSilu = EPI == MOEQ_EPI_SILU_MUL;
+  constexpr int kHalves = kSilu ? 2 : 1, KS = kShortK / 32;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int ln = lane & 15, kq = lane >> 4;
+  const int cols = kSilu ? s.N / 2 : s.N;
+  const int n0 = 64 * blockIdx.x + 16 * wave, p0 = 16 * blockIdx.y, rows = min(16, s.M - p0);
+  const PlanView pv = plan_view(args.plan, s.L + 1, s.M);
+  int wrow[kHalves], slice[kHalves];
+  uint4 wv[kHalves][KS];
+#pragma unroll
+  for (int h = 0; h < kHalves; ++h) {
+    wrow[h] = min(n0, cols - 16) + h * cols;
+    slice[h] = s.slices == 2 && wrow[h] >= s.N / 2;
+    const uint16_t* w = args.w + int64_t(wrow[h] + ln) * s.K;
+#pragma unroll
+    for (int j = 0; j < KS; ++j) wv[h][j] = load_in(w, 32 * j + 8 * kq, s.K);
+  }
+  const uint16_t* x = args.a + int64_t(plan_row(pv, p0 + ln, s.M)) * s.ld_a;
+  // lane i < 16: the adapter of row p0 + i (-1: none), the groups that end at or before it
+  int adapter = 0;
+  for (int a0 = 0; a0 < s.L; a0 += kWave) {
+    const int end = pv.offsets[min(a0 + lane + 1, s.L)];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int n = __popcll(__ballot(a0 + lane < s.L && end <= p0 + i));
+      adapter += lane == i ? n : 0;
+    }
+  }
+  if (lane >= rows || adapter >= s.L) adapter = -1;
+  uint4 xv[KS];
+#pragma unroll
+  for (int j = 0; j < KS; ++j) xv[j] = load_in(x, 32 * j + 8 * kq, s.K);
+#pragma unroll
+  for (int j = 0; j < KS; ++j) xv[j] = keep(xv[j], 32 * j + 8 * kq < s.K);
+  // rows are sorted by adapter: those of one follow its first, up to the next first
+  const uint32_t with = uint32_t(__ballot(adapter >= 0));
+  const int before = __shfl_up(adapter, 1);
+  const uint32_t firsts = uint32_t(__ballot(adapter >= 0 && (lane == 0 || before != adapter)));
+  const auto rows_of = [&](uint32_t left) {              // ... of the lowest bit of `left`
+    const uint32_t rest = left & (left - 1);
+    return with & ~((left & -left) - 1) & (rest ? (rest & -rest) - 1 : ~0u);
+  };
+  const int r32 = (s.r + 31) / 32 * 32, row_bytes = join_u_row(s.slices, s.r), ucols = s.slices * s.r;
+  for (int i = tid; i < 16 * s.slices * (r32 - s.r); i += 256) {         // ranks past r
+    const int at = i / (r32 - s.r), row = s.slices == 2 ? at >> 1 : at, k = s.r + i - at * (r32 - s.r);
+    uint8_t* to = us + row * row_bytes + ((s.slices == 2 ? at & 1 : 0) * 2 * r32 + k) * 2;
+    *reinterpret_cast<uint16_t*>(to) = *reinterpret_cast<uint16_t*>(to + 2 * r32) = 0;
+  }
+  const int blocks = (ucols + 15) / 16;
+  int at = 0;
+  for (uint32_t left = firsts; left; left &= left - 1) {
+    const int l = readlane(adapter, __ffs(left) - 1);
+    const uint32_t mine = rows_of(left);
+    for (int cb = 0; cb < blocks; ++cb, ++at) {
+      if ((at & 3) != wave) continue;
+      const int col = 16 * cb + ln;
+      const uint16_t* arow = args.lora_a + (int64_t(l) * ucols + min(col, ucols - 1)) * s.K;
+      uint4 av[KS];
+#pragma unroll
+      for (int j = 0; j < KS; ++j) av[j] = load_in(arow, 32 * j + 8 * kq, s.K);
+      const float scale = args.scale[l];
+      v4f d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < KS; ++j)
+        if (32 * j < s.K) d = mfma(xv[j], keep(av[j], 32 * j + 8 * kq < s.K), d);
+      const int sl = col >= s.r ? 1 : 0;
+      uint8_t* to = us + (sl * 2 * r32 + col - sl * s.r) * 2;
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        if (col < ucols && mine >> (4 * kq + v) & 1) {
+          uint16_t hi, lo;
+          split2(d[v] * scale, hi, lo);
+          *reinterpret_cast<uint16_t*>(to + (4 * kq + v) * row_bytes) = hi;
+          *reinterpret_cast<uint16_t*>(to + (4 * kq + v) * row_bytes + 2 * r32) = lo;
+        }
+    }
+  }
+  v4f acc[kHalves];
+#pragma unroll
+  for (int h = 0; h < kHalves; ++h) {
+    acc[h] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < KS; ++j)
+      if (32 * j < s.K) acc[h] = mfma(xv[j], keep(wv[h][j], 32 * j + 8 * kq < s.K), acc[h]);
+  }
+  __syncthreads();                                       // u is in LDS
+  if (n0 >= cols) return;
+  for (uint32_t left = firsts; left;) {                  // four adapters' B at a time
+    constexpr int kOnce = 4;
+    uint32_t of[kOnce];
+    int id[kOnce];
+#pragma unroll
+    for (int a = 0; a < kOnce; ++a) {
+      of[a] = left ? rows_of(left) : 0u;
+      id[a] = left ? readlane(adapter, __ffs(left) - 1) : 0;
+      left &= left - 1;
+    }
+    for (int k0 = 0; k0 < s.r; k0 += 32) {
+      uint4 b[kOnce][kHalves];
+#pragma unroll
+      for (int a = 0; a < kOnce; ++a)
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
+          b[a][h] = load_in(args.lora_b + (int64_t(id[a]) * s.N + wrow[h] + ln) * s.r, k0 + 8 * kq, s.r);
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) {
+        const uint8_t* from = us + ln * row_bytes + (slice[h] * 2 * r32 + k0 + 8 * kq) * 2;
+        const uint4 hi = *reinterpret_cast<const uint4*>(from), lo = *reinterpret_cast<const uint4*>(from + 2 * r32);
+#pragma unroll
+        for (int a = 0; a < kOnce; ++a) {
+          if (of[a] == 0) continue;
+          const uint4 bv = keep(b[a][h], k0 + 8 * kq < s.r);
+          v4f d = mfma(hi, bv, v4f{0.f, 0.f, 0.f, 0.f});
+          d = mfma(lo, bv, d);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[h][v] += of[a] >> (4 * kq + v) & 1 ? d[v] : 0.0f;
+        }
+      }
+    }
+  }
+  float f[4];
+#pragma unroll
+  for (int v = 0; v < 4; ++v) f[v] = kSilu ? silu_f32(acc[0][v]) * acc[kHalves - 1][v] : acc[0][v];
+  const uint2 four = quad_rows(f, lane);
+  const int p = 4 * kq + (ln & 3);
+  if (p < rows)
+    *reinterpret_cast<uint2*>(args.out + int64_t(plan_row(pv, p0 + p, s.M)) * cols + n0 + (ln & 12)) = four;
+}
+
+// One launch for K up to 256, if a workgroup has at most 8 pieces of 16 ranks to form (two a wave; an
+// adapter per row at most) and the workgroups, which all read x and W, fit the card in one go.  us in one
+// launch against two: 3 rows x 192 x 256 5.7 and 7.2 (with the host's time 8.6 and 11.8), 64 x 4096 x 256
+// 7.6 and 12.6, 512 x 1024 x 256 8.3 and 12.5, 1024 x 512 x 64 8.1 and 11.9; 16 rows x 1024 x 256 with 4 / 8 /
+// 16 pieces 7.1 / 8.3 / 10.7 against 9.1 / 9.2 / 9.3, 16 x 1024 x 64 with 32 15.0 and 11.6; 768 workgroups
+// (192 x 4096 x 256) 11.3 and 15.0, 1024 (256 x 4096 x 128) 15.4 and 9.7.  K = 512 with operands of all of K
+// in flight (16 x 1024): 10.4 and 9.2.
+bool is_short(const LoraShape& s) {
+  const int64_t cols = s.epilogue == MOEQ_EPI_SILU_MUL ? s.N / 2 : s.N;
+  return s.K <= kShortK && std::min(s.L, std::min(s.M, 16)) * ((s.slices * s.r + 15) / 16) <= kShortItems &&
+         int64_t((s.M + 15) / 16) * ((cols + 63) / 64) <= kShortGrid;
+}
+hipError_t launch_short(const LoraArgs& args, const LoraShape& s, hipStream_t stream) {
+  const bool silu = s.epilogue == MOEQ_EPI_SILU_MUL;
+  const int cols = silu ? s.N / 2 : s.N;
+  const auto fn = silu ? lora_short_kernel<MOEQ_EPI_SILU_MUL> : lora_short_kernel<MOEQ_EPI_NONE>;
+  hipLaunchKernelGGL(fn, dim3(unsigned((cols + 63) / 64), unsigned((s.M + 15) / 16)), dim3(256),
+                     unsigned(16 * join_u_row(s.slices, s.r)), stream, args, s);
+  return hipGetLastError();
+}
+
 size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
 // Splits of K of the few-row product: 16 slots (1024 K) each, as that is long enough for a ring's start
@@ -1187,6 +1349,7 @@ size_t lora_ws_bytes(const LoraShape& s) {
 
 hipError_t launch_shared_gemm_lora(const LoraArgs& args, const LoraShape& s, hipStream_t stream) {
   if (s.M == 0) return hipSuccess;
+  if (is_short(s)) return launch_short(args, s, stream);
   if (s.M <= kFewRows)
     return s.M <= 16 ? launch_few<1>(args, s, stream)
                      : s.M <= 32 ? launch_few<2>(args, s, stream) : launch_few<4>(args, s, stream);

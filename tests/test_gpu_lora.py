@@ -101,6 +101,15 @@ SHAPES = [
     # about as many tiles of 128 as there are CUs: K in halves, whole, odd, with a rest
     (300, 8736, 2248, 30, 2, 24), (513, 5920, 2176, 9, 1, 72), (1024, 4096, 2120, 5, 2, 16),
     (129, 13088, 2112, 40, 2, 136),
+    # K past what one launch takes, and off its steps: few rows, and tiles of every size
+    (1, 32, 520, 4, 2, 16), (2, 64, 552, 3, 2, 32), (15, 96, 584, 5, 2, 24), (17, 160, 616, 40, 1, 40),
+    (63, 2080, 840, 8, 2, 8), (64, 128, 1016, 3, 1, 16), (130, 96, 712, 7, 2, 64), (300, 528, 648, 20, 1, 256),
+    (260, 8544, 584, 5, 2, 16), (1500, 8736, 520, 3, 2, 8),
+    # one launch: K at, below and above 32 and 256; an adapter in every row, and one; pieces of ranks
+    # that two slices share; rows and columns off its blocks
+    (16, 64, 256, 16, 1, 8), (33, 96, 248, 3, 2, 16), (5, 1040, 256, 5, 1, 16), (200, 336, 200, 8, 1, 8),
+    (90, 64, 24, 1, 1, 128), (1, 16, 256, 70, 1, 128), (700, 160, 32, 2, 2, 24), (31, 48, 8, 8, 1, 16),
+    (2, 4096, 128, 900, 2, 32), (16, 32, 264, 2, 2, 8),
 ]
 
 
@@ -114,11 +123,13 @@ def test_shapes(M, N, K, n, S, r, how):
         assert torch.equal(got, c.run(epilogue))                 # the same bits again
 
 
-def test_integers_are_exact():
+@pytest.mark.parametrize("M,K", [(70, 136), (70, 520), (20, 520)])
+def test_integers_are_exact(M, K):
     """Small integers: every sum is exact in fp32, u in two bf16 parts, and the result in bf16."""
     g = gen(3)
-    c = Case(70, 96, 136, 5, 1, 16)
+    c = Case(M, 96, K, 5, 1, 16)
     c.x = torch.randint(-2, 3, c.x.shape, generator=g).to(BF)
+    c.x[:, 128:K - 8] = 0
     c.w = torch.randint(-1, 2, c.w.shape, generator=g).to(BF)
     c.a = torch.randint(-1, 2, c.a.shape, generator=g).to(BF)
     c.b = (torch.rand(c.b.shape, generator=g) < 0.1).to(BF)
@@ -129,10 +140,11 @@ def test_integers_are_exact():
     np.testing.assert_array_equal(to_np(c.run())[exact], v[exact])
 
 
-def test_u_keeps_sixteen_bits():
+@pytest.mark.parametrize("M,K", [(20, 64), (20, 584), (200, 584)])
+def test_u_keeps_sixteen_bits(M, K):
     """Two ranks whose parts cancel but for 2^-12 of themselves: a u in one bf16 value (2^-9) would
     lose what is left."""
-    M, N, K, r = 20, 32, 64, 8
+    N, r = 32, 8
     c = Case(M, N, K, 1, 1, r, how="one")
     g = gen(4)
     c.x = (torch.rand(M, K, generator=g) + 0.5).to(BF)
@@ -148,9 +160,10 @@ def test_u_keeps_sixteen_bits():
     assert (np.abs(got - 2.0 ** -12) <= 2.0 ** -17 * (2 * x0 + 2.0 ** -12) + 2.0 ** -20).all()
 
 
-def test_u_up_to_the_largest_fp32():
+@pytest.mark.parametrize("M,K", [(18, 16), (18, 520), (90, 520)])
+def test_u_up_to_the_largest_fp32(M, K):
     """u = 1.9989 * 2^127, finite in fp32 and past bf16's largest value, of either sign."""
-    M, N, K = 18, 32, 16
+    N = 32
     c = Case(M, N, K, 1, 1, 8, how="one")
     c.x = torch.zeros(M, K, dtype=BF)
     c.x[:, 0] = 1 - 2 * (torch.arange(M) % 2)
@@ -169,7 +182,8 @@ def test_u_up_to_the_largest_fp32():
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
-@pytest.mark.parametrize("M,N,K,how", [(40, 96, 136, "mixed"), (200, 64, 64, "runs"), (12, 512, 1024, "each")])
+@pytest.mark.parametrize("M,N,K,how", [(40, 96, 136, "mixed"), (200, 64, 64, "runs"), (12, 512, 1024, "each"),
+                                         (40, 96, 520, "mixed"), (200, 64, 520, "runs"), (700, 2144, 520, "runs")])
 def test_a_broken_adapter_or_row_spoils_only_its_own(M, N, K, how, bad):
     c = Case(M, N, K, 6, 1, 16, how)
     for epilogue in (mq.EPI_NONE, mq.EPI_SILU_MUL):
@@ -192,7 +206,8 @@ def test_a_broken_adapter_or_row_spoils_only_its_own(M, N, K, how, bad):
                 assert not torch.isfinite(got[own.to(DEV)]).all(), part
 
 
-@pytest.mark.parametrize("M,N,K,pad", [(1, 64, 72, 8), (5, 64, 72, 8), (100, 160, 1024, 56), (300, 96, 136, 24)])
+@pytest.mark.parametrize("M,N,K,pad", [(1, 64, 72, 8), (5, 64, 72, 8), (100, 160, 1024, 56), (300, 96, 136, 24),
+                                         (5, 64, 584, 8), (300, 96, 328, 24)])
 def test_rows_of_a_wider_matrix_and_bytes_around(M, N, K, pad):
     c = Case(M, N, K, 4, 2, 8)
     wide = torch.full((M, K + pad), float("nan"), dtype=BF)

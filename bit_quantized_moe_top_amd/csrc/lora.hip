@@ -18,8 +18,8 @@
 // Small problems of short K: lora_short_kernel, everything in one launch.
 //
 //   8192 x 4096, 16 rows on 32 adapters of rank 16: 20.3 us, 74 MB read (3.6 TB/s; W's stream alone
-//   10.7 at the 6.3 TB/s that a plain read reaches); 1 row 18.6.  2048 rows: 122 to 133 us from card to card, 1.04 to 1.14 PFLOP/s
-//   (a library product of these sizes without adapters: 107 us, 1.29).
+//   10.7 at the 6.3 TB/s that a plain read reaches); 1 row 18.6.  2048 rows: 122 to 133 us from card to
+//   card, 1.04 to 1.14 PFLOP/s (a library product of these sizes without adapters: 107 us, 1.29).
 //
 // The matrix instruction's lane layout: operand lane (row l % 16, kq = l / 16) holds k = 8 kq
 // .. 8 kq + 7; result lane l holds column l % 16 of rows 4 (l / 16) .. 4 (l / 16) + 3.

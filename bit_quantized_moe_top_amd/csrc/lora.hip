@@ -891,9 +891,11 @@ __host__ __device__ inline int join_u_row(int slices, int r) { return slices * (
 // over: 11.7 us for 64 rows of rank 64 x 4096 columns.)  This launch is latency: everything but B
 // is loaded at once, B as soon as the rows' adapters are known, and the adapters, up to 16, are
 // dealt over the four waves, so that none loads twice (four columns' worth per workgroup and all
-// adapters in each wave: 9.3 us instead of 4.8 for 16 rows x 8192).
-template <int EPI, bool kFew>
-__global__ void __launch_bounds__(256, kFew ? 2 : 3)
+// adapters in each wave: 9.3 us instead of 4.8 for 16 rows x 8192).  So are the parts, which keeps
+// registers at four workgroups a CU up to rank 32: 64 rows of gate/up 8192 are then one go (the call
+// 27.5 us; all parts in the first wave, two workgroups a CU, 30.3).
+template <int EPI, bool kFew, int kSteps>                // kSteps: steps of 32 ranks at a time
+__global__ void __launch_bounds__(256, kSteps == 1 ? 4 : 3)
 lora_join_kernel(LoraArgs args, LoraShape s, const float* __restrict__ u,
                  const v4f* __restrict__ parts, int splits, int u_splits) {
   extern __shared__ __align__(16) uint8_t us[];          // u: [16 rows][slice][hi, lo][r to 32]
@@ -911,11 +913,14 @@ lora_join_kernel(LoraArgs args, LoraShape s, const float* __restrict__ u,
   const int rows = min(16, s.M - 16 * mb);
   const int64_t part_stride = int64_t(mblocks) * nb * kWave, u_stride = int64_t(s.M) * s.slices * s.r / 4;
   const v4f* pat[kHalves];
-  PartSum<kFew ? 8 : kMaxSplits> ps[kHalves], pu;        // (more than 64 rows: 4 splits at most)
+  // the product's parts are dealt over the waves too: up to 8 of up to 64 rows, else up to 4
+  PartSum<kFew ? 2 : 1> ps[kHalves];
+  const int n_parts = (splits - wave + 3) / 4;
+  PartSum<kFew ? 8 : kMaxSplits> pu;
 #pragma unroll
   for (int h = 0; h < kHalves; ++h) {
-    pat[h] = parts + (int64_t(mb) * nb + cb + h * cblocks) * kWave + lane;
-    if (wave == 0) ps[h].load(pat[h], part_stride, 0, splits);
+    pat[h] = parts + wave * part_stride + (int64_t(mb) * nb + cb + h * cblocks) * kWave + lane;
+    if (n_parts > 0) ps[h].load(pat[h], 4 * part_stride, 0, n_parts);
   }
   // u's elements, four at a time: thread i takes quads i, i + 256, ... of [row][slice][r to 32]
   const int r32 = (s.r + 31) / 32 * 32, quads = s.slices * (r32 / 4), row_bytes = join_u_row(s.slices, s.r);
@@ -961,7 +966,7 @@ lora_join_kernel(LoraArgs args, LoraShape s, const float* __restrict__ u,
     firsts = rest;
     for (int j = 0; j < 3; ++j) firsts &= firsts - 1;
   }
-  uint4 b[kMine][2][kHalves];
+  uint4 b[kMine][kSteps][kHalves];
   auto load_b = [&](int k0) {
 #pragma unroll
     for (int a = 0; a < kMine; ++a)
@@ -969,14 +974,14 @@ lora_join_kernel(LoraArgs args, LoraShape s, const float* __restrict__ u,
       for (int h = 0; h < kHalves; ++h) {
         const uint16_t* at = args.lora_b + (int64_t(id[a]) * s.N + wrow[h] + ln) * s.r;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) b[a][j][h] = load16(at + min(k0 + 32 * j + 8 * kq, s.r - 8));
+        for (int j = 0; j < kSteps; ++j) b[a][j][h] = load16(at + min(k0 + 32 * j + 8 * kq, s.r - 8));
       }
   };
   if (n_mine > 0) load_b(0);
   v4f acc[kHalves];
 #pragma unroll
   for (int h = 0; h < kHalves; ++h)
-    acc[h] = wave == 0 ? ps[h].sum(pat[h], part_stride, splits) : v4f{0.f, 0.f, 0.f, 0.f};
+    acc[h] = n_parts > 0 ? ps[h].sum(pat[h], 4 * part_stride, n_parts) : v4f{0.f, 0.f, 0.f, 0.f};
   for (int i = tid; i < 16 * quads; i += 256) {
     if (i >= 256) {
       uat = u_quad(i, urow, uslice, uk);
@@ -992,10 +997,10 @@ lora_join_kernel(LoraArgs args, LoraShape s, const float* __restrict__ u,
         make_uint2(lo[0] | uint32_t(lo[1]) << 16, lo[2] | uint32_t(lo[3]) << 16);
   }
   __syncthreads();                                       // u is in LDS
-  for (int k0 = 0; n_mine > 0 && k0 < s.r; k0 += 64) {
-    uint4 hi[2][kHalves], lo[2][kHalves];
+  for (int k0 = 0; n_mine > 0 && k0 < s.r; k0 += 32 * kSteps) {
+    uint4 hi[kSteps][kHalves], lo[kSteps][kHalves];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < kSteps; ++j)
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) {
         const int k = min(k0 + 32 * j, r32 - 32) + 8 * kq;   // (a step past r is not used)
@@ -1010,7 +1015,7 @@ lora_join_kernel(LoraArgs args, LoraShape s, const float* __restrict__ u,
       for (int h = 0; h < kHalves; ++h) {
         v4f d = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < kSteps; ++j) {
           const bool in = k0 + 32 * j + 8 * kq < s.r;
           const uint4 w = b[a][j][h];
           const uint4 bv = make_uint4(in ? w.x : 0u, in ? w.y : 0u, in ? w.z : 0u, in ? w.w : 0u);
@@ -1237,7 +1242,8 @@ hipError_t launch_join(const LoraArgs& args, const LoraShape& s, const float* u,
                        int u_splits, hipStream_t stream) {
   const bool silu = s.epilogue == MOEQ_EPI_SILU_MUL;
   const int cblocks = (silu ? s.N / 2 : s.N) / 16;
-  const auto join = silu ? lora_join_kernel<MOEQ_EPI_SILU_MUL, kFew> : lora_join_kernel<MOEQ_EPI_NONE, kFew>;
+  const auto join = s.r <= 32 ? (silu ? lora_join_kernel<MOEQ_EPI_SILU_MUL, kFew, 1> : lora_join_kernel<MOEQ_EPI_NONE, kFew, 1>)
+                              : (silu ? lora_join_kernel<MOEQ_EPI_SILU_MUL, kFew, 2> : lora_join_kernel<MOEQ_EPI_NONE, kFew, 2>);
   hipLaunchKernelGGL(join, dim3(unsigned(cblocks), unsigned((s.M + 15) / 16)), dim3(256),
                      unsigned(16 * join_u_row(s.slices, s.r)), stream, args, s, u, parts, splits, u_splits);
   return hipGetLastError();
@@ -1277,9 +1283,9 @@ int64_t tiles_of(const LoraShape& s, int b) {
 
 // Parts are joined by lora_join_kernel up to this many of its workgroups, by 64 x 64 tiles from there
 // on: its workgroups end sooner, but one per 16 rows and columns each read u and the plan (128 rows x
-// 2048, 1024 workgroups: 15.4 us for the call against 19.3; x 4096, 2048: 26.4 against 26.7; x 8192:
-// 40.5 against 35.7).
-constexpr int kJoinBlocks = 1700;
+// 2048, 1024 workgroups: 15.7 us for the call against 20.9; x 4096, 2048: 26.7 against 29.4; 192 rows of
+// gate/up 8192: 45.9 against 43.0; 256 rows, 4096: 51.7 against 44.9).
+constexpr int kJoinBlocks = 2400;
 
 // How more than 64 rows are multiplied: tiles of `size` rows and columns by `groups` groups of waves, K
 // split over `splits` workgroups (1: whole tiles, the shrink ahead of them).  The larger the tile the

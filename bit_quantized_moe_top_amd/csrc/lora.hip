@@ -17,8 +17,8 @@
 // split over workgroups too and u's parts are formed by the same launch, and a second one joins.
 // Small problems of short K: lora_short_kernel, everything in one launch.
 //
-//   8192 x 4096, 16 rows on 32 adapters of rank 16: 20.3 us, 74 MB read (3.6 TB/s; W's stream alone
-//   10.7 at the 6.3 TB/s that a plain read reaches); 1 row 18.6.  2048 rows: 122 to 133 us from card to
+//   8192 x 4096, 16 rows on 32 adapters of rank 16: 19.5 us, 74 MB read (3.8 TB/s; W's stream alone
+//   10.7 at the 6.3 TB/s that a plain read reaches); 1 row 18.1.  2048 rows: 122 to 133 us from card to
 //   card, 1.04 to 1.14 PFLOP/s (a library product of these sizes without adapters: 107 us, 1.29).
 //
 // The matrix instruction's lane layout: operand lane (row l % 16, kq = l / 16) holds k = 8 kq
@@ -646,7 +646,7 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restr
 // Parts are stored as the matrix instruction leaves them: 16 bytes per lane, 1 KB per block.
 //
 // Against the tiles, us: 33 rows x 8192 x 4096 25.1 against 27.0, 48 rows 27.3 and 28.8, 64 rows 30.6 and
-// 32.0 (65 rows by tiles 32.5), 64 rows of rank 64 x 4096 x 4096 21.9 and 32.6.
+// 32.0, 64 rows of rank 64 x 4096 x 4096 21.9 and 32.6.
 constexpr int kFewRows = 64, kFewCols = 64;
 
 // u parts: a wave takes 16 rows of one adapter x 16 columns x a piece of 512 K (several, if there

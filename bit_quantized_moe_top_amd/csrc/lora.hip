@@ -645,8 +645,8 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restr
 //
 // Parts are stored as the matrix instruction leaves them: 16 bytes per lane, 1 KB per block.
 //
-// Against the tiles, us: 33 rows x 8192 x 4096 25.1 against 27.0, 48 rows 27.3 and 28.8, 64 rows 30.6 and
-// 32.0, 64 rows of rank 64 x 4096 x 4096 21.9 and 32.6.
+// Against the tiles, us: 33 rows x 8192 x 4096 22.9 against 26.9, 48 rows 24.6 and 28.0, 64 rows 27.6 and
+// 29.9, 64 rows of rank 64 x 4096 x 4096 23.4 and 32.5.
 constexpr int kFewRows = 64, kFewCols = 64;
 
 // u parts: a wave takes 16 rows of one adapter x 16 columns x a piece of 512 K (several, if there
@@ -1211,11 +1211,10 @@ size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 // Splits of K of the few-row product: 16 slots (1024 K) each, as that is long enough for a ring's start
 // to weigh little and short enough for the parts (8 bytes of traffic an element and split), but at least
 // 128 workgroups and at most 8 splits, which the join loads at once.  us by splits 2 / 3 / 4 / 8:
-// 16 rows x 8192 x 4096 23.4 / 21.3 / 20.5 / 23.0, 64 x 4096 x 4096 24.5 / 21.4 / 19.4 / 20.6, 16 x 2048 x
-// 2048 11.5 / 11.0 / 10.9 / 12.4, 16 x 1024 x 4096 14.6 / 13.0 / 11.6 / 11.0, 16 x 2048 x 8192 22.5 / 18.5 /
-// 17.5 / 16.2, 1 x 16384 x 4096 38.0 / 31.2 / 30.5 / 33.6.  (About 512 workgroups whatever K: 64 x 4096
-// 20.6, 16 x 2048 14.4, 1 x 16384 37.7.)
-// Splits of u: one piece each.  16 splits against 4: 19.2 against 21.1 us for 1 row, 20.6 against 22.2
+// 16 rows x 8192 x 4096 22.9 / 20.7 / 20.0 / 22.5, 64 x 4096 x 4096 23.5 / 20.6 / 18.4 / 20.0, 16 x 2048 x
+// 2048 10.8 / 10.4 / 10.1 / 11.7, 16 x 1024 x 4096 13.8 / 12.4 / 10.9 / 10.2, 16 x 2048 x 8192 21.8 / 18.0 /
+// 16.8 / 15.7, 1 x 16384 x 4096 37.5 / 30.7 / 29.9 / 33.5.
+// Splits of u: one piece each.  16 splits against 4: 18.8 against 20.8 us for 1 row, 20.0 against 21.6
 // for 16 (x 8192 x 4096).
 struct FewSplit {
   int splits, slots;                                     // slots of 64 K per split
@@ -1303,8 +1302,8 @@ constexpr int kJoinBlocks = 2400;
 //     512 x 4096      105         58           51          39       44       47      53      66
 //     256 x 8192      111         60           55          42       48       51      57      65
 //     128 x 8192      113         62           57          39       36       37      41      44
-//     128 x 4096      112         60           55          33       29       34      27      29
-//     128 x 2048      101         51           40          24       18       26      17      15
+//     128 x 4096      112         60           55          32       27       34      26      28
+//     128 x 2048      101         51           40          24       17       26      17      15
 // and 64 whole for short K while it fills the card: 512 x 4096 x 2048 25.5 against 27.2 (128, 2 groups)
 // and 27.6 (128 / 2); x 1024 19.4, 21.3, 21.5.
 struct TilePlan {

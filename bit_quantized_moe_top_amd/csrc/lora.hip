@@ -24,6 +24,7 @@
 // The matrix instruction's lane layout: operand lane (row l % 16, kq = l / 16) holds k = 8 kq
 // .. 8 kq + 7; result lane l holds column l % 16 of rows 4 (l / 16) .. 4 (l / 16) + 3.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.hpp"
 #include "lora_kernels.hpp"
@@ -244,7 +245,6 @@ __device__ __forceinline__ void add_adapters(v4f (&acc)[T::kM][T::kN], const Pla
                                              int u_splits, uint8_t* lds, int m0, int p0,
                                              const int (&wrow)[T::kN], int lane) {
   constexpr int kM = T::kEndM, kN = T::kN;
-  constexpr int kAtOnce = T::kRows == 128 ? 1 : 8 / kN;  // (what the registers hold)
   const int ln = lane & 15, kq = lane >> 4;
   const int pend = min(p0 + 16 * kM, s.M);
   // the adapters of the wave's rows: the first, and the offsets of 64 groups from there
@@ -270,16 +270,17 @@ __device__ __forceinline__ void add_adapters(v4f (&acc)[T::kM][T::kN], const Pla
     return s.L;
   };
   const int cols = s.slices * s.r;
-  for (int k0 = 0; k0 < s.r; k0 += 64) {
-    const int kc = s.r - k0 > 32 ? 64 : 32;              // ranks in LDS, zeros past r
+  // ranks k0 .. + 63 (or the rest), in steps of 32: one (up to 32 ranks), or two
+  const auto pass = [&](int k0, auto n_steps) {
+    constexpr int kSteps = decltype(n_steps)::value, kOnce = T::kRows == 128 ? 1 : 16 / (kN * kSteps);
+    const int kc = kSteps == 2 && s.r - k0 > 32 ? 64 : 32;               // ranks in LDS, zeros past r
     const int plane = 2 * kc, row_bytes = s.slices * 2 * plane + 16;
-    const bool two = kc == 64;
-    // kAtOnce adapters' B at a time
-    int id[kAtOnce], from[kAtOnce], to[kAtOnce];
-    uint4 b[kAtOnce][2][kN];
+    // kOnce adapters' B at a time: what the registers hold
+    int id[kOnce], from[kOnce], to[kOnce];
+    uint4 b[kOnce][kSteps][kN];
     const auto load_b = [&](int l) {
 #pragma unroll
-      for (int a = 0; a < kAtOnce; ++a) {
+      for (int a = 0; a < kOnce; ++a) {
         l = next_adapter(l);
         id[a] = l;
         from[a] = lo;
@@ -287,13 +288,13 @@ __device__ __forceinline__ void add_adapters(v4f (&acc)[T::kM][T::kN], const Pla
         l = min(l + 1, s.L);
       }
 #pragma unroll
-      for (int a = 0; a < kAtOnce; ++a) {
+      for (int a = 0; a < kOnce; ++a) {
         if (id[a] >= s.L) break;
 #pragma unroll
         for (int q = 0; q < kN; ++q) {
           const uint16_t* at = args.lora_b + (int64_t(id[a]) * s.N + wrow[q] + ln) * s.r;
-          b[a][0][q] = load_in(at, k0 + 8 * kq, s.r);
-          b[a][1][q] = load_in(at, k0 + 32 + 8 * kq, s.r);
+#pragma unroll
+          for (int j = 0; j < kSteps; ++j) b[a][j][q] = load_in(at, k0 + 32 * j + 8 * kq, s.r);
         }
       }
     };
@@ -301,7 +302,7 @@ __device__ __forceinline__ void add_adapters(v4f (&acc)[T::kM][T::kN], const Pla
     if (k0 > 0) __syncthreads();                         // the ranks before are done with
     // u's elements, four at a time, those of kU quads in flight together
     constexpr int kU = T::kSize == 256 ? 1 : 2;          // (what the registers hold)
-    const int rows = min(T::kSize, s.M - m0), quads = min(s.r - k0, 64) / 4, pads = kc / 4 - quads;
+    const int rows = min(T::kSize, s.M - m0), quads = min(s.r - k0, kc) / 4, pads = kc / 4 - quads;
     const int n = rows * s.slices * quads;
     const int64_t u_stride = int64_t(s.M) * cols;
     const auto place = [&](int i, int per, int& k) {     // quad i of rows x slices x `per` quads
@@ -343,10 +344,10 @@ __device__ __forceinline__ void add_adapters(v4f (&acc)[T::kM][T::kN], const Pla
     __syncthreads();
     while (id[0] < s.L) {
 #pragma unroll
-      for (int a = 0; a < kAtOnce; ++a) {
+      for (int a = 0; a < kOnce; ++a) {
         if (id[a] >= s.L) break;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < kSteps; ++j)
 #pragma unroll
           for (int q = 0; q < kN; ++q) b[a][j][q] = keep(b[a][j][q], k0 + 32 * j + 8 * kq < s.r);
 #pragma unroll
@@ -361,11 +362,11 @@ __device__ __forceinline__ void add_adapters(v4f (&acc)[T::kM][T::kN], const Pla
             for (int q = 0; q < kN; ++q) {
               const int slice = s.slices == 2 && wrow[q] >= s.N / 2 ? 2 * plane : 0;
               v4f d = v4f{0.f, 0.f, 0.f, 0.f};
-              d = mfma(*reinterpret_cast<const uint4*>(at + slice), b[a][0][q], d);
-              d = mfma(*reinterpret_cast<const uint4*>(at + slice + plane), b[a][0][q], d);
-              if (two) {
-                d = mfma(*reinterpret_cast<const uint4*>(at + slice + 64), b[a][1][q], d);
-                d = mfma(*reinterpret_cast<const uint4*>(at + slice + plane + 64), b[a][1][q], d);
+#pragma unroll
+              for (int j = 0; j < kSteps; ++j) {
+                if (j == 1 && kc == 32) break;
+                d = mfma(*reinterpret_cast<const uint4*>(at + slice + 64 * j), b[a][j][q], d);
+                d = mfma(*reinterpret_cast<const uint4*>(at + slice + plane + 64 * j), b[a][j][q], d);
               }
 #pragma unroll
               for (int v = 0; v < 4; ++v) acc[i][q][v] += mine[v] ? d[v] : 0.0f;
@@ -374,8 +375,13 @@ __device__ __forceinline__ void add_adapters(v4f (&acc)[T::kM][T::kN], const Pla
           __builtin_amdgcn_sched_barrier(0);
         }
       }
-      load_b(min(id[kAtOnce - 1] + 1, s.L));
+      load_b(min(id[kOnce - 1] + 1, s.L));
     }
+  };
+  for (int k0 = 0; k0 < s.r; k0 += 64) {
+    // (the 256 tile's accumulators leave no room for both)
+    if (T::kRows == 128 || s.r - k0 > 32) pass(k0, std::integral_constant<int, 2>());
+    else pass(k0, std::integral_constant<int, 1>());
   }
 }
 

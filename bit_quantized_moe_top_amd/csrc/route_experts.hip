@@ -61,6 +61,11 @@ __device__ __forceinline__ double shfl64(double v, int from) {
   return __builtin_bit_cast(double, shfl64(__builtin_bit_cast(uint64_t, v), from));
 }
 
+__device__ __forceinline__ uint64_t readlane64(uint64_t v, int from) {
+  return uint64_t(uint32_t(readlane(int(uint32_t(v)), from))) |
+         (uint64_t(uint32_t(readlane(int(uint32_t(v >> 32)), from))) << 32);
+}
+
 // score of a logit in fp32: softmax relative to `top`, times 1 / denominator
 __device__ __forceinline__ float fast_score(float l, bool softmax, float top, float rden) {
   return softmax ? exp_fast(l - top) * rden : __builtin_amdgcn_rcpf(1.0f + exp_fast(-l));
@@ -135,51 +140,40 @@ struct WideChoice {
     const uint64_t mine = shfl64(value, lane << shift & 63);             // lane g: group g's
     int above = 0;
     for (int o = 0; o < p.n_group; ++o) {
-      const uint64_t other = shfl64(mine, o);
+      const uint64_t other = readlane64(mine, o);
       above += other > mine || (other == mine && o < lane);
     }
     return __ballot(lane < p.n_group && above < p.topk_group);
   }
 
-  // The k best of the experts whose fp32 sum is above `edge` in the groups of `stay`: lane r returns
-  // the r-th (-1: there are fewer).  cand: 64 ints of LDS.
-  __device__ __forceinline__ int picks(uint64_t stay, float edge, float rden, int* cand) const {
-    const int S = p.E / p.n_group;
-    const auto in = [&](int e, float l, float b) {
-      return l != -INFINITY && !(fast_score(l, softmax, float(top), rden) + b <= edge) && (stay >> (e / S & 63) & 1);
-    };
-    int m = 0;
-    each(lane, kWave, p.E, [&](int e, float l, float b) {
-      const bool take = in(e, l, b);
-      const uint64_t takers = __ballot(take);
-      const int at = m + __popcll(takers & ((uint64_t(1) << lane) - 1));
-      if (take && at < kWave) cand[at] = e;
-      m += __popcll(takers);
-    });
-    lds_wave_sync();
-    if (m <= kWave) {
-      const int e = lane < m ? cand[lane] : -1;
-      const uint64_t key = e >= 0 ? wide_key(c(load1(row + e), bias[e])) : 0;
-      int rank = 0;                                      // (candidates ascend with the lane)
-      for (int i = 0; i < m; ++i) {
-        const uint64_t other = shfl64(key, i);
-        rank += other > key || (other == key && i < lane);
-      }
-      lds_wave_sync();
-      if (lane < m && rank < p.k) cand[rank] = e;
-      lds_wave_sync();
-      const int got = lane < min(m, p.k) ? cand[lane] : -1;
-      lds_wave_sync();                                   // (the next token's candidates)
-      return got;
+  // The k best of n <= 64 candidates in LDS, which are overwritten: lane r returns the r-th (-1: there
+  // are fewer).
+  __device__ __forceinline__ int ranked(int* cand, int n) const {
+    const int e = lane < n ? cand[lane] : 0;
+    const uint64_t key = lane < n ? wide_key(c(load1(row + e), bias[e])) : 0;
+    int rank = 0;
+    for (int i = 0; i < n; ++i) {
+      const uint64_t other = readlane64(key, i);
+      rank += other > key || (other == key && readlane(e, i) < e);
     }
-    // more candidates than lanes: round by round, the best after the last taken
+    lds_wave_sync();
+    if (lane < n && rank < p.k) cand[rank] = e;
+    lds_wave_sync();
+    return lane < min(n, p.k) ? cand[lane] : -1;
+  }
+  // The same of all experts whose fp32 sum is above `edge` in the groups of `stay`, however many they
+  // are: round by round, the best after the last taken.
+  __device__ __forceinline__ int rounds(uint64_t stay, float edge, float rden) const {
+    const int S = p.E / p.n_group;
     uint64_t last = ~0ull;
     int last_e = -1, mine = -1;
     for (int r = 0; r < p.k; ++r) {
       uint64_t best = 0;
       int at = -1;
       each(lane, kWave, p.E, [&](int e, float l, float b) {
-        const uint64_t key = in(e, l, b) ? wide_key(c(l, b)) : 0;
+        const bool in = l != -INFINITY && !(fast_score(l, softmax, float(top), rden) + b <= edge) &&
+                        (stay >> (e / S & 63) & 1);
+        const uint64_t key = in ? wide_key(c(l, b)) : 0;
         if ((key < last || (key == last && e > last_e)) && key > best) {
           best = key;
           at = e;
@@ -561,19 +555,44 @@ route_experts_kernel(const LT* __restrict__ logits, const float* __restrict__ bi
           }
     }
     if (__ballot(open)) {
+      // candidates: the picks that have a score and the experts within tol of the last one or above it,
+      // W at most in LDS
+      int n = 0;
+      const auto add = [&](bool take, int expert) {
+        const uint64_t takers = Tok::ballot(take, lane);
+        const int to = n + __popcll(takers & ((uint64_t(1) << sub) - 1));
+        if (take && to < W) s_cand[wave][(lane & ~(W - 1)) + to] = expert;
+        n += __popcll(takers);
+      };
+      add(live, e);
+      if (__ballot(near)) {
+#pragma unroll
+        for (int i = 0; i < SortedSlots<NS>::kLists; ++i)
+#pragma unroll
+          for (int j = 0; j < SortedSlots<NS>::kLen; ++j)
+            add(left.key[i][j] > edge_key,
+                ln.first + SortedSlots<NS>::kLen * i + int(left.order[i] >> (8 * j) & 255u));
+      }
+      lds_wave_sync();
       // tokens in turn, each by the whole wave
       for (int i = 0; i < kTokens; ++i) {
         const uint64_t mine = W == 64 ? ~0ull : uint64_t(0xFFFFu) << (16 * i);
         if ((__ballot(open) & mine) == 0) continue;
-        uint64_t stay = ~0ull;                               // groups of the public numbering
-        if (grouped) {
-          const uint64_t lanes = __ballot(stays) >> (W * i & 63);
-          stay = 0;
-          for (int g = 0; g < lay.G; ++g) stay |= (lanes >> (g << lay.shift) & 1) << g;
-        }
         const WideChoice<LT> wide(logits + int64_t(min(t0 + i, p.T - 1)) * p.ld, bias, p, lane,
                                   readlane(top, W * i));
-        int got = wide.picks(stay, readlane(edge, W * i), readlane(rden, W * i), s_cand[wave]);
+        const int m = readlane(n, W * i);
+        int got;
+        if (m <= W) {
+          got = wide.ranked(s_cand[wave] + W * i, m);
+        } else {
+          uint64_t stay = ~0ull;                             // groups of the public numbering
+          if (grouped) {
+            const uint64_t lanes = __ballot(stays) >> (W * i & 63);
+            stay = 0;
+            for (int g = 0; g < lay.G; ++g) stay |= (lanes >> (g << lay.shift) & 1) << g;
+          }
+          got = wide.rounds(stay, readlane(edge, W * i), readlane(rden, W * i));
+        }
         // (as many as have a score: with a NaN among the values not always, and then the fp32 picks,
         // which are distinct, stay)
         const bool all = __popcll(__ballot(got >= 0)) == __popcll(__ballot(live) & mine);

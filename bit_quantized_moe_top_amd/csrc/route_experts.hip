@@ -22,8 +22,9 @@
 // 2^-22 |c| with smax = pmax, or 1/8 for sigmoid.
 //
 // Bound by VALU issue, a token's scores, sorts and k rounds against 2 or 4 E bytes read: 16384 tokens of
-// 256 experts in 8 groups 15.3 us (17.8 MB, 1.2 TB/s; some 1340 vector instructions a wave of four tokens),
-// 4096 of 1024 experts with a bias 15.3 us (0.57 TB/s; 1160 a wave of one), 64 of 256 3.6 us, a launch.
+// 256 experts in 8 groups 14.1 us (17.8 MB, 1.3 TB/s; some 1300 vector instructions a wave of four
+// tokens), 4096 of 1024 experts with a bias 13.3 us (0.65 TB/s; 1160 a wave of one, and the choice in 64
+// bits at the end; without a bias 9.2), 64 of 256 3.8 us, a launch.
 #include <algorithm>
 
 #include "front.hpp"
@@ -73,10 +74,10 @@ __device__ __forceinline__ float fast_score(float l, bool softmax, float top, fl
 
 // ---------------------------------------------------- the choice in 64 bits
 // One token by a whole wave.  Rare, but a wave that comes here ends last: experts are read four a lane at
-// a time and the candidates ranked side by side (4096 tokens of 1024 experts, six of them here: 15.3 us
-// against 18.5 with one expert a lane at a time and a pass over them for each pick).  Few registers, for
-// these are the whole kernel's: with the row kept in them that case took 16.2 us, but 16384 tokens of 256
-// experts 18.5 against 15.3.
+// a time and the candidates, taken from the sorted lists, are ranked side by side (4096 tokens of 1024
+// experts, some six of them here: 13.3 us; with the candidates found by another pass over the row 15.3,
+// one expert a lane at a time and a pass for each pick 18.5).  Few registers, for these are the whole
+// kernel's: the row kept in them cost 16384 tokens of 256 experts a fifth.
 template <typename LT>
 struct WideChoice {
   const LT* row;
@@ -460,18 +461,24 @@ route_experts_kernel(const LT* __restrict__ logits, const float* __restrict__ bi
         const float other = readlane(hi, g << lay.shift);
         maybe += other > lo || (other == lo && (scores || g <= ln.g)) ? 1 : 0;
       }
-    } else {                                                 // lanes of groups, by rotation of the row
+    } else {                                                 // a lane of each group, by rotation of the row
       const auto count = [&](auto n) {
         const float other = dpp<kDppRowRor + decltype(n)::value>(0.0f, hi);
         const int og = ((sub - decltype(n)::value) & 15) >> lay.shift;
         maybe += other > lo || (other == lo && (scores || og <= ln.g)) ? 1 : 0;
       };
       maybe += hi >= lo ? 1 : 0;
-      count(SlotsTag<1>{}); count(SlotsTag<2>{}); count(SlotsTag<3>{}); count(SlotsTag<4>{});
-      count(SlotsTag<5>{}); count(SlotsTag<6>{}); count(SlotsTag<7>{}); count(SlotsTag<8>{});
-      count(SlotsTag<9>{}); count(SlotsTag<10>{}); count(SlotsTag<11>{}); count(SlotsTag<12>{});
-      count(SlotsTag<13>{}); count(SlotsTag<14>{}); count(SlotsTag<15>{});
-      maybe >>= lay.shift;
+      count(SlotsTag<8>{});
+      if (lay.shift <= 2) {
+        count(SlotsTag<4>{}); count(SlotsTag<12>{});
+      }
+      if (lay.shift <= 1) {
+        count(SlotsTag<2>{}); count(SlotsTag<6>{}); count(SlotsTag<10>{}); count(SlotsTag<14>{});
+      }
+      if (lay.shift == 0) {
+        count(SlotsTag<1>{}); count(SlotsTag<3>{}); count(SlotsTag<5>{}); count(SlotsTag<7>{});
+        count(SlotsTag<9>{}); count(SlotsTag<11>{}); count(SlotsTag<13>{}); count(SlotsTag<15>{});
+      }
     }
     const bool lead = ln.g < lay.G && sub == ln.g << lay.shift;
     const int n_live = __popcll(Tok::ballot(live && lead, lane));

@@ -658,9 +658,9 @@ hipError_t launch_slots(const LT* logits, const float* bias, const RouteShape& s
 
 // Four tokens a wave from this many tokens on for each expert of a lane: before that there are fewer
 // waves than SIMDs want, and one takes longer.  us at 1024 / 2048 / 4096 / 8192 / 16384 tokens, four
-// against one: 64 experts 3.4 / 3.4 / 3.5 / 3.6 / 5.0 against 3.4 / 3.5 / 4.4 / 6.1 / 10.4; 128 with a
-// bias 5.1 / 5.7 / 6.5 / 7.7 / 9.7 against 4.5 / 5.1 / 6.4 / 8.7 / 13.4; 256 in 8 groups 7.7 / 8.8 / 10.1 /
-// 12.9 / 17.7 against 5.7 / 6.8 / 8.9 / 13.3 / 20.6.
+// against one: 64 experts 3.5 / 3.5 / 3.5 / 3.7 / 5.0 against 3.4 / 3.6 / 4.4 / 6.2 / 10.3; 128 with a
+// bias 5.0 / 5.4 / 6.0 / 7.3 / 9.6 against 4.3 / 4.7 / 5.8 / 8.5 / 13.7; 256 in 8 groups 6.8 / 7.5 / 8.3 /
+// 10.5 / 13.9 against 5.2 / 5.8 / 7.5 / 11.7 / 18.5.
 constexpr int kShareTokens = 512;
 
 template <typename LT>

@@ -12,7 +12,7 @@
 //    if neighbours among them, and the last pick and every expert left, are at least tol apart or are
 //    the same number (equal logit and equal bias, hence a tie that the index decides).  Otherwise the
 //    experts within tol of the last pick or above it, the only ones the true choice can be among, are
-//    ranked by their c in 64 bits.  Likewise for groups.  (For random logits some 3 tokens in 10000.)
+//    ranked by their c in 64 bits.  Likewise for groups.  (For random logits some 3 to 15 tokens in 10000.)
 //
 // tol: with u = 2^-24, exp by the hardware's 2^x is within (1.5 |x| + 2) u of its value (the product
 // with log2 e, its rounding, 1 ulp).  Sigmoid: s (1 - s) |l| < 0.23, so |ds| <= (0.9 + 1 + 2) u with the

@@ -209,7 +209,7 @@ __device__ __forceinline__ uint32_t lds_offset(const uint8_t* p) {
 }
 
 // ------------------------------------------------------------- shared product
-// B x B tiles by G groups of kWM x kWN waves, each wave B / kWM rows x B / kWN columns.  A group has a
+// BM x BN tiles by G groups of kWM x kWN waves, each wave BM / kWM rows x BN / kWN columns.  A group has a
 // ring of its own and a G-th of K; the groups' sums meet in LDS.  The ring holds units: the 128-byte
 // pieces (64 K) of the tile's w rows or of its x rows, in turn (w first: it comes from farther and has
 // half a slot more time).  The first kUnits - 1 go out up front.  A slot (a w unit and the x unit after
@@ -220,18 +220,30 @@ __device__ __forceinline__ uint32_t lds_offset(const uint8_t* p) {
 // (lgkmcnt(0), which waits for nothing), and this wave's loads of slot st + 1 have landed (all but those
 // of the kUnits - 4 units issued after them); after the barrier the same holds for every wave, so slot
 // st + 1 can be read, and the next two units take slot st's places.
-template <int B, int G>
+template <int BM_, int BN_, int G>
 struct Tile {
-  static constexpr int kSize = B, kGroups = G;
-  static constexpr int kWM = 2, kWN = B == 256 ? 4 : 2, kGroupWaves = kWM * kWN;
-  static constexpr int kRows = B / kWM, kCols = B / kWN, kM = kRows / 16, kN = kCols / 16;
+  static constexpr int BM = BM_, BN = BN_, kGroups = G;
+  static constexpr int kWM = BM > BN ? 4 : 2, kWN = BN == 256 ? 4 : 2, kGroupWaves = kWM * kWN;
+  static constexpr int kRows = BM / kWM, kCols = BN / kWN, kM = kRows / 16, kN = kCols / 16;
   static constexpr int kEndM = kM / G;                   // row blocks that a wave finishes
-  static constexpr int kUnitB = B * kRowB, kLoads = B / 8 / kGroupWaves;   // loads of a unit per wave
-  // a CU's 160 KB for one workgroup of 256 x 256 or of two groups, half of them for the others
-  static constexpr int kUnits = B == 256 ? 5 : 80 * 1024 / kUnitB;
-  static constexpr int kRingB = kUnits * kUnitB, kLds = G * kRingB, kThreads = 64 * kGroupWaves * G;
+  static constexpr int kXB = BM * kRowB, kWB = BN * kRowB;               // bytes of a unit
+  static constexpr int kLX = BM / 8 / kGroupWaves, kLW = BN / 8 / kGroupWaves;   // and loads of a wave
+  // a CU's 160 KB for one workgroup of 256 rows or of two groups, half of them for the others
+  static constexpr int kRoom = BM == 256 ? 160 * 1024 : 80 * 1024;
+  static constexpr int kUnits = BM == BN ? kRoom / kXB : kRoom / (kXB + kWB) * 2;
+  static constexpr int kRingB = BM == BN ? kUnits * kXB : kUnits / 2 * (kXB + kWB);
+  static constexpr int kLds = G * kRingB, kThreads = 64 * kGroupWaves * G;
   static_assert(kUnits >= 4, "two slots");
-  static_assert((G == 1 ? 0 : B * B * 4) + B * (2 * 2 * 128 + 16) <= kLds, "the exchange, and 64 ranks of u");
+  static_assert((G == 1 ? 0 : BM * BN * 4) + BM * (2 * 2 * 128 + 16) <= kLds, "the exchange, and 64 ranks of u");
+  // where unit j (j < kUnits) lies; loads of units from .. to - 1 (even: w)
+  static __device__ __forceinline__ int place(int j) {
+    return BM == BN ? j * kXB : (j >> 1) * (kXB + kWB) + (j & 1) * kWB;
+  }
+  static constexpr int loads(int from, int to) {
+    int n = 0;
+    for (int j = from; j < to; ++j) n += j & 1 ? kLX : kLW;
+    return n;
+  }
 };
 
 // acc[i][q] += u B_l^T, i < kEndM, for the rows p0 + 16 i .. and w rows wrow[q] .. + 15, by all waves of
@@ -301,8 +313,8 @@ __device__ __forceinline__ void add_adapters(v4f (&acc)[T::kM][T::kN], const Pla
     load_b(first);
     if (k0 > 0) __syncthreads();                         // the ranks before are done with
     // u's elements, four at a time, those of kU quads in flight together
-    constexpr int kU = T::kSize == 256 ? 1 : 2;          // (what the registers hold)
-    const int rows = min(T::kSize, s.M - m0), quads = min(s.r - k0, kc) / 4, pads = kc / 4 - quads;
+    constexpr int kU = T::kRows == 128 ? 1 : 2;          // (what the registers hold)
+    const int rows = min(T::BM, s.M - m0), quads = min(s.r - k0, kc) / 4, pads = kc / 4 - quads;
     const int n = rows * s.slices * quads;
     const int64_t u_stride = int64_t(s.M) * cols;
     const auto place = [&](int i, int per, int& k) {     // quad i of rows x slices x `per` quads
@@ -397,7 +409,7 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restr
   static_assert(MODE != kParts || EPI == MOEQ_EPI_NONE, "parts are of W's own columns");
   static_assert(MODE == kWhole || T::kGroups == 1, "groups are for whole tiles");
   constexpr int kM = T::kM, kN = T::kN, kG = T::kGroups;       // kM x kN blocks of 16 x 16 per wave
-  constexpr int B = T::kSize, kL = T::kLoads, kEndM = T::kEndM;
+  constexpr int BM = T::BM, BN = T::BN, kLX = T::kLX, kLW = T::kLW, kEndM = T::kEndM;
   constexpr bool kSilu = EPI == MOEQ_EPI_SILU_MUL;
   extern __shared__ __align__(16) uint8_t lds[];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -407,7 +419,7 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restr
   const int wm = gw / T::kWN, wn = gw % T::kWN;
   const PlanView pv = plan_view(args.plan, s.L + 1, s.M);
   const int cols = kSilu ? s.N / 2 : s.N;                // output columns, a multiple of 16
-  constexpr int kOut = kSilu ? B / 2 : B;                // output columns per workgroup
+  constexpr int kOut = kSilu ? BN / 2 : BN;                // output columns per workgroup
   // Workgroups go round the XCDs: each takes a run of tiles, all row tiles of a column tile before
   // the next one, so that an XCD's tiles share their w rows in its L2.
   int block = blockIdx.x, blocks = gridDim.x;
@@ -419,7 +431,7 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restr
       return;
     }
   }
-  const int mtiles = (s.M + B - 1) / B;
+  const int mtiles = (s.M + BM - 1) / BM;
   const int xcd = block & 7;
   int tile = xcd * (blocks >> 3) + min(xcd, blocks & 7) + (block >> 3), split = 0;
   if constexpr (MODE == kParts) {                        // the splits of a tile follow each other
@@ -427,30 +439,34 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restr
     tile /= splits;
   }
   const int nt = tile / mtiles, mt = tile - nt * mtiles;
-  const int m0 = mt * B, n0 = nt * kOut;
+  const int m0 = mt * BM, n0 = nt * kOut;
 
-  // w row of tile row i: B columns, or B/2 gate and their B/2 up rows; past the end the last one
+  // w row of tile row i: BN columns, or BN/2 gate and their BN/2 up rows; past the end the last one
   // again (its results are not stored)
   const auto w_row = [&](int i) {
-    if (kSilu) return i < B / 2 ? min(n0 + i, cols - 1) : cols + min(n0 + i - B / 2, cols - 1);
+    if (kSilu) return i < BN / 2 ? min(n0 + i, cols - 1) : cols + min(n0 + i - BN / 2, cols - 1);
     return min(n0 + i, cols - 1);
   };
   // tile row of the wave's 16-column block q: gate blocks, then the matching up blocks
   const auto block_row = [&](int q) {
-    return kSilu ? (q < kN / 2 ? 0 : B / 2) + (T::kCols / 2) * wn + 16 * (q % (kN / 2))
+    return kSilu ? (q < kN / 2 ? 0 : BN / 2) + (T::kCols / 2) * wn + 16 * (q % (kN / 2))
                  : T::kCols * wn + 16 * q;
   };
 
-  // loads: wave v of a group moves rows 8 (kL v + g) + lr, lane's chunk (lane % 8) ^ swz(row)
-  const uint16_t *xsrc[kL], *wsrc[kL];
+  // loads: wave v of a group moves rows 8 (its loads v + g) + lr, lane's chunk (lane % 8) ^ swz(row)
+  const uint16_t *xsrc[kLX], *wsrc[kLW];
 #pragma unroll
-  for (int g = 0; g < kL; ++g) {
-    const int row = 8 * (kL * gw + g) + lr, c = ((lane & 7) ^ swz(row & 15)) * 8;
-    xsrc[g] = args.a + int64_t(plan_row(pv, m0 + row, s.M)) * s.ld_a + c;
-    wsrc[g] = args.w + int64_t(w_row(row)) * s.K + c;
+  for (int g = 0; g < kLX; ++g) {
+    const int row = 8 * (kLX * gw + g) + lr;
+    xsrc[g] = args.a + int64_t(plan_row(pv, m0 + row, s.M)) * s.ld_a + ((lane & 7) ^ swz(row & 15)) * 8;
+  }
+#pragma unroll
+  for (int g = 0; g < kLW; ++g) {
+    const int row = 8 * (kLW * gw + g) + lr;
+    wsrc[g] = args.w + int64_t(w_row(row)) * s.K + ((lane & 7) ^ swz(row & 15)) * 8;
   }
   const uint8_t* const ring = lds + group * T::kRingB;
-  const uint32_t ring0 = lds_offset(ring) + 8 * kL * gw * kRowB;
+  const uint32_t ring0 = lds_offset(ring);
   // this group's (or launch's) slots of 64 K: first, number
   const int all_slots = s.K / kSlotK;
   const int s0 = MODE == kParts ? int(int64_t(all_slots) * split / splits) : group * (all_slots / kG);
@@ -459,8 +475,9 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restr
   // load g of unit `unit` (2 st: w, 2 st + 1: x of slot st); past the last slot, the last again
   const auto issue = [&](bool is_w, int g, int unit) {
     const int k = (s0 + min(unit >> 1, slots - 1)) * kSlotK;
-    load_lds<false>((is_w ? wsrc[g] : xsrc[g]) + k,
-                    ring0 + uint32_t(unit % T::kUnits) * T::kUnitB + 8 * g * kRowB);
+    const int row = 8 * ((is_w ? kLW : kLX) * gw + g);
+    load_lds<false>((is_w ? wsrc[is_w ? g : 0] : xsrc[is_w ? 0 : g]) + k,
+                    ring0 + uint32_t(T::place(unit % T::kUnits) + row * kRowB));
   };
 
   v4f acc[kM][kN];
@@ -487,26 +504,26 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restr
 #pragma unroll
     for (int unit = 0; unit + 1 < T::kUnits; ++unit)
 #pragma unroll
-      for (int g = 0; g < kL; ++g) issue(!(unit & 1), g, unit);
-    wait_vmem<(T::kUnits - 3) * kL>();
+      for (int g = 0; g < (unit & 1 ? kLX : kLW); ++g) issue(!(unit & 1), g, unit);
+    wait_vmem<T::loads(2, T::kUnits - 1)>();
     ring_barrier();
     int px = 1, pw = 0;                                  // ring places of the slot's units
     read_w(ring, 0);
 #pragma unroll
-    for (int i = 0; i < kM; ++i) read_x(i, ring + T::kUnitB, 0);
+    for (int i = 0; i < kM; ++i) read_x(i, ring + T::place(1), 0);
     // unit `unit`'s loads, spread over the rows from `first` on
     const auto issue_row = [&](int i, int first, int unit, bool is_w) {
-      const int rows = kM - first, per = (kL + rows - 1) / rows;
+      const int n = is_w ? kLW : kLX, rows = kM - first, per = (n + rows - 1) / rows;
 #pragma unroll
-      for (int j = 0; j < kL; ++j)
+      for (int j = 0; j < n; ++j)
         if (i >= first && j / per == i - first) issue(is_w, j, unit);
     };
     const auto first_half = [&](int st) {
-      read_w(ring + pw * T::kUnitB, 1);
+      read_w(ring + T::place(pw), 1);
 #pragma unroll
       for (int i = 0; i < kM; ++i) {
         multiply(i, 0);
-        read_x(i, ring + px * T::kUnitB, 1);
+        read_x(i, ring + T::place(px), 1);
         issue_row(i, 0, 2 * st + T::kUnits - 1, T::kUnits & 1);
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -518,15 +535,15 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restr
 #pragma unroll
       for (int i = 0; i < kM; ++i) {
         if (i == kOpen) {
-          wait_vmem<(T::kUnits - 4) * kL>();
+          wait_vmem<T::loads(4, T::kUnits)>();
           ring_barrier();
-          read_w(ring + pw * T::kUnitB, 0);
+          read_w(ring + T::place(pw), 0);
 #pragma unroll
-          for (int j = 0; j < kOpen; ++j) read_x(j, ring + px * T::kUnitB, 0);
+          for (int j = 0; j < kOpen; ++j) read_x(j, ring + T::place(px), 0);
         }
         multiply(i, 1);
         if (i >= kOpen) {
-          read_x(i, ring + px * T::kUnitB, 0);
+          read_x(i, ring + T::place(px), 0);
           issue_row(i, kOpen, 2 * st + T::kUnits, !(T::kUnits & 1));
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -544,17 +561,17 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restr
       const int k0 = (all_slots / kG * kG + rest) * kSlotK;
       if (k0 >= s.K) break;
       ring_barrier();
-      for (int i = tid; i < 2 * B * 8; i += T::kThreads) {
+      for (int i = tid; i < (BM + BN) * 8; i += T::kThreads) {
         const int row = i >> 3, c = i & 7;
-        const uint16_t* src = row < B ? args.a + int64_t(plan_row(pv, m0 + row, s.M)) * s.ld_a
-                                       : args.w + int64_t(w_row(row - B)) * s.K;
+        const uint16_t* src = row < BM ? args.a + int64_t(plan_row(pv, m0 + row, s.M)) * s.ld_a
+                                       : args.w + int64_t(w_row(row - BM)) * s.K;
         *reinterpret_cast<uint4*>(lds + row * kRowB + ((c ^ swz(row & 15)) * 16)) = load_k(src, k0 + 8 * c, s.K);
       }
       __syncthreads();
       if (group > 0) continue;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        read_w(lds + B * kRowB, h);
+        read_w(lds + BM * kRowB, h);
 #pragma unroll
         for (int i = 0; i < kM; ++i) {
           read_x(i, lds, h);
@@ -569,7 +586,7 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restr
 #pragma unroll
   for (int q = 0; q < kN; ++q) {
     const bool up = kSilu && q >= kN / 2;
-    ocol[q] = n0 + block_row(q) - (up ? B / 2 : 0);
+    ocol[q] = n0 + block_row(q) - (up ? BN / 2 : 0);
     wrow[q] = min(ocol[q], cols - 16) + (up ? cols : 0);
   }
   const int p0 = m0 + T::kRows * wm + 16 * kEndM * group;
@@ -605,7 +622,7 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restr
     if constexpr (MODE == kParts) return;
   }
   ring_barrier();                                        // the ring's LDS is free
-  constexpr int kMeet = kG == 1 ? 0 : B * B * 4;       // LDS of the groups' exchange: half of either's sums
+  constexpr int kMeet = kG == 1 ? 0 : BM * BN * 4;       // LDS of the groups' exchange: half of either's sums
   if constexpr (kG > 1) {
     // group g finishes row blocks g kEndM ...: it leaves its sums of the others to their group
     static_assert(kG == 2, "one other group");
@@ -1282,8 +1299,8 @@ ShrinkGrid shrink_grid(const LoraShape& s) {
           (s.slices * s.r + kShrinkCols - 1) / kShrinkCols, s.M > 4096 ? 1 : pieces < 4 ? pieces : 4};
 }
 
-int64_t tiles_of(const LoraShape& s, int b) {
-  return int64_t((s.M + b - 1) / b) * ((s.N + b - 1) / b);
+int64_t tiles_of(const LoraShape& s, int bm, int bn) {
+  return int64_t((s.M + bm - 1) / bm) * ((s.N + bn - 1) / bn);
 }
 
 // Parts are joined by lora_join_kernel up to this many of its workgroups, by 64 x 64 tiles from there
@@ -1292,37 +1309,39 @@ int64_t tiles_of(const LoraShape& s, int b) {
 // gate/up 8192: 45.9 against 43.0; 256 rows, 4096: 51.7 against 44.9).
 constexpr int kJoinBlocks = 2400;
 
-// How more than 64 rows are multiplied: tiles of `size` rows and columns by `groups` groups of waves, K
-// split over `splits` workgroups (1: whole tiles, the shrink ahead of them).  The larger the tile the
+// How more than 64 rows are multiplied: tiles of bm x bn by `groups` groups of waves, K split over `splits` workgroups (1: whole tiles, the shrink ahead of them).  The larger the tile the
 // fewer bytes reach LDS per product, and a CU takes in some 45 KB of them a microsecond whatever it has in
 // flight (rows that L2 has wait behind the w rows that it has not); but there are 256 CUs to fill.  So
 // the largest tile that is met often enough, and below that K is divided: between two groups of waves
 // of a workgroup while one tile a CU fills the card in one go, else between workgroups.  us, K = 4096,
-// rows x columns:
-//                 256 whole  128 whole  128, 2 groups  128 / 2  128 / 4  64 whole  64 / 2  64 / 4
-//    2048 x 8192      128        160          182         240      310      330
-//    1280 x 8192      108        125          130         148      187      201
-//    1024 x 8192      105         83           95         116      150      154     202     231
-//     768 x 8192      106         79           93          94      112      120     142     172
-//     512 x 8192      107         62           53          67       78       84      99     127
-//     512 x 4096      105         58           51          39       44       47      53      66
-//     256 x 8192      111         60           55          42       48       51      57      65
-//     128 x 8192      113         62           57          39       36       37      41      44
-//     128 x 4096      112         60           55          32       27       34      26      28
-//     128 x 2048      101         51           40          24       17       26      17      15
-// and 64 whole for short K while it fills the card: 512 x 4096 x 2048 25.5 against 27.2 (128, 2 groups)
-// and 27.6 (128 / 2); x 1024 19.4, 21.3, 21.5.
+// one slice, 16 adapters mixed, rows x columns:
+//                 256   256x128   128   128, 2 groups   128 / 2   128 / 4   64    64 / 2   64 / 4
+//    2048 x 8192  128     141     160        182           240      310     330
+//    1280 x 8192  108     132     125        130           148      187     201
+//    1024 x 8192  105      75      83         95           116      150     154     202     231
+//     768 x 8192  106      70      79         93            94      112     120     142     172
+//     640 x 8192           65      76                       86               99
+//     512 x 8192  107      68      62         53            67       78      84      99     127
+//     512 x 4096  105              58         51            39       44      47      53      66
+//     256 x 8192  111              60         55            42       48      51      57      65
+//     128 x 8192  113              62         57            39       36      37      41      44
+//     128 x 4096  112              60         55            32       27      34      26      28
+//     128 x 2048  101              51         40            24       17      26      17      15
+// and 64 for short K while it fills the card: 512 x 4096 x 2048 25.5 against 27.2 (128, 2 groups) and
+// 27.6 (128 / 2); x 1024 19.4, 21.3, 21.5.
 struct TilePlan {
-  int size, groups, splits;
+  int bm, bn, groups, splits;
 };
 TilePlan tile_plan(const LoraShape& s) {
-  const int64_t t256 = tiles_of(s, 256), t128 = tiles_of(s, 128), t64 = tiles_of(s, 64);
-  if (t256 >= 150) return {256, 1, 1};
-  if (t128 >= 350) return {128, 1, 1};
-  if (t64 >= 200 && s.K <= 2048) return {64, 1, 1};
-  if (t128 >= 200 && t128 <= 256) return {128, 2, 1};
-  if (t128 >= 64) return {128, 1, t128 >= 128 ? 2 : 4};
-  return {64, 1, t64 >= 100 ? 2 : 4};
+  const int64_t t256 = tiles_of(s, 256, 256), t256x128 = tiles_of(s, 256, 128), t128 = tiles_of(s, 128, 128),
+                t64 = tiles_of(s, 64, 64);
+  if (t256 >= 150) return {256, 256, 1, 1};
+  if (t256x128 >= 150 && t256x128 <= 256) return {256, 128, 1, 1};
+  if (t128 >= 350) return {128, 128, 1, 1};
+  if (t64 >= 200 && s.K <= 2048) return {64, 64, 1, 1};
+  if (t128 >= 200 && t128 <= 256) return {128, 128, 2, 1};
+  if (t128 >= 64) return {128, 128, 1, t128 >= 128 ? 2 : 4};
+  return {64, 64, 1, t64 >= 100 ? 2 : 4};
 }
 size_t tile_u_bytes(const LoraShape& s) {
   return align256(size_t(shrink_grid(s).splits) * s.M * s.slices * s.r * sizeof(float));
@@ -1336,7 +1355,7 @@ hipError_t launch_tile_kernel(const LoraArgs& args, const LoraShape& s, float* u
                                              hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
   if (err != hipSuccess) return err;
   const ShrinkGrid sgrid = shrink_grid(s);
-  const int64_t tiles = tiles_of(s, T::kSize), blocks = MODE == kParts ? sgrid.blocks() + tiles * splits : tiles;
+  const int64_t tiles = tiles_of(s, T::BM, T::BN), blocks = MODE == kParts ? sgrid.blocks() + tiles * splits : tiles;
   hipLaunchKernelGGL(fn, dim3(unsigned(blocks)), dim3(T::kThreads), T::kLds, stream, args, s, u, parts, splits,
                      sgrid);
   return hipGetLastError();
@@ -1369,22 +1388,23 @@ hipError_t launch_shared_gemm_lora(const LoraArgs& args, const LoraShape& s, hip
   const TilePlan tp = tile_plan(s);
   hipError_t err;
   if (tp.splits > 1) {
-    err = tp.size == 128
-              ? launch_tile_kernel<MOEQ_EPI_NONE, Tile<128, 1>, kParts>(args, s, u, parts, tp.splits, stream)
-              : launch_tile_kernel<MOEQ_EPI_NONE, Tile<64, 1>, kParts>(args, s, u, parts, tp.splits, stream);
+    err = tp.bm == 128
+              ? launch_tile_kernel<MOEQ_EPI_NONE, Tile<128, 128, 1>, kParts>(args, s, u, parts, tp.splits, stream)
+              : launch_tile_kernel<MOEQ_EPI_NONE, Tile<64, 64, 1>, kParts>(args, s, u, parts, tp.splits, stream);
     if (err != hipSuccess) return err;
     const int64_t join_blocks = int64_t((s.M + 15) / 16) * ((s.epilogue == MOEQ_EPI_SILU_MUL ? s.N / 2 : s.N) / 16);
     return join_blocks <= kJoinBlocks ? launch_join<false>(args, s, u, parts, tp.splits, shrink_grid(s).splits, stream)
-                            : launch_tiles<Tile<64, 1>, kJoin>(args, s, u, parts, tp.splits, stream);
+                            : launch_tiles<Tile<64, 64, 1>, kJoin>(args, s, u, parts, tp.splits, stream);
   }
   const ShrinkGrid sgrid = shrink_grid(s);
   hipLaunchKernelGGL(lora_shrink_kernel, dim3(unsigned(sgrid.blocks())), dim3(256), 0, stream, args, s, u,
                      sgrid);
   if ((err = hipGetLastError()) != hipSuccess) return err;
-  if (tp.size == 256) return launch_tiles<Tile<256, 1>, kWhole>(args, s, u, parts, 1, stream);
-  if (tp.size == 64) return launch_tiles<Tile<64, 1>, kWhole>(args, s, u, parts, 1, stream);
-  if (tp.groups == 2) return launch_tiles<Tile<128, 2>, kWhole>(args, s, u, parts, 1, stream);
-  return launch_tiles<Tile<128, 1>, kWhole>(args, s, u, parts, 1, stream);
+  if (tp.bn == 256) return launch_tiles<Tile<256, 256, 1>, kWhole>(args, s, u, parts, 1, stream);
+  if (tp.bm == 256) return launch_tiles<Tile<256, 128, 1>, kWhole>(args, s, u, parts, 1, stream);
+  if (tp.bm == 64) return launch_tiles<Tile<64, 64, 1>, kWhole>(args, s, u, parts, 1, stream);
+  if (tp.groups == 2) return launch_tiles<Tile<128, 128, 2>, kWhole>(args, s, u, parts, 1, stream);
+  return launch_tiles<Tile<128, 128, 1>, kWhole>(args, s, u, parts, 1, stream);
 }
 
 }  // namespace moeq

@@ -105,6 +105,8 @@ SHAPES = [
     (1, 32, 520, 4, 2, 16), (2, 64, 552, 3, 2, 32), (15, 96, 584, 5, 2, 24), (17, 160, 616, 40, 1, 40),
     (63, 2080, 840, 8, 2, 8), (64, 128, 1016, 3, 1, 16), (130, 96, 712, 7, 2, 64), (300, 528, 648, 20, 1, 256),
     (260, 8544, 584, 5, 2, 16), (1500, 8736, 520, 3, 2, 8),
+    # tiles of 256 rows and 128 columns: a step of K, none, many; ragged
+    (1000, 7232, 200, 5, 2, 16), (770, 6720, 328, 70, 1, 64), (900, 8000, 40, 3, 1, 8), (1800, 3872, 1096, 6, 2, 40),
     # one launch: K at, below and above 32 and 256; an adapter in every row, and one; pieces of ranks
     # that two slices share; rows and columns off its blocks
     (16, 64, 256, 16, 1, 8), (33, 96, 248, 3, 2, 16), (5, 1040, 256, 5, 1, 16), (200, 336, 200, 8, 1, 8),

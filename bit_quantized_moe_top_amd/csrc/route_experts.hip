@@ -449,9 +449,11 @@ route_experts_kernel(const LT* __restrict__ logits, const float* __restrict__ bi
     const bool live = b1 > none;
     const bool two = p.group_best == 2 && b2 > none;
     const float f1 = key_score(b1), f2 = two ? key_score(b2) : 0.0f;
-    const float half = scores ? 0x1p-17f * smax + 0x1p-22f * (fabsf(f1) + fabsf(f2)) : 0.0f;
-    const float lo = scores ? f1 + f2 - half : f1;
-    const float hi = live ? (scores ? f1 + f2 + half : f1) : -INFINITY;
+    // (of sums half their value: that of two biases at either end of fp32 passes it)
+    const float mid = scores ? 0.5f * f1 + 0.5f * f2 : f1;
+    const float half = scores ? 0x1p-18f * smax + 0x1p-23f * fabsf(f1) + 0x1p-23f * fabsf(f2) : 0.0f;
+    const float lo = mid - half;
+    const float hi = live ? mid + half : -INFINITY;
     // A group stays for sure if at most topk_group - 1 others may be above it.  If as many stay for
     // sure as are to stay, the choice is made.  (The best of the logits are exact: equal ones count
     // if their group is lower.)

@@ -333,3 +333,28 @@ def test_rows_past_32_bits(dtype):
     ids, w = mq.moe_route_experts(z, 5, scoring=SIGM)
     ref = mq.moe_route_experts(rows.to(DEV), 5, scoring=SIGM)
     assert torch.equal(ids, ref[0]) and torch.equal(w, ref[1])
+
+
+@pytest.mark.parametrize("scoring", [SOFT, SIGM])
+@pytest.mark.parametrize("many", [False, True])
+def test_groups_whose_sums_pass_the_largest_fp32(scoring, many):
+    """Biases of either end of fp32, as a mask of the lowest value or of an expert that is always
+    taken: finite, while the sum of a group's best two is not in fp32."""
+    g = gen(19)
+    E, G, S, k = 64, 8, 8, 8
+    low, high = torch.finfo(torch.float32).min, torch.finfo(torch.float32).max
+    rows = torch.randn(12, E, generator=g)
+    rows[1:5, :3 * S][torch.rand(4, 3 * S, generator=g) < 0.9] = -INF
+    rows[5:9][torch.rand(4, E, generator=g) < 0.7] = -INF
+    rows[9] = -INF
+    groups = [torch.full((E,), low), torch.full((E,), high), torch.randn(E, generator=g) * 0.1]
+    groups[2][3 * S:] = low                                          # three groups without the lowest value
+    groups.append(groups[2].roll(S))
+    groups.append(torch.where(torch.arange(E) % S < 2, high, low))
+    groups.append((torch.rand(E, generator=g) - 0.5) * 2 * high)
+    groups.append(torch.where(torch.rand(E, generator=g) < 0.5, -0.75 * high, 0.1))
+    fn = check_many if many else check
+    for bias in groups:
+        for tg in (1, 3, 4, 7):
+            for best in (1, 2):
+                fn(rows, bias, k, scoring=scoring, n_group=G, topk_group=tg, group_best=best)

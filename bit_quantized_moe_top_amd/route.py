@@ -13,7 +13,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import MAX_EXPERTS, MAX_TOPK, lib
-from .mx import _CALL, _float_dtype, _launch, _output, _tensor
+from .mx import _CALL, _INT_MAX, _float_dtype, _launch, _output, _tensor
 
 __all__ = ["SCORE_SOFTMAX", "SCORE_SIGMOID", "MAX_GROUPS", "ROUTE_SYMBOLS", "moe_route_experts"]
 
@@ -67,6 +67,8 @@ def moe_route_experts(logits: torch.Tensor, k: int, scoring: int = SCORE_SOFTMAX
     if logits.dim() != 2:
         raise ValueError(f"logits must be [T, E], got {tuple(logits.shape)}")
     T, E = logits.shape
+    if T > _INT_MAX:
+        raise ValueError(f"{T} tokens are too many")
     ld = logits.stride(0) if T > 1 else E
     if (E > 1 and logits.stride(1) != 1) or ld < E:
         raise ValueError("logits must have contiguous rows that do not overlap")

@@ -109,3 +109,21 @@ def test_binding_refusals_without_a_gpu():
         mq.moe_route_experts(z.half(), 2)
     with pytest.raises(TypeError, match="float32 or bfloat16"):
         mq.moe_route_experts(z.double(), 2)
+
+
+def test_more_tokens_than_32_bits_are_refused(monkeypatch):
+    """Not cut down to their low 32 bits on the way into the library."""
+    import bit_quantized_moe_top_amd.route as route
+
+    class OnDevice(torch.Tensor):
+        def get_device(self):
+            return 0
+
+    calls = []
+    monkeypatch.setattr(route, "_launch", lambda *args: calls.append(args))
+    monkeypatch.setattr(route, "_output", lambda t, *args: torch.empty(0))
+    T = 2 ** 32 + 5
+    z = torch.empty(T, 1, dtype=torch.bfloat16).as_subclass(OnDevice)        # (memory that nothing touches)
+    with pytest.raises(ValueError, match="too many"):
+        mq.moe_route_experts(z, 1)
+    assert not calls

@@ -55,6 +55,8 @@ def moe_adapter_plan(ids: torch.Tensor, n_adapters: int,
 
 
 def moe_shared_gemm_lora_ws_size(M: int, N: int, K: int, L: int, slices: int, r: int) -> int:
+    if not 0 <= min(M, N, K, L, slices, r) <= max(M, N, K, L, slices, r) <= _INT_MAX:
+        return 0                         # refused, as by the call itself
     return lib.moe_shared_gemm_lora_ws_size(M, N, K, L, slices, r)
 
 
@@ -89,7 +91,7 @@ def moe_shared_gemm_lora_bf16(a: torch.Tensor, w: torch.Tensor, lora_a: torch.Te
     if lora_b.shape != (L, N, r) or scale.shape[0] != L:
         raise ValueError(f"lora_a [L, slices, r, K], lora_b [L, N, r] and scale [L] do not match: "
                          f"{tuple(lora_a.shape)}, {tuple(lora_b.shape)}, {tuple(scale.shape)}")
-    if max(M, N, K) > _INT_MAX:
+    if max(M, N, K, L, slices, r) > _INT_MAX:
         raise ValueError("sizes past 32 bits")
     ld = a.stride(0) if M > 1 else (K + 7) // 8 * 8
     if (K > 1 and a.stride(1) != 1) or ld < K:

@@ -131,3 +131,34 @@ def test_binding_refusals_without_a_gpu():
         mq.moe_adapter_plan(torch.zeros(4, dtype=torch.int32), 2)
     with pytest.raises(TypeError, match="int32"):
         mq.moe_adapter_plan(torch.zeros(4, dtype=torch.int64), 2)
+
+
+def test_sizes_past_32_bits_are_refused(monkeypatch):
+    """Not cut down to their low 32 bits on the way into the library."""
+    import bit_quantized_moe_top_amd.lora as lora
+    size = mq.moe_shared_gemm_lora_ws_size
+    good = [10, 96, 64, 3, 1, 8]
+    assert size(*good) > 0
+    for i in range(len(good)):
+        for by in (2 ** 32, -2 ** 32):
+            bad = list(good)
+            bad[i] += by
+            assert size(*bad) == 0, bad
+
+    class OnDevice(torch.Tensor):
+        def get_device(self):
+            return 0
+
+    calls = []
+    monkeypatch.setattr(lora, "_launch", lambda *args: calls.append(args))
+    monkeypatch.setattr(lora, "_output", lambda t, *args: torch.empty(0))
+    none = torch.empty(0)                                        # (memory that nothing touches)
+    bf = dict(dtype=torch.bfloat16)
+    for L, S, r, n in ((1, 1, 2 ** 32 + 8, 0), (1, 2 ** 32 + 1, 8, 0), (2 ** 32 + 1, 1, 8, 0)):
+        a, w = torch.empty(10, n, **bf), torch.empty(n, n, **bf)
+        la, lb = torch.empty(L, S, r, n, **bf), torch.empty(L, n, r, **bf)
+        sc, plan, ws = torch.empty(L), torch.empty(4, dtype=torch.int32), torch.empty(8, dtype=torch.uint8)
+        args = [t.as_subclass(OnDevice) for t in (a, w, la, lb, sc, plan)]
+        with pytest.raises(ValueError, match="past 32 bits"):
+            mq.moe_shared_gemm_lora_bf16(*args, out=none, ws=ws.as_subclass(OnDevice))
+    assert not calls

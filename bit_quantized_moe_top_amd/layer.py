@@ -119,7 +119,10 @@ class MoELayer:
 
     # ---------------------------------------------------------------- buffers
     def buffers(self, T: int) -> dict:
-        b = self._bufs.get(T)
+        # the shared experts' width is part of the key: set_shared may come after a call, and the
+        # earlier buffers stay, since a captured graph may hold them
+        S = 0 if self.ws13 is None else self.ws2.shape[1]
+        b = self._bufs.get((T, S))
         if b is None:
             H, I, E, k, d = self.H, self.I, self.E, self.k, self.device
             R = T * k
@@ -139,10 +142,9 @@ class MoELayer:
                 "y": torch.empty(T, H, dtype=torch.bfloat16, device=d),
             }
             if self.ws13 is not None:
-                S = self.ws2.shape[1]
                 b["sh_h"] = torch.empty(T, S, dtype=torch.bfloat16, device=d)
                 b["shared"] = torch.empty(T, H, dtype=torch.bfloat16, device=d)
-            self._bufs[T] = b
+            self._bufs[T, S] = b
         return b
 
     def _lora_ws(self, T: int) -> torch.Tensor:

@@ -257,7 +257,8 @@ class HybridMoELayer(MoELayer):
     Cold slabs: per projection a list of code tensors ([n_cold, out, in/8], one
                 per book), the list of fp16 codebooks [entries, 8], and the fp16
                 row scales [n_cold, out].
-    Each GEMM step runs both formats' kernels; each fills only its experts' rows.
+    Each GEMM step runs both formats' kernels; each fills only its experts' rows.  Shared experts
+    and their adapters as in MoELayer.
     """
 
     def __init__(self, H: int, I: int, E: int, k: int, renormalize: bool = True, device="cuda"):
@@ -294,7 +295,8 @@ class HybridMoELayer(MoELayer):
     @_on_x_device
     def forward(self, x: torch.Tensor, logits: Optional[torch.Tensor] = None,
                 bias: Optional[torch.Tensor] = None, return_all: bool = False,
-                events: Optional[list] = None, split_mlp: bool = True):
+                events: Optional[list] = None, split_mlp: bool = True,
+                adapter_plan: Optional[torch.Tensor] = None):
         T = x.shape[0]
         b = self.buffers(T)
 
@@ -317,7 +319,8 @@ class HybridMoELayer(MoELayer):
              EPI_SILU_MUL, b["h"])
         step("quant_h", quant_fp8_per_token, b["h"], q=b["h_q"], scale=b["h_s"])
         step("gemm_down", self._gemm_both, b["h_q"], b["h_s"], b["plan"], "w2", EPI_NONE, b["o"])
-        step("combine", moe_combine, b["o"], b["plan"], b["w"], None, y=b["y"], E=self.E)
+        shared = self._shared(x, b, step, adapter_plan)
+        step("combine", moe_combine, b["o"], b["plan"], b["w"], shared, y=b["y"], E=self.E)
         return b if return_all else b["y"]
 
     __call__ = forward

@@ -215,3 +215,64 @@ def test_batches_of_two_sizes_and_two_streams_have_their_own_workspaces():
     torch.cuda.synchronize()
     for (s, *_), ref in zip(args, refs):
         assert torch.equal(s.layer.buffers(5)["y"], ref)
+
+
+@pytest.mark.parametrize("routed", [False, True])
+def test_hybrid_layer_with_shared_experts_and_adapters(routed):
+    cfg = W.get_config("hybrid_tiny")
+    inp = W.make_layer_inputs(cfg, device="cpu")
+    hot_ids, cold_ids = W.hybrid_partition(cfg)
+    layer = mq.HybridMoELayer(cfg.H, cfg.I, cfg.E, cfg.k, device=DEV)
+    to = lambda d: {k: [t.to(DEV) for t in v] if isinstance(v, list) else v.to(DEV)  # noqa: E731
+                    for k, v in d.items()}
+    layer.set_hybrid_weights(hot_ids, cold_ids, to(W.make_nvfp4_slabs(cfg, len(hot_ids), device="cpu")),
+                             to(W.make_aqlm_slabs(cfg, len(cold_ids), device="cpu")))
+    if routed:
+        layer.set_routing(mq.SCORE_SIGMOID, n_group=2, topk_group=1)
+    x, logits = inp["x"].to(BF).to(DEV), inp["logits"].to(DEV)
+    bare = {n: t.clone() for n, t in layer.forward(x, logits, return_all=True).items()}
+    s = Set(cfg.T)                                      # shared experts, adapters and ids of H = 256
+    assert cfg.H == H
+    a13, b13, a2, b2, scale = [t.to(DEV) for t in s.adapters]
+    layer.set_shared(*[t.to(DEV) for t in s.shared])
+    layer.set_shared_adapters(a13, b13, a2, b2, scale)
+    plan = s.plan()
+    for p in (None, plan):
+        b = layer.forward(x, logits, return_all=True, adapter_plan=p)
+        if p is None:
+            h = mq.moe_shared_gemm_bf16(x, layer.ws13, mq.EPI_SILU_MUL)
+            sh = mq.moe_shared_gemm_bf16(h, layer.ws2)
+        else:
+            h = mq.moe_shared_gemm_lora_bf16(x, layer.ws13, a13, b13, scale, plan, mq.EPI_SILU_MUL)
+            sh = mq.moe_shared_gemm_lora_bf16(h, layer.ws2, a2, b2, scale, plan)
+        assert torch.equal(b["shared"], sh) and sh.abs().max() > 0
+        for n in ("ids", "w", "o"):
+            assert torch.equal(b[n], bare[n]), n
+        assert torch.equal(b["y"], mq.moe_combine(b["o"], b["plan"], b["w"], sh, E=cfg.E))
+        assert not torch.equal(b["y"], bare["y"])
+    layer.set_shared(None, None)
+    assert torch.equal(layer.forward(x, logits), bare["y"])
+
+
+@pytest.mark.parametrize("kind", ["w4a8", "fp8row", "mxfp4"])
+def test_shared_experts_set_after_a_call(kind):
+    s = Set(9, kind)
+    x, logits, bias = s.batch()
+    expect = s.layer.forward(x, logits, bias, adapter_plan=s.plan()).clone()
+    late = Set(9, kind)
+    late.layer.set_shared(None, None)
+    late.layer.set_shared_adapters(None)
+    plain = late.layer.forward(x, logits, bias).clone()
+    late.layer.set_shared(*[t.to(DEV) for t in late.shared])
+    late.layer.set_shared_adapters(*[t.to(DEV) for t in late.adapters])
+    assert torch.equal(late.layer.forward(x, logits, bias, adapter_plan=late.plan()), expect)
+    late.layer.set_shared(None, None)
+    assert torch.equal(late.layer.forward(x, logits, bias), plain)
+
+
+@pytest.mark.parametrize("kind", ["w4a8", "fp8row", "mxfp4"])
+def test_no_tokens(kind):
+    s = Set(3, kind)
+    x, logits, bias = s.batch()
+    plan = mq.moe_adapter_plan(s.ids[:0].to(DEV), L)
+    assert s.layer.forward(x[:0], logits[:0], bias, adapter_plan=plan).shape == (0, H)

@@ -78,3 +78,24 @@ def test_shared_experts_and_adapters_set_after_a_call(kind, calls):
             layer.forward(x, logits, adapter_plan=p)
             name = "moe_shared_gemm_bf16" if p is None else "moe_shared_gemm_lora_bf16"
             assert [c[2]["out"].shape for c in calls if c[0] == name] == [(T, S), (T, H)]
+
+
+@pytest.mark.parametrize("kind", ["w4a8", "fp8row", "hybrid", "mxfp4"])
+def test_every_layer_adds_its_shared_experts(kind, calls):
+    layer = make(kind)
+    x, logits, plan = torch.zeros(T, H, dtype=BF).as_subclass(Host), torch.zeros(T, E), object()
+    layer.set_shared(*shared(96))
+    with pytest.raises(ValueError, match="set_shared_adapters"):
+        layer.forward(x, logits, adapter_plan=plan)
+    layer.set_shared_adapters(*adapters(96))
+    for p in (None, plan):
+        calls.clear()
+        layer.forward(x, logits, adapter_plan=p)
+        down = [c for c in calls if c[0].startswith("moe_shared_gemm")][-1]
+        combine = [c for c in calls if c[0] == "moe_combine"]
+        assert len(combine) == 1 and combine[0][1][3] is down[2]["out"]
+        assert down[0] == ("moe_shared_gemm_bf16" if p is None else "moe_shared_gemm_lora_bf16")
+    layer.set_shared(None, None)
+    calls.clear()
+    layer.forward(x, logits)
+    assert [c[1][3] for c in calls if c[0] == "moe_combine"] == [None]

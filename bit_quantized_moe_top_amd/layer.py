@@ -149,9 +149,10 @@ class MoELayer:
 
     def _lora_ws(self, T: int) -> torch.Tensor:
         """The workspace of the shared experts' two products with adapters, one per batch size and
-        set of shapes (earlier ones stay, since a captured graph may hold them)."""
-        a13, b13, a2, b2, _ = self.adapters
-        key = (T, self.ws13.shape, self.ws2.shape, a13.shape, a2.shape)
+        set of shapes, whatever the number of adapters, which its size does not depend on (earlier
+        ones stay, since a captured graph may hold them)."""
+        a13, _, a2, _, _ = self.adapters
+        key = (T, self.ws13.shape, self.ws2.shape, a13.shape[1:], a2.shape[1:])
         ws = self._adapter_ws.get(key)
         if ws is None:
             n = max(moe_shared_gemm_lora_ws_size(T, *w.shape, *a.shape[:3])

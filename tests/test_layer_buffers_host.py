@@ -99,3 +99,28 @@ def test_every_layer_adds_its_shared_experts(kind, calls):
     calls.clear()
     layer.forward(x, logits)
     assert [c[1][3] for c in calls if c[0] == "moe_combine"] == [None]
+
+
+def test_adapter_workspaces_by_what_they_hold():
+    """Loading more adapters of the same shapes starts no further workspace; one batch size and one
+    width each have their own."""
+    layer = make("w4a8")
+    layer.set_shared(*shared(96))
+    layer.set_shared_adapters(*adapters(96))
+    ws = layer._lora_ws(T)
+    for n in (1, 7, 200):
+        layer.set_shared_adapters(*adapters(96, n))
+        assert layer._lora_ws(T) is ws
+    assert layer._lora_ws(T + 1) is not ws
+    layer.set_shared(*shared(416))
+    layer.set_shared_adapters(*adapters(416))
+    wide = layer._lora_ws(T)
+    for w, a in ((layer.ws13, layer.adapters[0]), (layer.ws2, layer.adapters[2])):
+        assert wide.numel() >= mq.moe_shared_gemm_lora_ws_size(T, *w.shape, *a.shape[:3])
+    assert wide.numel() > ws.numel()
+    layer.set_shared(*shared(96))
+    layer.set_shared_adapters(*adapters(96))
+    assert all(mq.moe_shared_gemm_lora_ws_size(m, 4096, 2048, n, 2, 16) ==
+               mq.moe_shared_gemm_lora_ws_size(m, 4096, 2048, 1, 2, 16)
+               for m in (1, 40, 64, 65, 300, 1000, 5000) for n in (2, 30, 1000))
+    assert layer._lora_ws(T) is ws                       # (a captured graph may hold it)

@@ -48,7 +48,7 @@ int moe_adapter_plan(const int32_t* ids, int M, int L, void* plan, size_t plan_b
 
 size_t moe_shared_gemm_lora_ws_size(int M, int N, int K, int L, int slices, int r) {
   const moeq::LoraShape s = {M, N, K, L, slices, r, K, MOEQ_EPI_NONE};
-  return check_shape(s) ? 0 : moeq::lora_ws_bytes(s);
+  return check_shape(s) ? 0 : moeq::lora_path(s).ws_bytes();
 }
 
 int moe_shared_gemm_lora_bf16(const uint16_t* a, int64_t ld_a, const uint16_t* w, int M, int N,
@@ -66,7 +66,7 @@ int moe_shared_gemm_lora_bf16(const uint16_t* a, int64_t ld_a, const uint16_t* w
       !aligned16(out) || !aligned_to(scale, 4) || !aligned_to(ws, 256))
     return MOEQ_ERR_INVALID_ARG;
   if (int rc = check_plan(plan, plan_bytes, L + 1, M)) return rc;
-  const size_t need = moeq::lora_ws_bytes(s);
+  const size_t need = moeq::lora_path(s).ws_bytes();
   if (ws_bytes < need) return MOEQ_ERR_WORKSPACE;
   // what is written must not lie over what is read
   const int64_t cols = epilogue == MOEQ_EPI_SILU_MUL ? N / 2 : N;

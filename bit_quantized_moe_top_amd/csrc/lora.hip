@@ -85,7 +85,7 @@ __device__ __forceinline__ int plan_row(const PlanView& pv, int p, int M) {
 // in flight at once: the launch is a chain of memory latencies, not of work (2048 rows x 32 columns,
 // K = 4096: 11.3 us, 17 MB; 777 x 24, K = 1448: 4.7).
 constexpr int kShrinkRows = 32, kShrinkCols = 32;
-constexpr int kShrinkPiece = 128, kShrinkSteps = kShrinkPiece / 32;
+constexpr int kShrinkSteps = kShrinkPiece / 32;
 
 // Workgroups of one launch: (plan tile and its 32-row part, 32 columns, split of K)
 struct ShrinkGrid {
@@ -173,7 +173,7 @@ __device__ __forceinline__ int adapter_at(const PlanView& pv, int L, int p, int 
 
 // ------------------------------------------------------- operands through LDS
 // Rows of 64 K, one 128-byte line each, loaded straight into LDS.
-constexpr int kSlotK = 64, kRowB = 2 * kSlotK;
+constexpr int kRowB = 2 * kSlotK;
 
 // Position of 16-byte chunk c of a 128-byte LDS row r: c ^ swz(r).  The 16 rows x 2 chunks that
 // 32 lanes of an operand read take are then 32 different 16-byte slots modulo 512 bytes.
@@ -400,7 +400,6 @@ __device__ __forceinline__ void add_adapters(v4f (&acc)[T::kM][T::kN], const Pla
 // What a launch of the tile kernel does: the whole projection; a split of K of the product, to parts
 // (with the shrink); or the join of the parts, the adapters and the epilogue.
 enum TileMode { kWhole, kParts, kJoin };
-constexpr int kMaxSplits = 4;
 
 template <int EPI, typename T, TileMode MODE>
 __global__ void __launch_bounds__(T::kThreads, 2)
@@ -667,14 +666,10 @@ lora_gemm_kernel(LoraArgs args, LoraShape s, float* __restrict__ u, v4f* __restr
 // and applies the epilogue.
 //
 // Parts are stored as the matrix instruction leaves them: 16 bytes per lane, 1 KB per block.
-//
-// Against the tiles, us: 33 rows x 8192 x 4096 22.9 against 26.9, 48 rows 24.6 and 28.0, 64 rows 27.6 and
-// 29.9, 64 rows of rank 64 x 4096 x 4096 23.4 and 32.5.
-constexpr int kFewRows = 64, kFewCols = 64;
 
 // u parts: a wave takes 16 rows of one adapter x 16 columns x a piece of 512 K (several, if there
 // are more than 16)
-constexpr int kUPiece = 512, kUSteps = kUPiece / 32, kUSplits = 16;
+constexpr int kUSteps = kUPiece / 32;
 
 // the plan's tiles by lane: all of them (at most 64 of up to 64 rows), or those from sorted row p0's on
 struct FewPlan {
@@ -1072,8 +1067,6 @@ lora_join_kernel(LoraArgs args, LoraShape s, const float* __restrict__ u,
 // Everything in one launch: a workgroup forms 16 rows x 64 output columns, a wave 16 of them (of the gate
 // and the up half with SILU_MUL) over all of K, whose operands go out at once.  u of the 16 rows is formed
 // by every workgroup that needs it, the adapters' pieces of 16 ranks dealt over its waves.
-constexpr int kShortK = 256, kShortItems = 8, kShortGrid = 768;
-
 template <int EPI>
 __global__ void __launch_bounds__(256)
 lora_short_kernel(LoraArgs args, LoraShape s) {
@@ -1208,18 +1201,6 @@ lora_short_kernel(LoraArgs args, LoraShape s) {
     *reinterpret_cast<uint2*>(args.out + int64_t(plan_row(pv, p0 + p, s.M)) * cols + n0 + (ln & 12)) = four;
 }
 
-// One launch for K up to 256, if a workgroup has at most 8 pieces of 16 ranks to form (two a wave; an
-// adapter per row at most) and the workgroups, which all read x and W, fit the card in one go.  us in one
-// launch against two: 3 rows x 192 x 256 5.7 and 7.2 (with the host's time 8.6 and 11.8), 64 x 4096 x 256
-// 7.6 and 12.6, 512 x 1024 x 256 8.3 and 12.5, 1024 x 512 x 64 8.1 and 11.9; 16 rows x 1024 x 256 with 4 / 8 /
-// 16 pieces 7.1 / 8.3 / 10.7 against 9.1 / 9.2 / 9.3, 16 x 1024 x 64 with 32 15.0 and 11.6; 768 workgroups
-// (192 x 4096 x 256) 11.3 and 15.0, 1024 (256 x 4096 x 128) 15.4 and 9.7.  K = 512 with operands of all of K
-// in flight (16 x 1024): 10.4 and 9.2.
-bool is_short(const LoraShape& s) {
-  const int64_t cols = s.epilogue == MOEQ_EPI_SILU_MUL ? s.N / 2 : s.N;
-  return s.K <= kShortK && std::min(s.L, std::min(s.M, 16)) * ((s.slices * s.r + 15) / 16) <= kShortItems &&
-         int64_t((s.M + 15) / 16) * ((cols + 63) / 64) <= kShortGrid;
-}
 hipError_t launch_short(const LoraArgs& args, const LoraShape& s, hipStream_t stream) {
   const bool silu = s.epilogue == MOEQ_EPI_SILU_MUL;
   const int cols = silu ? s.N / 2 : s.N;
@@ -1227,36 +1208,6 @@ hipError_t launch_short(const LoraArgs& args, const LoraShape& s, hipStream_t st
   hipLaunchKernelGGL(fn, dim3(unsigned((cols + 63) / 64), unsigned((s.M + 15) / 16)), dim3(256),
                      unsigned(16 * join_u_row(s.slices, s.r)), stream, args, s);
   return hipGetLastError();
-}
-
-size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
-
-// Splits of K of the few-row product: 16 slots (1024 K) each, as that is long enough for a ring's start
-// to weigh little and short enough for the parts (8 bytes of traffic an element and split), but at least
-// 128 workgroups and at most 8 splits, which the join loads at once.  us by splits 2 / 3 / 4 / 8:
-// 16 rows x 8192 x 4096 22.9 / 20.7 / 20.0 / 22.5, 64 x 4096 x 4096 23.5 / 20.6 / 18.4 / 20.0, 16 x 2048 x
-// 2048 10.8 / 10.4 / 10.1 / 11.7, 16 x 1024 x 4096 13.8 / 12.4 / 10.9 / 10.2, 16 x 2048 x 8192 21.8 / 18.0 /
-// 16.8 / 15.7, 1 x 16384 x 4096 37.5 / 30.7 / 29.9 / 33.5.
-// Splits of u: one piece each.  16 splits against 4: 18.8 against 20.8 us for 1 row, 20.0 against 21.6
-// for 16 (x 8192 x 4096).
-struct FewSplit {
-  int splits, slots;                                     // slots of 64 K per split
-  int u_splits, u_pieces;                                // pieces of 512 K per split of u
-};
-FewSplit few_split(const LoraShape& s) {
-  const int ntiles = (s.N + kFewCols - 1) / kFewCols;
-  const int slots = s.K / kSlotK > 0 ? s.K / kSlotK : 1;
-  const int want = std::min(slots, std::min(8, std::max(slots / 16, (128 + ntiles - 1) / ntiles)));
-  const int per = (slots + want - 1) / want;
-  const int pieces = (s.K + kUPiece - 1) / kUPiece;
-  const int u_per = (pieces + kUSplits - 1) / kUSplits;
-  return {(slots + per - 1) / per, per, (pieces + u_per - 1) / u_per, u_per};
-}
-size_t few_u_bytes(const LoraShape& s) {
-  return align256(size_t(few_split(s).u_splits) * s.M * s.slices * s.r * sizeof(float));
-}
-size_t few_part_bytes(const LoraShape& s) {
-  return size_t(few_split(s).splits) * ((s.M + 15) / 16 * 16) * s.N * sizeof(float);
 }
 
 template <bool kFew>
@@ -1272,139 +1223,80 @@ hipError_t launch_join(const LoraArgs& args, const LoraShape& s, const float* u,
 }
 
 template <int MB>
-hipError_t launch_few(const LoraArgs& args, const LoraShape& s, hipStream_t stream) {
-  const FewSplit fs = few_split(s);
-  float* u = static_cast<float*>(args.ws);
-  v4f* parts = reinterpret_cast<v4f*>(static_cast<uint8_t*>(args.ws) + few_u_bytes(s));
+hipError_t launch_few(const LoraArgs& args, const LoraShape& s, const LoraPath& path, float* u, v4f* parts,
+                      hipStream_t stream) {
   const int reached = s.L < s.M ? s.L : s.M;             // adapters that have rows, at most
   const int row_pieces = reached + s.M / 16 < s.M ? reached + s.M / 16 : s.M;
-  const int u_cols = (s.slices * s.r + 15) / 16, items = row_pieces * u_cols * fs.u_splits;
+  const int u_cols = (s.slices * s.r + 15) / 16, items = row_pieces * u_cols * path.u_splits;
   const int ntiles = (s.N + kFewCols - 1) / kFewCols;
   const unsigned lds = few_ring<MB>() * few_slot_bytes<MB>();
   static_assert(few_ring<MB>() * few_slot_bytes<MB>() <= 64 * 1024, "no attribute needed");
-  hipLaunchKernelGGL(lora_few_kernel<MB>, dim3(unsigned((items + 3) / 4 + ntiles * fs.splits)), dim3(256),
-                     lds, stream, args, s, u, parts, items, u_cols, fs.u_splits, fs.u_pieces, fs.slots);
+  hipLaunchKernelGGL(lora_few_kernel<MB>, dim3(unsigned((items + 3) / 4 + ntiles * path.splits)), dim3(256),
+                     lds, stream, args, s, u, parts, items, u_cols, path.u_splits, path.u_pieces, path.slots);
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  return launch_join<true>(args, s, u, parts, fs.splits, fs.u_splits, stream);
+  return launch_join<true>(args, s, u, parts, path.splits, path.u_splits, stream);
 }
 
-// The grid of the shrink.  Splits of K, at most 4 (add_adapters): for up to 4096 rows, whose blocks
-// of 32 alone would leave CUs idle.  Call, us, by splits 1 / 2 / 4: 777 rows x 1504 x 1448 23.2 / 22.0 /
-// 20.9, 1024 x 8192 x 4096 93.6 / 87.3 / 84.7, 2048 x 8192 x 4096 135.8 / 129.0 / 130.1, 8192 x 4096 x
-// 4096 274.0 / 275.5 / 279.1.
-ShrinkGrid shrink_grid(const LoraShape& s) {
-  const int pieces = (s.K + 4 * kShrinkPiece - 1) / (4 * kShrinkPiece);
+ShrinkGrid shrink_grid(const LoraShape& s, const LoraPath& path) {
   return {plan_max_tiles(s.L + 1, s.M) * (MOEQ_TILE_M / kShrinkRows),
-          (s.slices * s.r + kShrinkCols - 1) / kShrinkCols, s.M > 4096 ? 1 : pieces < 4 ? pieces : 4};
-}
-
-int64_t tiles_of(const LoraShape& s, int bm, int bn) {
-  return int64_t((s.M + bm - 1) / bm) * ((s.N + bn - 1) / bn);
-}
-
-// Parts are joined by lora_join_kernel up to this many of its workgroups, by 64 x 64 tiles from there
-// on: its workgroups end sooner, but one per 16 rows and columns each read u and the plan (128 rows x
-// 2048, 1024 workgroups: 15.7 us for the call against 20.9; x 4096, 2048: 26.7 against 29.4; 192 rows of
-// gate/up 8192: 45.9 against 43.0; 256 rows, 4096: 51.7 against 44.9).
-constexpr int kJoinBlocks = 2400;
-
-// How more than 64 rows are multiplied: tiles of bm x bn by `groups` groups of waves, K split over `splits` workgroups (1: whole tiles, the shrink ahead of them).  The larger the tile the
-// fewer bytes reach LDS per product, and a CU takes in some 45 KB of them a microsecond whatever it has in
-// flight (rows that L2 has wait behind the w rows that it has not); but there are 256 CUs to fill.  So
-// the largest tile that is met often enough, and below that K is divided: between two groups of waves
-// of a workgroup while one tile a CU fills the card in one go, else between workgroups.  us, K = 4096,
-// one slice, 16 adapters mixed, rows x columns:
-//                 256   256x128   128   128, 2 groups   128 / 2   128 / 4   64    64 / 2   64 / 4
-//    2048 x 8192  128     141     160        182           240      310     330
-//    1280 x 8192  108     132     125        130           148      187     201
-//    1024 x 8192  105      75      83         95           116      150     154     202     231
-//     768 x 8192  106      70      79         93            94      112     120     142     172
-//     640 x 8192           65      76                       86               99
-//     512 x 8192  107      68      62         53            67       78      84      99     127
-//     512 x 4096  105              58         51            39       44      47      53      66
-//     256 x 8192  111              60         55            42       48      51      57      65
-//     128 x 8192  113              62         57            39       36      37      41      44
-//     128 x 4096  112              60         55            32       27      34      26      28
-//     128 x 2048  101              51         40            24       17      26      17      15
-// and 64 for short K while it fills the card: 512 x 4096 x 2048 25.5 against 27.2 (128, 2 groups) and
-// 27.6 (128 / 2); x 1024 19.4, 21.3, 21.5.
-struct TilePlan {
-  int bm, bn, groups, splits;
-};
-TilePlan tile_plan(const LoraShape& s) {
-  const int64_t t256 = tiles_of(s, 256, 256), t256x128 = tiles_of(s, 256, 128), t128 = tiles_of(s, 128, 128),
-                t64 = tiles_of(s, 64, 64);
-  if (t256 >= 150) return {256, 256, 1, 1};
-  if (t256x128 >= 150 && t256x128 <= 256) return {256, 128, 1, 1};
-  if (t128 >= 350) return {128, 128, 1, 1};
-  if (t64 >= 200 && s.K <= 2048) return {64, 64, 1, 1};
-  if (t128 >= 200 && t128 <= 256) return {128, 128, 2, 1};
-  if (t128 >= 64) return {128, 128, 1, t128 >= 128 ? 2 : 4};
-  return {64, 64, 1, t64 >= 100 ? 2 : 4};
-}
-size_t tile_u_bytes(const LoraShape& s) {
-  return align256(size_t(shrink_grid(s).splits) * s.M * s.slices * s.r * sizeof(float));
+          (s.slices * s.r + kShrinkCols - 1) / kShrinkCols, path.u_splits};
 }
 
 template <int EPI, typename T, TileMode MODE>
-hipError_t launch_tile_kernel(const LoraArgs& args, const LoraShape& s, float* u, v4f* parts, int splits,
-                              hipStream_t stream) {
+hipError_t launch_tile_kernel(const LoraArgs& args, const LoraShape& s, const LoraPath& path, float* u,
+                              v4f* parts, hipStream_t stream) {
   const auto fn = lora_gemm_kernel<EPI, T, MODE>;
   const hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void*>(fn),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds);
   if (err != hipSuccess) return err;
-  const ShrinkGrid sgrid = shrink_grid(s);
-  const int64_t tiles = tiles_of(s, T::BM, T::BN), blocks = MODE == kParts ? sgrid.blocks() + tiles * splits : tiles;
-  hipLaunchKernelGGL(fn, dim3(unsigned(blocks)), dim3(T::kThreads), T::kLds, stream, args, s, u, parts, splits,
-                     sgrid);
+  const ShrinkGrid sgrid = shrink_grid(s, path);
+  const int64_t tiles = tiles_of(s, T::BM, T::BN),
+                blocks = MODE == kParts ? sgrid.blocks() + tiles * path.splits : tiles;
+  hipLaunchKernelGGL(fn, dim3(unsigned(blocks)), dim3(T::kThreads), T::kLds, stream, args, s, u, parts,
+                     path.splits, sgrid);
   return hipGetLastError();
 }
 template <typename T, TileMode MODE>
-hipError_t launch_tiles(const LoraArgs& args, const LoraShape& s, float* u, v4f* parts, int splits,
+hipError_t launch_tiles(const LoraArgs& args, const LoraShape& s, const LoraPath& path, float* u, v4f* parts,
                         hipStream_t stream) {
   return s.epilogue == MOEQ_EPI_SILU_MUL
-             ? launch_tile_kernel<MOEQ_EPI_SILU_MUL, T, MODE>(args, s, u, parts, splits, stream)
-             : launch_tile_kernel<MOEQ_EPI_NONE, T, MODE>(args, s, u, parts, splits, stream);
+             ? launch_tile_kernel<MOEQ_EPI_SILU_MUL, T, MODE>(args, s, path, u, parts, stream)
+             : launch_tile_kernel<MOEQ_EPI_NONE, T, MODE>(args, s, path, u, parts, stream);
 }
 
 }  // namespace
 
-size_t lora_ws_bytes(const LoraShape& s) {
-  if (s.M <= kFewRows) return few_u_bytes(s) + align256(few_part_bytes(s)) + 256;
-  const TilePlan tp = tile_plan(s);
-  const size_t parts = tp.splits > 1 ? size_t(tp.splits) * ((s.M + 15) / 16 * 16) * s.N * sizeof(float) : 0;
-  return tile_u_bytes(s) + align256(parts);
-}
-
 hipError_t launch_shared_gemm_lora(const LoraArgs& args, const LoraShape& s, hipStream_t stream) {
   if (s.M == 0) return hipSuccess;
-  if (is_short(s)) return launch_short(args, s, stream);
-  if (s.M <= kFewRows)
-    return s.M <= 16 ? launch_few<1>(args, s, stream)
-                     : s.M <= 32 ? launch_few<2>(args, s, stream) : launch_few<4>(args, s, stream);
+  const LoraPath path = lora_path(s);
+  if (path.one_launch) return launch_short(args, s, stream);
   float* u = static_cast<float*>(args.ws);
-  v4f* parts = reinterpret_cast<v4f*>(static_cast<uint8_t*>(args.ws) + tile_u_bytes(s));
-  const TilePlan tp = tile_plan(s);
-  hipError_t err;
-  if (tp.splits > 1) {
-    err = tp.bm == 128
-              ? launch_tile_kernel<MOEQ_EPI_NONE, Tile<128, 128, 1>, kParts>(args, s, u, parts, tp.splits, stream)
-              : launch_tile_kernel<MOEQ_EPI_NONE, Tile<64, 64, 1>, kParts>(args, s, u, parts, tp.splits, stream);
-    if (err != hipSuccess) return err;
-    const int64_t join_blocks = int64_t((s.M + 15) / 16) * ((s.epilogue == MOEQ_EPI_SILU_MUL ? s.N / 2 : s.N) / 16);
-    return join_blocks <= kJoinBlocks ? launch_join<false>(args, s, u, parts, tp.splits, shrink_grid(s).splits, stream)
-                            : launch_tiles<Tile<64, 64, 1>, kJoin>(args, s, u, parts, tp.splits, stream);
+  v4f* parts = reinterpret_cast<v4f*>(static_cast<uint8_t*>(args.ws) + path.u_bytes);
+  if (path.few) {
+    static_assert(kFewRows <= 64, "four blocks of 16 rows");
+    return s.M <= 16 ? launch_few<1>(args, s, path, u, parts, stream)
+                     : s.M <= 32 ? launch_few<2>(args, s, path, u, parts, stream)
+                                 : launch_few<4>(args, s, path, u, parts, stream);
   }
-  const ShrinkGrid sgrid = shrink_grid(s);
+  hipError_t err;
+  if (path.splits > 1) {
+    err = path.bm == 128
+              ? launch_tile_kernel<MOEQ_EPI_NONE, Tile<128, 128, 1>, kParts>(args, s, path, u, parts, stream)
+              : launch_tile_kernel<MOEQ_EPI_NONE, Tile<64, 64, 1>, kParts>(args, s, path, u, parts, stream);
+    if (err != hipSuccess) return err;
+    return path.join_rows ? launch_join<false>(args, s, u, parts, path.splits, path.u_splits, stream)
+                          : launch_tiles<Tile<64, 64, 1>, kJoin>(args, s, path, u, parts, stream);
+  }
+  const ShrinkGrid sgrid = shrink_grid(s, path);
   hipLaunchKernelGGL(lora_shrink_kernel, dim3(unsigned(sgrid.blocks())), dim3(256), 0, stream, args, s, u,
                      sgrid);
   if ((err = hipGetLastError()) != hipSuccess) return err;
-  if (tp.bn == 256) return launch_tiles<Tile<256, 256, 1>, kWhole>(args, s, u, parts, 1, stream);
-  if (tp.bm == 256) return launch_tiles<Tile<256, 128, 1>, kWhole>(args, s, u, parts, 1, stream);
-  if (tp.bm == 64) return launch_tiles<Tile<64, 64, 1>, kWhole>(args, s, u, parts, 1, stream);
-  if (tp.groups == 2) return launch_tiles<Tile<128, 128, 2>, kWhole>(args, s, u, parts, 1, stream);
-  return launch_tiles<Tile<128, 128, 1>, kWhole>(args, s, u, parts, 1, stream);
+  if (path.bn == 256) return launch_tiles<Tile<256, 256, 1>, kWhole>(args, s, path, u, parts, stream);
+  if (path.bm == 256) return launch_tiles<Tile<256, 128, 1>, kWhole>(args, s, path, u, parts, stream);
+  if (path.bm == 64) return launch_tiles<Tile<64, 64, 1>, kWhole>(args, s, path, u, parts, stream);
+  if (path.groups == 2) return launch_tiles<Tile<128, 128, 2>, kWhole>(args, s, path, u, parts, stream);
+  return launch_tiles<Tile<128, 128, 1>, kWhole>(args, s, path, u, parts, stream);
 }
 
 }  // namespace moeq

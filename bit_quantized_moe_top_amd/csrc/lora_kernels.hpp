@@ -6,16 +6,10 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "../../include/moeq_lora.h"
 #include "kernels.hpp"
+#include "lora_paths.hpp"
 
 namespace moeq {
-
-struct LoraShape {
-  int M, N, K, L, slices, r;
-  int64_t ld_a;
-  int epilogue;
-};
 
 struct LoraArgs {
   const uint16_t *a, *w, *lora_a, *lora_b;
@@ -27,7 +21,6 @@ struct LoraArgs {
 
 hipError_t launch_adapter_plan(const int32_t* ids, int M, int L, void* plan, hipStream_t stream);
 
-size_t lora_ws_bytes(const LoraShape& s);
 hipError_t launch_shared_gemm_lora(const LoraArgs& args, const LoraShape& s, hipStream_t stream);
 
 }  // namespace moeq

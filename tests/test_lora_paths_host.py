@@ -1,5 +1,6 @@
 """Which kernels the shared projection with adapters takes for a shape (csrc/lora_paths.hpp, which is
-host code), and the workspace that they fill (no GPU)."""
+host code), and that the GPU tests compare every one of them with the oracle (no GPU)."""
+import itertools
 import os
 import random
 import shutil
@@ -8,6 +9,8 @@ import subprocess
 import pytest
 
 import bit_quantized_moe_top_amd as mq
+from test_gpu_lora import SHAPES
+from test_gpu_lora_paths import PATH_SHAPES
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CXX = shutil.which(os.environ.get("CXX", "g++"))
@@ -45,6 +48,46 @@ def paths(tmp_path_factory):
         assert len(got) == len(shapes)
         return got
     return ask
+
+
+def labels(shape, p):
+    """The kernels, by what their launch is compiled for, and the ways through them."""
+    M, _, _, _, _, r, epilogue = shape
+    rank = "r<=32" if r <= 32 else "r>32"
+    if p["one_launch"]:
+        return {("short", epilogue)}
+    if p["few"]:
+        rows = 1 if M <= 16 else 2 if M <= 32 else 4
+        return {("few", rows), ("few u", "one piece" if p["u_pieces"] == 1 else "more"),
+                ("few join", epilogue, rank)}
+    tile = (p["bm"], p["bn"], p["groups"])
+    found = {("shrink", p["u_splits"])}
+    if p["splits"] == 1:
+        return found | {("tile", tile, epilogue, rank)}
+    join = ("join rows", epilogue, rank) if p["join_rows"] else ("join tiles", epilogue, rank)
+    return found | {("parts", tile, p["splits"], p["join_rows"]), join}
+
+
+def with_epilogues(shapes):
+    return [s + (e,) for s in shapes for e in ((0, 1) if s[1] % 32 == 0 else (0,))]
+
+
+def test_every_path_is_compared_with_the_oracle(paths):
+    rng = random.Random(1)
+    rows = list(range(1, 80)) + [96, 128, 129, 160, 200, 256, 257, 300, 400, 513, 640, 777, 1000, 1500, 2048,
+                                 3000, 4096, 4097, 6000, 9000]
+    columns = [32 * n for n in (1, 2, 3, 8, 17, 30, 32, 47, 64, 96, 128, 160, 200, 256, 300, 400, 512, 640, 1024)]
+    depths = [8, 64, 256, 264, 1024, 1448, 2048, 2056, 4096, 8192, 8200, 9000, 16384]
+    drawn = [(M, N, rng.choice(depths), rng.choice((1, 5, 60)), rng.choice((1, 2)), r, e)
+             for M, N, r, e in itertools.product(rows, columns, (8, 32, 64, 256), (0, 1))]
+    reached, tested = set(), set()
+    for s, p in zip(drawn, paths(drawn)):
+        reached |= labels(s, p)
+    mine = with_epilogues(SHAPES + PATH_SHAPES)
+    for s, p in zip(mine, paths(mine)):
+        tested |= labels(s, p)
+    assert len(reached) >= 30
+    assert reached <= tested, sorted(map(str, reached - tested))
 
 
 def test_workspace_holds_what_the_launches_write(paths):

@@ -358,3 +358,37 @@ def test_groups_whose_sums_pass_the_largest_fp32(scoring, many):
         for tg in (1, 3, 4, 7):
             for best in (1, 2):
                 fn(rows, bias, k, scoring=scoring, n_group=G, topk_group=tg, group_best=best)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,E", [(2051, 64), (4097, 128), (8195, 256), (8198, 250), (5, 256), (130, 1024)])
+def test_rows_and_bias_off_alignment_and_bytes_around(T, E, dtype):
+    """Four tokens a wave (and one): row strides and starts off the wide loads' alignment, tokens that
+    are no multiple of four, and nothing written past the last."""
+    k = 8
+    g = gen(E + T)
+    data = torch.randn(T, E, generator=g).to(dtype).to(DEV)
+    data[::5, ::3] = -INF
+    shifted = torch.zeros(E + 1, device=DEV)
+    shifted[1:] = (torch.randn(E, generator=g) * 0.1).to(DEV)
+    ids = torch.full((T + 4, k), 77, dtype=torch.int32, device=DEV)
+    w = torch.full((T + 4, k), 77.0, device=DEV)
+    G = 8 if E % 8 == 0 else 5
+    for kw in (dict(scoring=SIGM, bias=shifted[1:]), dict(scoring=SOFT, renormalize=False),
+               dict(scoring=SIGM, bias=shifted[1:], n_group=G, topk_group=2, group_best=2)):
+        aligned = dict(kw)
+        if "bias" in kw:
+            aligned["bias"] = kw["bias"].clone()
+        ref = mq.moe_route_experts(data, k, **aligned)
+        for first, pad in ((0, 1), (0, 2), (0, 4), (1, 3), (2, 2), (4, 4), (1, 1)):
+            wide = torch.full((T, first + E + pad), INF, dtype=dtype, device=DEV)     # not to be read as scores
+            wide[:, first:first + E] = data
+            ids.fill_(77)
+            w.fill_(77.0)
+            got = mq.moe_route_experts(wide[:, first:first + E], k, ids=ids[1:T + 1], weights=w[1:T + 1], **kw)
+            assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1]), (first, pad)
+            for t in (ids, w):
+                assert (t[0] == 77).all() and (t[T + 1:] == 77).all()
+    rows = data[:40].cpu()
+    check(rows, shifted[1:].cpu(), k, scoring=SIGM, n_group=G, topk_group=2, group_best=2)
+    assert torch.equal(ref[0][:40].cpu(), mq.moe_route_experts(rows.to(DEV), k, **aligned)[0].cpu())

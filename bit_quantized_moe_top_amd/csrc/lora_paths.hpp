@@ -98,19 +98,43 @@ inline int64_t tiles_of(const LoraShape& s, int bm, int bn) {
 //     128 x 8192  113              62         57            39       36      37      41      44
 //     128 x 4096  112              60         55            32       27      34      26      28
 //     128 x 2048  101              51         40            24       17      26      17      15
-// and 64 for short K while it fills the card: 512 x 4096 x 2048 25.5 against 27.2 (128, 2 groups) and
-// 27.6 (128 / 2); x 1024 19.4, 21.3, 21.5.
+//    1024 x 9216  104             114
+//     600 x 12800 104     114      80
+//     300 x 19456 109     119      85
+//     256 x 18432 116      75      88        100            92             101
+//     512 x 7168           56      47         41            46              60      67
+//     512 x 6144           56      47         39            43              49      60
+//     512 x 4224           56      46         39            41              50      50
+//     100 x 65536 170     154     141
+//      72 x 40960 124     133     104        119           121             101     121
+//      72 x 20480 110      72      68         64            69              64      67
+//      72 x 16384 110      68      65         59            50              55      56
+// and at K = 1024:
+//    1024 x 9216   46              43
+//     600 x 12800  47      45      30
+//     256 x 18432  60*     37*     39*        47*           50*             44*           (* K = 1536)
+//     512 x 8192                              22                            29
+//     512 x 7168           28      24         22            28              28      35
+//     512 x 4224           27      23         21            25              25      27
+//     512 x 4096           27      23         21            19              19      23
+//      72 x 20480  48      31      29         25            30              28      33
+// Tiles of 128 rows and columns take half of a CU: up to 512 of them are one go, and quicker than larger
+// tiles that one go of 256 does not fill; a tile of 256 rows for up to 128 is half empty.  From 129 to 199
+// of them at long K groups and splits are within a tenth, either way by the adapters' ranks (512 x 6144
+// 39.3 and 43.4 with rank 16, 512 x 4224 with two slices of rank 64 91 and 84).  Tiles that the last rows
+// leave mostly empty weigh less: hence the bound on tiles of 64 (300 x 6400, 150 tiles of 128 and 500 of 64,
+// K = 2048: 26.2 in groups, 24.1 in tiles of 64).  64 for short K while it fills the card: 512 x 4096 x
+// 2048 24.2 against 26.5 (128, 2 groups) and 23.5 (128 / 2); x 1024 18.7, 21.0, 18.9.
 struct TilePlan {
   int bm, bn, groups, splits;
 };
 inline TilePlan tile_plan(const LoraShape& s) {
   const int64_t t256 = tiles_of(s, 256, 256), t256x128 = tiles_of(s, 256, 128), t128 = tiles_of(s, 128, 128),
                 t64 = tiles_of(s, 64, 64);
-  if (t256 >= 150) return {256, 256, 1, 1};
-  if (t256x128 >= 150 && t256x128 <= 256) return {256, 128, 1, 1};
-  if (t128 >= 350) return {128, 128, 1, 1};
+  if (t128 > 512 && s.M > 128 && (t256 >= 150 || s.K > 2048)) return {256, 256, 1, 1};
+  if (t128 > 256) return t256x128 <= 256 ? TilePlan{256, 128, 1, 1} : TilePlan{128, 128, 1, 1};
+  if (t64 > 512 && (t128 >= 200 || s.M <= 128 || s.K <= 2048)) return {128, 128, 2, 1};
   if (t64 >= 200 && s.K <= 2048) return {64, 64, 1, 1};
-  if (t128 >= 200 && t128 <= 256) return {128, 128, 2, 1};
   if (t128 >= 64) return {128, 128, 1, t128 >= 128 ? 2 : 4};
   return {64, 64, 1, t64 >= 100 ? 2 : 4};
 }

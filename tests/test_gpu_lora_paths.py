@@ -17,7 +17,9 @@ PATH_SHAPES = [
     # 64 x 64 tiles with K in two parts, joined by rows and by tiles, and in four, most of them empty
     (129, 2176, 520, 5, 1, 40), (1100, 832, 2056, 20, 2, 24), (90, 544, 72, 5, 2, 24),
     # whole tiles of 128 and of 64
-    (1100, 6720, 136, 4, 1, 16), (1100, 6720, 72, 4, 2, 40), (1300, 704, 264, 4, 2, 40),
+    (1100, 6720, 136, 4, 1, 16), (1100, 6720, 72, 4, 2, 40), (1300, 704, 264, 4, 2, 40), (1300, 704, 264, 4, 2, 16),
+    # one tile of 128 rows and very many columns, whole and by groups; one of 256
+    (100, 33056, 72, 5, 2, 16), (72, 16672, 136, 4, 1, 24), (250, 16672, 72, 9, 1, 16),
     # u in one part for more than 4096 rows; few rows with several pieces of K in a part of u
     (4200, 96, 264, 5, 1, 16), (5, 64, 8712, 3, 2, 16), (40, 96, 16456, 50, 1, 40),
 ]

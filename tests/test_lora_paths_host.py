@@ -110,3 +110,22 @@ def test_workspace_holds_what_the_launches_write(paths):
             assert M > 64 and p["splits"] <= 4 and p["u_splits"] <= 4
         if p["few"] or p["splits"] > 1:
             assert p["part_bytes"] >= 4 * p["splits"] * (-(-M // 16) * 16) * N
+
+
+def test_tiles_follow_the_rows_that_there_are(paths):
+    """No tile of 256 rows for up to 128; no split of K past one go of whole tiles of 128; whole
+    halves by groups, not splits, for rows of one tile."""
+    for M, N, K in ((65, 20480, 4096), (100, 32768, 1024), (128, 40960, 4096), (128, 1 << 18, 520), (72, 1 << 20, 520)):
+        assert paths([(M, N, K, 5, 1, 16, 0)])[0]["bm"] <= 128, (M, N, K)
+    for M, N, K in ((256, 18432, 4096), (256, 16640, 4096), (512, 9216, 4096), (768, 6144, 4096), (100, 36864, 4096),
+                    (300, 19456, 4096), (600, 12800, 1024)):
+        p = paths([(M, N, K, 5, 1, 16, 0)])[0]
+        assert p["splits"] == p["groups"] == 1 and (p["bm"], p["bn"]) in ((128, 128), (256, 128)), (M, N, K, p)
+    for M, N, K in ((72, 20480, 4096), (128, 17408, 4096), (512, 7168, 1024), (512, 4224, 2048), (300, 9728, 4096)):
+        assert paths([(M, N, K, 5, 1, 16, 0)])[0]["groups"] == 2, (M, N, K)
+    for M, N, K, bm, bn, groups, splits in ((2048, 8192, 4096, 256, 256, 1, 1), (1024, 8192, 4096, 256, 128, 1, 1),
+                                            (512, 8192, 4096, 128, 128, 2, 1), (256, 8192, 4096, 128, 128, 1, 2),
+                                            (128, 8192, 4096, 128, 128, 1, 4), (777, 1504, 1448, 64, 64, 1, 1),
+                                            (128, 2048, 4096, 64, 64, 1, 4)):
+        p = paths([(M, N, K, 5, 1, 16, 0)])[0]
+        assert (p["bm"], p["bn"], p["groups"], p["splits"]) == (bm, bn, groups, splits), (M, N, K, p)

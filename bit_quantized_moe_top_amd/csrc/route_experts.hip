@@ -12,7 +12,8 @@
 //    if neighbours among them, and the last pick and every expert left, are at least tol apart or are
 //    the same number (equal logit and equal bias, hence a tie that the index decides).  Otherwise the
 //    experts within tol of the last pick or above it, the only ones the true choice can be among, are
-//    ranked by their c in 64 bits.  Likewise for groups.  (For random logits some 3 to 15 tokens in 10000.)
+//    ranked by their c in 64 bits.  Likewise for groups.  (Of random logits of unit variance
+//    some 3 to 15 tokens in 10000; how many depends on the values, see WideChoice.)
 //
 // tol: with u = 2^-24, exp by the hardware's 2^x is within (1.5 |x| + 2) u of its value (the product
 // with log2 e, its rounding, 1 ulp).  Sigmoid: s (1 - s) |l| < 0.23, so |ds| <= (0.9 + 1 + 2) u with the
@@ -163,7 +164,10 @@ struct WideChoice {
     return lane < min(n, p.k) ? cand[lane] : -1;
   }
   // The same of all experts whose fp32 sum is above `edge` in the groups of `stay`, however many they
-  // are: round by round, the best after the last taken.
+  // are: round by round, the best after the last taken.  Every token of a peaked softmax comes here where
+  // the bias is as small as the other scores (one score near 1, the others some 2e-9 and a bias of 1e-7:
+  // all sums lie within 2^-17 of each other): 4096 tokens of 1024 experts 127 us, 16384 of 256 145, 64 of
+  // 256 23; with a bias of 1e-3 10 to 16.
   __device__ __forceinline__ int rounds(uint64_t stay, float edge, float rden) const {
     const int S = p.E / p.n_group;
     uint64_t last = ~0ull;
